@@ -193,6 +193,98 @@ m2rnn_status m2rnn_backward_noalloc(const m2rnn_dims* d,
                                     float* dk, float* dv, float* dq, float* df,
                                     float* dW, float* dH0, m2rnn_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the same state, gates, head
+ * groups and layouts without the transition S·W and the tanh,
+ *   S_t = f_t S_{t-1} + k_t v_tᵀ,    y_t = S_tᵀ q_t,
+ * for the linear layers that a hybrid stack places between M²RNN layers.
+ *
+ * Tensors are dense and head-first as above: k, q, dk, dq [B][G][T][K];
+ * v, y, dy, dv [B][H][T][V]; S0, ST, dST, dS0 [B][H][K][V] fp32; f, df fp32
+ * [B][H][T], or [H] with f_per_head (one constant gate per head; df is then
+ * the sum over batch and time).  ckpt [B][H][ceil(T/128)][K][V] fp32 holds the
+ * states before tokens 0, 128, 256, …: the forward writes it, the backward
+ * starts from it (there is no S0 argument: ckpt[.][.][0] is S0).
+ * Element types: with mode M2RNN_MODE_BF16_TC k, v, q, dy and the results y,
+ * dk, dv, dq are bf16 (unlike the M²RNN recurrence, whose results are fp32:
+ * here no later step amplifies a result's rounding, so it is rounded once,
+ * from fp32 sums, to the type that the next matrix product reads); with
+ * M2RNN_MODE_FP32_DEBUG everything is fp32 and runs on the CUDA cores.  The
+ * other modes are refused.  States, gates and their gradients are fp32.
+ *
+ * Gates lie in [0, 1].  A gate of exactly 0 discards the state before it.  In
+ * the tensor-core kernels a gate below 2^-64 acts as 2^-64 (in the forward, the decay
+ * over a stretch that falls to 2^-64 or below is taken as 0).  A state that
+ * holds an infinity or NaN is not discarded by a gate of 0 (0·inf = NaN, as in
+ * the formula).
+ *
+ * Errors, ownership, ordering and alignment are as above; ws may be NULL when
+ * the workspace size is 0.  Tensors with no elements may be NULL.  The
+ * workspace needs no initialisation.  A wait inside a kernel that runs out is
+ * reported by m2rnn_linear_attention_status. */
+typedef struct {
+    int B, H, T, K, V;  /* K, V in {16, 32, 64, 128} */
+    int mode;           /* M2RNN_MODE_BF16_TC or M2RNN_MODE_FP32_DEBUG */
+    int qk_heads;       /* as in m2rnn_dims */
+    int f_is_logit;     /* as in m2rnn_dims */
+    int f_per_head;     /* 1: f and df are [H] */
+} m2rnn_la_dims;
+
+/* Bytes of device workspace a call needs; (size_t)-1 for dims that are refused. */
+size_t m2rnn_linear_attention_workspace(const m2rnn_la_dims* d, int backward);
+
+/* Forward.  S0 NULL = zeros; ST and ckpt may be NULL.  ST may be the buffer of
+ * S0 (a decode step is this call with T = 1 and ST == S0). */
+m2rnn_status m2rnn_linear_attention_forward(const m2rnn_la_dims* d, const void* k, const void* v, const void* q,
+                                            const float* f, const float* S0, void* y, float* ST, float* ckpt,
+                                            void* workspace, size_t ws_bytes, m2rnn_stream_t stream);
+
+/* Gradients of L with dL/dy = dy and dL/dS_T = dST (NULL = 0; dST and dS0 may
+ * be the same buffer).  df is dL/df_t, or the logit's gradient with
+ * f_is_logit.  Every output is written. */
+m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void* k, const void* v, const void* q,
+                                             const float* f, const float* ckpt, const void* dy, const float* dST,
+                                             void* dk, void* dv, void* dq, float* df, float* dS0, void* workspace,
+                                             size_t ws_bytes, m2rnn_stream_t stream);
+
+/* Synchronises `stream`, reads and clears the current device's status of the
+ * linear-attention kernels (every stream of the device shares it): M2RNN_OK,
+ * M2RNN_ERR_DEVICE_TIMEOUT or M2RNN_ERR_CUDA. */
+m2rnn_status m2rnn_linear_attention_status(m2rnn_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm of rows of N values, and its RMS form: the norm between a
+ * readout and the output projection.
+ *   m = mean(x), r = 1/sqrt(mean((x - m)²) + eps), y = (x - m) r w + b
+ * (rms: m = 0).  x is [B][H][T][N], head-first like the readouts above; y is
+ * token-first, [B][T][H][N]; weight w and bias b are [H][N] fp32.  Plain rows
+ * with one weight are B = H = 1.  mean and rstd are fp32 [B][H][T].  Sums and
+ * statistics are fp32 whatever the types.  Any N >= 1; pointers are 16-byte
+ * aligned. */
+typedef struct {
+    int B, H, T, N;
+    int x_fp32;         /* element type of x: 0 = bf16, 1 = fp32 */
+    int y_fp32;         /* of y and dy */
+    int dx_fp32;        /* of dx; 1 needs x_fp32 (backward only) */
+    int rms;            /* 1: no mean is subtracted; `mean` is ignored */
+    float eps;          /* >= 0 */
+} m2rnn_norm_dims;
+
+/* weight (NULL = 1), bias (NULL = 0), mean and rstd may be NULL. */
+m2rnn_status m2rnn_layer_norm_forward(const m2rnn_norm_dims* d, const void* x, const float* weight, const float* bias,
+                                      void* y, float* mean, float* rstd, m2rnn_stream_t stream);
+
+/* Bytes of workspace of the backward; (size_t)-1 for dims that are refused. */
+size_t m2rnn_layer_norm_workspace(const m2rnn_norm_dims* d);
+
+/* dx from dy and the forward's x, mean (ignored with rms) and rstd.  dweight
+ * and dbias, [H][N] fp32, are the sums over batch and time in a fixed order;
+ * both NULL leaves them out (and needs no workspace).  dx may be the buffer of
+ * x when their types are the same. */
+m2rnn_status m2rnn_layer_norm_backward(const m2rnn_norm_dims* d, const void* dy, const void* x, const float* weight,
+                                       const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
+                                       void* workspace, size_t ws_bytes, m2rnn_stream_t stream);
+
 /* Synchronises `stream`, reads and clears the status word in `workspace`.
  * Returns M2RNN_OK or M2RNN_ERR_DEVICE_TIMEOUT (or M2RNN_ERR_CUDA). */
 m2rnn_status m2rnn_get_device_status(void* workspace, m2rnn_stream_t stream);

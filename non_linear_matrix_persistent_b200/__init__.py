@@ -7,7 +7,9 @@ import importlib
 
 from .inputs import WORKLOADS, Workload, make_inputs  # noqa: F401
 
-_API_NAMES = ("forward", "backward", "step", "device_status", "set_wait_limit_ns", "decay_logit_bias")
+_API_NAMES = ("forward", "backward", "step", "device_status", "set_wait_limit_ns", "decay_logit_bias",
+              "linear_attention", "linear_attention_backward", "linear_attention_step", "layer_norm",
+              "layer_norm_backward")
 
 
 def __getattr__(name):

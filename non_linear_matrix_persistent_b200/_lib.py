@@ -18,13 +18,26 @@ MODE_BF16_TC, MODE_FP32_DEBUG, MODE_BF16_TC_FAST_TANH, MODE_BF16_MMA_SYNC = 0, 1
 # Every entry point declared in include/m2rnn.h.
 EXPORTS = ("m2rnn_workspace_size", "m2rnn_forward", "m2rnn_backward", "m2rnn_backward_noalloc",
            "m2rnn_get_device_status", "m2rnn_status_string", "m2rnn_set_wait_limit_ns",
-           "m2rnn_debug_set_fault")
+           "m2rnn_debug_set_fault", "m2rnn_linear_attention_workspace", "m2rnn_linear_attention_forward",
+           "m2rnn_linear_attention_backward", "m2rnn_linear_attention_status", "m2rnn_layer_norm_forward",
+           "m2rnn_layer_norm_workspace", "m2rnn_layer_norm_backward")
+
+REFUSED = ctypes.c_size_t(-1).value     # workspace size of refused dims
 
 
 class Dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int), ("K", ctypes.c_int),
                 ("V", ctypes.c_int), ("mode", ctypes.c_int), ("ckpt_stride", ctypes.c_int),
                 ("qk_heads", ctypes.c_int), ("f_is_logit", ctypes.c_int)]
+
+
+class LaDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "T", "K", "V", "mode", "qk_heads", "f_is_logit", "f_per_head")]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "T", "N", "x_fp32", "y_fp32", "dx_fp32", "rms")] + \
+        [("eps", ctypes.c_float)]
 
 
 class M2RNNError(RuntimeError):
@@ -59,6 +72,21 @@ def lib():
         L.m2rnn_set_wait_limit_ns.restype = None
         L.m2rnn_debug_set_fault.argtypes = [i]
         L.m2rnn_debug_set_fault.restype = i
+        PL, PN = ctypes.POINTER(LaDims), ctypes.POINTER(NormDims)
+        L.m2rnn_linear_attention_workspace.argtypes = [PL, i]
+        L.m2rnn_linear_attention_workspace.restype = sz
+        L.m2rnn_linear_attention_forward.argtypes = [PL] + [vp] * 9 + [sz, vp]
+        L.m2rnn_linear_attention_forward.restype = i
+        L.m2rnn_linear_attention_backward.argtypes = [PL] + [vp] * 13 + [sz, vp]
+        L.m2rnn_linear_attention_backward.restype = i
+        L.m2rnn_linear_attention_status.argtypes = [vp]
+        L.m2rnn_linear_attention_status.restype = i
+        L.m2rnn_layer_norm_forward.argtypes = [PN] + [vp] * 7
+        L.m2rnn_layer_norm_forward.restype = i
+        L.m2rnn_layer_norm_workspace.argtypes = [PN]
+        L.m2rnn_layer_norm_workspace.restype = sz
+        L.m2rnn_layer_norm_backward.argtypes = [PN] + [vp] * 9 + [sz, vp]
+        L.m2rnn_layer_norm_backward.restype = i
         _lib = L
     return _lib
 

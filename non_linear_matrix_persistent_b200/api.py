@@ -7,6 +7,11 @@ device memory and the current stream.  Names follow include/m2rnn.h.
   grads       = backward(k, v, q, f, W, ckpt, dy, dHT=None, ckpt_stride=8)
   y_t         = step(k_t, v_t, q_t, f_t, W, H)        # one decode step, H updated in place
   b           = decay_logit_bias(H)                   # per-head gate-logit bias at initialisation
+  y, ST, ckpt = linear_attention(k, v, q, f, S0=None, want_ckpt=False)   # S_t = f_t S_{t-1} + k_t v_tᵀ
+  grads       = linear_attention_backward(k, v, q, f, ckpt, dy, dST=None)
+  y_t         = linear_attention_step(k_t, v_t, q_t, f_t, S)             # one decode step, S updated in place
+  n, mu, r    = layer_norm(y, weight, bias)           # readout [B, H, T, V] -> normalised rows [B, T, H, V]
+  grads       = layer_norm_backward(dn, y, weight, mu, r)
 
 k and q may carry fewer heads than v (G dividing H: grouped k / q, head h
 uses group h // (H // G)); dk and dq then have G heads too.  With
@@ -32,6 +37,9 @@ from . import _lib
 from ._lib import Dims, M2RNNError
 
 _workspaces: Dict[Tuple[int, int], torch.Tensor] = {}
+
+# Tokens between the states that linear_attention keeps for its backward.
+LA_CHUNK = 128
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -195,13 +203,15 @@ def backward(k, v, q, f, W, ckpt, dy, dHT=None, *, ckpt_stride: int = 8, out: Op
 
 def device_status(device=None) -> int:
     """Synchronises the current stream and returns (and clears) the device
-    status of the workspace cached for that stream."""
+    status of the workspace cached for that stream, and that of the device's
+    linear-attention kernels (which all streams share)."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     key = _ws_key(dev)
     ws = _workspaces.get(key)
-    if ws is None:
-        return _lib.OK
-    return _lib.lib().m2rnn_get_device_status(_ptr(ws), _stream(dev))
+    st = _lib.OK if ws is None else _lib.lib().m2rnn_get_device_status(_ptr(ws), _stream(dev))
+    with torch.cuda.device(dev):
+        other = _lib.lib().m2rnn_linear_attention_status(_stream(dev))
+    return st if st != _lib.OK else other
 
 
 def set_wait_limit_ns(ns: int) -> None:
@@ -226,3 +236,206 @@ def decay_logit_bias(H: int, tau_min: float = 2.0, tau_max: float = 256.0) -> to
     frac = h / (H - 1) if H > 1 else torch.zeros(1, dtype=torch.float64)
     tau = tau_min * (tau_max / tau_min) ** frac
     return torch.log(tau - 1.0).float()
+
+
+# ------------------------------------------------------------------ linear attention
+
+def _la_dims(k, v, q, f, f_is_logit) -> "_lib.LaDims":
+    """Checks k, v, q and f of a call and gives its dims."""
+    if k.dim() != 4 or v.dim() != 4:
+        raise ValueError("k and v must have 4 dimensions (batch, heads, tokens, width), got %d and %d" % (k.dim(), v.dim()))
+    B, G, T, K = k.shape
+    H, V = v.shape[1], v.shape[3]
+    if G != H and (G < 1 or H % G != 0):
+        raise ValueError("k has %d heads: it must have H = %d heads or a divisor of H" % (G, H))
+    dev, lp = k.device, k.dtype
+    mode = _mode(k)
+    _check("k", k, (B, G, T, K), lp, dev)
+    _check("v", v, (B, H, T, V), lp, dev)
+    _check("q", q, (B, G, T, K), lp, dev)
+    per_head = f.dim() == 1
+    _check("f", f, (H,) if per_head else (B, H, T), torch.float32, dev)
+    return _lib.LaDims(B, H, T, K, V, mode, G if G != H else 0, int(bool(f_is_logit)), int(per_head))
+
+
+def _scratch(need: int, device, what: str) -> Optional[torch.Tensor]:
+    """Workspace of one call, from torch's allocator: calls on different
+    streams, and captured graphs, never share one."""
+    if need == _lib.REFUSED:
+        raise M2RNNError(_lib.ERR_UNSUPPORTED_SHAPE, what)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def _output(out: dict, name: str, shape, dtype, device) -> torch.Tensor:
+    t = out.get(name)
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(name, t, shape, dtype, device)
+    return t
+
+
+def _call(what: str, device, fn, *args) -> None:
+    """Calls the library on the device of the tensors, on its current stream."""
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(device))
+    else:
+        st = fn(*args, _stream(device))
+    if st != _lib.OK:
+        raise M2RNNError(st, what)
+
+
+def linear_attention(k, v, q, f, S0=None, *, want_ST: bool = True, want_ckpt: bool = False,
+                     f_is_logit: bool = False, out: Optional[dict] = None):
+    """Linear attention with a decay for each head, over a whole sequence:
+    S_t = f_t S_{t-1} + k_t v_tᵀ, y_t = S_tᵀ q_t.  Returns (y, ST or None, ckpt or None).
+
+    k, q [B, G, T, K] and v [B, H, T, V] (bf16, or fp32 for the debug mode),
+    f [B, H, T] fp32 in [0, 1] (or logits, with f_is_logit) or [H], one
+    constant for each head; S0 [B, H, K, V] fp32 (None: zeros).  y has the
+    inputs' type, ST [B, H, K, V] is fp32.  ckpt [B, H, ceil(T/128), K, V]
+    holds the states that linear_attention_backward starts from.  `out` may
+    hold buffers for y, ST and ckpt; ST may be S0's."""
+    d = _la_dims(k, v, q, f, f_is_logit)
+    dev, lp = k.device, k.dtype
+    B, H, T, K, V = d.B, d.H, d.T, d.K, d.V
+    _check("S0", S0, (B, H, K, V), torch.float32, dev)
+    out = out or {}
+    y = _output(out, "y", (B, H, T, V), lp, dev)
+    ST = _output(out, "ST", (B, H, K, V), torch.float32, dev) if want_ST else None
+    ckpt = _output(out, "ckpt", (B, H, num_checkpoints(T, LA_CHUNK), K, V), torch.float32, dev) if want_ckpt else None
+    L = _lib.lib()
+    ws = _scratch(L.m2rnn_linear_attention_workspace(d, 0), dev, "m2rnn_linear_attention_forward")
+    _call("m2rnn_linear_attention_forward", dev, L.m2rnn_linear_attention_forward, d, _ptr(k), _ptr(v), _ptr(q),
+          _ptr(f), _ptr(S0), _ptr(y), _ptr(ST), _ptr(ckpt), _ptr(ws), ws.numel() if ws is not None else 0)
+    return y, ST, ckpt
+
+
+def linear_attention_step(k, v, q, f, S, *, ST: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                          f_is_logit: bool = False):
+    """One decode step: advances the fp32 state S [B, H, K, V] by one token with
+    k, q [B, G, K], v [B, H, V] and f [B, H] (or [H]), in place, or into ST
+    where that is given.  Returns y [B, H, V]."""
+    if S is None:
+        raise ValueError("linear_attention_step needs the state buffer S")
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k and v of a step must have 3 dimensions (batch, heads, width), got %d and %d" % (k.dim(), v.dim()))
+    yb = None if y is None else y.unsqueeze(2)
+    o = linear_attention(k.unsqueeze(2), v.unsqueeze(2), q.unsqueeze(2), f if f.dim() == 1 else f.unsqueeze(2), S,
+                         f_is_logit=f_is_logit, out={"y": yb, "ST": S if ST is None else ST})[0]
+    return o.squeeze(2) if y is None else y
+
+
+def linear_attention_backward(k, v, q, f, ckpt, dy, dST=None, *, f_is_logit: bool = False,
+                              out: Optional[dict] = None) -> dict:
+    """Gradients of linear_attention from the checkpoints of its forward.
+    Returns dict dk, dv, dq (the inputs' type), df (fp32, f's shape), dS0 (fp32).
+    dk and dq of shared k and q are the sums over each group's heads."""
+    d = _la_dims(k, v, q, f, f_is_logit)
+    dev, lp = k.device, k.dtype
+    B, H, T, K, V = d.B, d.H, d.T, d.K, d.V
+    G = d.qk_heads or H
+    _check("dy", dy, (B, H, T, V), lp, dev)
+    _check("dST", dST, (B, H, K, V), torch.float32, dev)
+    if ckpt is None:
+        raise ValueError("linear_attention_backward needs the checkpoints of linear_attention(..., want_ckpt=True)")
+    _check("ckpt", ckpt, (B, H, num_checkpoints(T, LA_CHUNK), K, V), torch.float32, dev)
+    out = dict(out or {})
+    for n, shape, t in (("dk", (B, G, T, K), lp), ("dv", (B, H, T, V), lp), ("dq", (B, G, T, K), lp),
+                        ("df", tuple(f.shape), torch.float32), ("dS0", (B, H, K, V), torch.float32)):
+        out[n] = _output(out, n, shape, t, dev)
+    L = _lib.lib()
+    ws = _scratch(L.m2rnn_linear_attention_workspace(d, 1), dev, "m2rnn_linear_attention_backward")
+    _call("m2rnn_linear_attention_backward", dev, L.m2rnn_linear_attention_backward, d, _ptr(k), _ptr(v), _ptr(q),
+          _ptr(f), _ptr(ckpt), _ptr(dy), _ptr(dST), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dq"]),
+          _ptr(out["df"]), _ptr(out["dS0"]), _ptr(ws), ws.numel() if ws is not None else 0)
+    return out
+
+
+# ------------------------------------------------------------------ layer norm
+
+_NORM_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _norm_shape(x, weight, bias):
+    """(B, H, T, N) of a call, and whether x is a head-first readout."""
+    params = [t for t in (weight, bias) if t is not None]
+    heads = bool(params) and params[0].dim() == 2
+    if x.dtype not in _NORM_TYPES:
+        raise TypeError("x must be bfloat16 or float32, got %s" % x.dtype)
+    if heads:
+        if x.dim() != 4:
+            raise ValueError("a norm with one weight per head takes x [B, H, T, N], got %d dimensions" % x.dim())
+        B, H, T, N = x.shape
+    else:
+        if x.dim() < 1:
+            raise ValueError("x must have at least one dimension")
+        N = x.shape[-1]
+        B, H, T = 1, 1, x.numel() // N if N else 0
+    if N < 1:
+        raise ValueError("the last dimension of x is empty")
+    _check("x", x, x.shape, x.dtype, x.device)
+    for n, t in (("weight", weight), ("bias", bias)):
+        _check(n, t, (H, N) if heads else (N,), torch.float32, x.device)
+    return B, H, T, N, heads
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = False,
+               out_dtype: Optional[torch.dtype] = None, out: Optional[dict] = None):
+    """Layer norm over the last dimension (with rms=True, its RMS form).
+    Returns (y, mean, rstd); mean is None with rms=True.
+
+    weight and bias [H, N] (fp32): x is a readout [B, H, T, N] as forward and
+    linear_attention give it, normalised per head, and y is token-first,
+    [B, T, H, N]: the rows of the output projection.  weight and bias [N] or
+    None: plain rows, y has x's shape.  x is bf16 or fp32; y has type out_dtype
+    (x's by default).  mean and rstd (fp32, x's leading shape) feed
+    layer_norm_backward.  `out` may hold buffers for y, mean and rstd."""
+    B, H, T, N, heads = _norm_shape(x, weight, bias)
+    dev = x.device
+    yt = x.dtype if out_dtype is None else out_dtype
+    if yt not in _NORM_TYPES:
+        raise TypeError("out_dtype must be bfloat16 or float32, got %s" % yt)
+    out = out or {}
+    lead = tuple(x.shape[:-1])
+    y = _output(out, "y", (B, T, H, N) if heads else tuple(x.shape), yt, dev)
+    rstd = _output(out, "rstd", lead, torch.float32, dev)
+    mean = None if rms else _output(out, "mean", lead, torch.float32, dev)
+    d = _lib.NormDims(B, H, T, N, _NORM_TYPES[x.dtype], _NORM_TYPES[yt], 0, int(bool(rms)), eps)
+    _call("m2rnn_layer_norm_forward", dev, _lib.lib().m2rnn_layer_norm_forward, d, _ptr(x), _ptr(weight), _ptr(bias),
+          _ptr(y), _ptr(mean), _ptr(rstd))
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, *, rms: bool = False, heads: Optional[bool] = None,
+                        dx_dtype: Optional[torch.dtype] = None, out: Optional[dict] = None) -> dict:
+    """Gradients of layer_norm: dict dx (x's shape; type dx_dtype, x's by
+    default), dweight and dbias (fp32, in weight's shape).  dy has y's shape
+    and type.  With weight=None, `heads` says which form x was in (a readout
+    with dy [B, T, H, N], or plain rows)."""
+    if weight is None and heads and x.dim() != 4:
+        raise ValueError("heads=True takes x [B, H, T, N], got %d dimensions" % x.dim())
+    B, H, T, N, per_head = _norm_shape(x, weight, None)
+    if weight is None and heads:
+        (B, H, T, N), per_head = x.shape, True
+    dev = x.device
+    dt = x.dtype if dx_dtype is None else dx_dtype
+    if dy.dtype not in _NORM_TYPES or dt not in _NORM_TYPES or (dt == torch.float32 and x.dtype != torch.float32):
+        raise TypeError("dy must be bfloat16 or float32 and dx bfloat16 or x's type, got %s and %s" % (dy.dtype, dt))
+    _check("dy", dy, (B, T, H, N) if per_head else tuple(x.shape), dy.dtype, dev)
+    lead = tuple(x.shape[:-1])
+    if rstd is None or (mean is None and not rms):
+        raise ValueError("layer_norm_backward needs the forward's rstd, and its mean unless rms=True")
+    _check("rstd", rstd, lead, torch.float32, dev)
+    _check("mean", None if rms else mean, lead, torch.float32, dev)
+    out = dict(out or {})
+    shape = (H, N) if per_head else (N,)
+    for n, sh, t in (("dx", tuple(x.shape), dt), ("dweight", shape, torch.float32), ("dbias", shape, torch.float32)):
+        out[n] = _output(out, n, sh, t, dev)
+    d = _lib.NormDims(B, H, T, N, _NORM_TYPES[x.dtype], _NORM_TYPES[dy.dtype], _NORM_TYPES[dt], int(bool(rms)), 0.0)
+    L = _lib.lib()
+    ws = _scratch(L.m2rnn_layer_norm_workspace(d), dev, "m2rnn_layer_norm_backward")
+    _call("m2rnn_layer_norm_backward", dev, L.m2rnn_layer_norm_backward, d, _ptr(dy), _ptr(x), _ptr(weight),
+          None if rms else _ptr(mean), _ptr(rstd), _ptr(out["dx"]), _ptr(out["dweight"]), _ptr(out["dbias"]),
+          _ptr(ws), ws.numel() if ws is not None else 0)
+    return out

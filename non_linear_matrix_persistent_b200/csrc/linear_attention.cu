@@ -1,0 +1,195 @@
+// C ABI of linear attention and of the layer norm: argument validation,
+// workspace carving and dispatch (declared in include/m2rnn.h).
+#include "linear_attention.h"
+
+#include <cstring>
+#include <initializer_list>
+
+#include "../../include/m2rnn.h"
+#include "kernels.h"
+#include "layer_norm.h"
+
+namespace {
+
+constexpr size_t kRefused = ~(size_t)0;
+
+bool state_dim_ok(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
+
+bool any_misaligned(std::initializer_list<const void*> ptrs) {
+    for (const void* p : ptrs)
+        if (reinterpret_cast<uintptr_t>(p) & 15u) return true;
+    return false;
+}
+
+m2rnn_status check(const m2rnn_la_dims* d) {
+    if (d == nullptr || d->B < 0 || d->H < 0 || d->T < 0) return M2RNN_ERR_INVALID_ARG;
+    if (d->mode != M2RNN_MODE_BF16_TC && d->mode != M2RNN_MODE_FP32_DEBUG) return M2RNN_ERR_INVALID_ARG;
+    if (d->qk_heads < 0 || (d->qk_heads > 0 && (d->qk_heads > d->H || d->H % d->qk_heads != 0)))
+        return M2RNN_ERR_INVALID_ARG;
+    if ((d->f_is_logit & ~1) || (d->f_per_head & ~1)) return M2RNN_ERR_INVALID_ARG;
+    if (!state_dim_ok(d->K) || !state_dim_ok(d->V)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+    // pairs, and tokens over all pairs, index 32-bit grids and coordinates
+    if ((long long)d->B * d->H > (1 << 24) || d->T > (1 << 30)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+    return M2RNN_OK;
+}
+
+int groups(const m2rnn_la_dims* d) { return d->qk_heads > 0 ? d->qk_heads : d->H; }
+size_t pairs(const m2rnn_la_dims* d) { return (size_t)d->B * d->H; }
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Per-head fp32 dk and dq before the sum over each group's heads.
+size_t group_bytes(const m2rnn_la_dims* d) {
+    return groups(d) == d->H ? 0 : round256(2 * sizeof(float) * pairs(d) * d->T * d->K);
+}
+// Per-token df before the sum over batch and time.
+size_t df_bytes(const m2rnn_la_dims* d) { return d->f_per_head ? round256(sizeof(float) * pairs(d) * d->T) : 0; }
+
+m2rnn::LaParams params(const m2rnn_la_dims* d) {
+    m2rnn::LaParams p;
+    std::memset(&p, 0, sizeof p);
+    p.B = d->B; p.H = d->H; p.T = d->T; p.K = d->K; p.V = d->V;
+    p.G = groups(d);
+    p.bf16 = d->mode == M2RNN_MODE_BF16_TC;
+    p.f_is_logit = d->f_is_logit;
+    p.f_per_head = d->f_per_head;
+    return p;
+}
+
+m2rnn_status status_of(cudaError_t e) { return e == cudaSuccess ? M2RNN_OK : M2RNN_ERR_CUDA; }
+
+// No tokens: the state (or its gradient) passes through.
+m2rnn_status pass_through(float* out, const float* in, size_t n, cudaStream_t s) {
+    if (!out || out == in || n == 0) return M2RNN_OK;
+    return status_of(in ? cudaMemcpyAsync(out, in, n * sizeof(float), cudaMemcpyDeviceToDevice, s)
+                        : cudaMemsetAsync(out, 0, n * sizeof(float), s));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t m2rnn_linear_attention_workspace(const m2rnn_la_dims* d, int backward) {
+    if (check(d) != M2RNN_OK) return kRefused;
+    if (!backward || pairs(d) * d->T == 0) return 0;
+    return group_bytes(d) + df_bytes(d);
+}
+
+m2rnn_status m2rnn_linear_attention_forward(const m2rnn_la_dims* d, const void* k, const void* v, const void* q,
+                                            const float* f, const float* S0, void* y, float* ST, float* ckpt,
+                                            void* workspace, size_t ws_bytes, m2rnn_stream_t stream) {
+    const m2rnn_status st = check(d);
+    if (st != M2RNN_OK) return st;
+    if (pairs(d) * d->T > 0 && (!k || !v || !q || !f || !y)) return M2RNN_ERR_INVALID_ARG;
+    if (any_misaligned({k, v, q, f, S0, y, ST, ckpt, workspace})) return M2RNN_ERR_MISALIGNED;
+    const size_t need = m2rnn_linear_attention_workspace(d, 0);
+    if (need > 0 && (!workspace || ws_bytes < need)) return M2RNN_ERR_WORKSPACE;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (pairs(d) * d->T == 0) return pass_through(ST, S0, pairs(d) * d->K * d->V, s);
+    m2rnn::LaParams p = params(d);
+    p.k = k; p.v = v; p.q = q; p.f = f; p.S0 = S0; p.y = y; p.ST = ST; p.ckpt = ckpt;
+    return status_of(m2rnn::launch_la_rec(p, s));
+}
+
+m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void* k, const void* v, const void* q,
+                                             const float* f, const float* ckpt, const void* dy, const float* dST,
+                                             void* dk, void* dv, void* dq, float* df, float* dS0, void* workspace,
+                                             size_t ws_bytes, m2rnn_stream_t stream) {
+    const m2rnn_status st = check(d);
+    if (st != M2RNN_OK) return st;
+    if (pairs(d) * d->T > 0 && (!k || !v || !q || !f || !ckpt || !dy || !dk || !dv || !dq || !df))
+        return M2RNN_ERR_INVALID_ARG;
+    if ((pairs(d) > 0 && !dS0) || (d->f_per_head && d->H > 0 && !df)) return M2RNN_ERR_INVALID_ARG;
+    if (any_misaligned({k, v, q, f, ckpt, dy, dST, dk, dv, dq, df, dS0, workspace})) return M2RNN_ERR_MISALIGNED;
+    const size_t need = m2rnn_linear_attention_workspace(d, 1);
+    if (need > 0 && (!workspace || ws_bytes < need)) return M2RNN_ERR_WORKSPACE;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (pairs(d) * d->T == 0) {
+        if (d->f_per_head && d->H > 0) {
+            const cudaError_t e = cudaMemsetAsync(df, 0, sizeof(float) * d->H, s);
+            if (e != cudaSuccess) return M2RNN_ERR_CUDA;
+        }
+        return pass_through(dS0, dST, pairs(d) * d->K * d->V, s);
+    }
+    m2rnn::LaParams p = params(d);
+    p.k = k; p.v = v; p.q = q; p.f = f; p.ckpt = const_cast<float*>(ckpt); p.dy = dy; p.dST = dST;
+    p.dk = dk; p.dq = dq; p.dv = dv; p.df = df; p.dS0 = dS0;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (group_bytes(d)) {
+        p.dkq_fp32 = 1;
+        p.dk = ws;
+        p.dq = reinterpret_cast<float*>(ws) + pairs(d) * d->T * d->K;
+    }
+    if (d->f_per_head) p.df = reinterpret_cast<float*>(ws + group_bytes(d));
+    cudaError_t e = m2rnn::launch_la_bwd_simt(p, s);
+    if (e == cudaSuccess && group_bytes(d))
+        e = m2rnn::launch_la_group_sum(p, static_cast<const float*>(p.dk), static_cast<const float*>(p.dq), dk, dq, s);
+    if (e == cudaSuccess && d->f_per_head) e = m2rnn::launch_la_df_sum(p, p.df, df, s);
+    return status_of(e);
+}
+
+m2rnn_status m2rnn_linear_attention_status(m2rnn_stream_t stream) {
+    return status_of(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ layer norm
+
+static m2rnn_status check_norm(const m2rnn_norm_dims* d) {
+    if (d == nullptr || d->B < 0 || d->H < 0 || d->T < 0 || d->N < 1) return M2RNN_ERR_INVALID_ARG;
+    if ((d->x_fp32 & ~1) || (d->y_fp32 & ~1) || (d->dx_fp32 & ~1) || (d->rms & ~1)) return M2RNN_ERR_INVALID_ARG;
+    if (d->dx_fp32 && !d->x_fp32) return M2RNN_ERR_INVALID_ARG;
+    if (!(d->eps >= 0.f)) return M2RNN_ERR_INVALID_ARG;
+    if ((long long)d->B * d->H > (1 << 24) || d->N > (1 << 28)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+    return M2RNN_OK;
+}
+
+static m2rnn::NormParams norm_params(const m2rnn_norm_dims* d) {
+    m2rnn::NormParams p;
+    std::memset(&p, 0, sizeof p);
+    p.B = d->B; p.H = d->H; p.T = d->T; p.N = d->N;
+    p.x_fp32 = d->x_fp32; p.y_fp32 = d->y_fp32; p.dx_fp32 = d->dx_fp32; p.rms = d->rms; p.eps = d->eps;
+    return p;
+}
+
+m2rnn_status m2rnn_layer_norm_forward(const m2rnn_norm_dims* d, const void* x, const float* weight, const float* bias,
+                                      void* y, float* mean, float* rstd, m2rnn_stream_t stream) {
+    const m2rnn_status st = check_norm(d);
+    if (st != M2RNN_OK) return st;
+    if ((size_t)d->B * d->H * d->T == 0) return M2RNN_OK;
+    if (!x || !y) return M2RNN_ERR_INVALID_ARG;
+    if (any_misaligned({x, weight, bias, y, mean, rstd})) return M2RNN_ERR_MISALIGNED;
+    m2rnn::NormParams p = norm_params(d);
+    p.x = x; p.weight = weight; p.bias = bias; p.y = y; p.mean = mean; p.rstd = rstd;
+    return status_of(m2rnn::launch_norm_fwd(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t m2rnn_layer_norm_workspace(const m2rnn_norm_dims* d) {
+    if (check_norm(d) != M2RNN_OK) return kRefused;
+    if ((size_t)d->B * d->H * d->T == 0) return 0;
+    return sizeof(float) * 2 * d->N * ((size_t)d->B * d->H * m2rnn::norm_bwd_chunks(d->B, d->H, d->T, d->N));
+}
+
+m2rnn_status m2rnn_layer_norm_backward(const m2rnn_norm_dims* d, const void* dy, const void* x, const float* weight,
+                                       const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
+                                       void* workspace, size_t ws_bytes, m2rnn_stream_t stream) {
+    const m2rnn_status st = check_norm(d);
+    if (st != M2RNN_OK) return st;
+    if (any_misaligned({dy, x, weight, mean, rstd, dx, dweight, dbias, workspace})) return M2RNN_ERR_MISALIGNED;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if ((size_t)d->B * d->H * d->T == 0) {
+        for (float* g : {dweight, dbias})
+            if (g && d->H > 0 && cudaMemsetAsync(g, 0, sizeof(float) * d->H * d->N, s) != cudaSuccess)
+                return M2RNN_ERR_CUDA;
+        return M2RNN_OK;
+    }
+    if (!dy || !x || !rstd || !dx || (!d->rms && !mean)) return M2RNN_ERR_INVALID_ARG;
+    const bool sums = dweight || dbias;
+    if (sums && (!workspace || ws_bytes < m2rnn_layer_norm_workspace(d))) return M2RNN_ERR_WORKSPACE;
+    m2rnn::NormParams p = norm_params(d);
+    p.dy = dy; p.x = x; p.weight = weight; p.mean = const_cast<float*>(mean); p.rstd = const_cast<float*>(rstd);
+    p.dx = dx; p.dweight = dweight; p.dbias = dbias;
+    p.part = sums ? static_cast<float*>(workspace) : nullptr;
+    p.chunks = m2rnn::norm_bwd_chunks(d->B, d->H, d->T, d->N);
+    return status_of(m2rnn::launch_norm_bwd(p, s));
+}
+
+}  // extern "C"
