@@ -51,6 +51,10 @@ constexpr int kNumSMs = 148;
 // and checkpoint stride C.
 int bwd_tc_slices(int K, int V, int C);
 
+// Limit of device-side waits and injected fault of later launches (m2rnn_abi.cu).
+uint64_t wait_limit_ns();
+int injected_fault();
+
 // Workspace bytes beyond the 256-byte status header.
 size_t bwd_fp32_workspace(int B, int H, int K, int V, int C);
 size_t bwd_tc_workspace(int B, int H, int T, int K, int V, int C);

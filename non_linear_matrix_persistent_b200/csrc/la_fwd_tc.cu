@@ -1,0 +1,510 @@
+// Linear attention in chunks of 128 tokens on the tensor cores (bf16).
+//
+// With L_t the cumulative log-decay inside a chunk, D_ts = 2^(L_t - L_s),
+// a_t = 2^(L_t), b_s = 2^(L_end - L_s) and S the state at its start,
+//   y_t  = a_t (Q S)_t + ((Q Kᵀ ∘ D) V)_t          (s <= t)
+//   S'   = a_end S + Σ_s (b_s k_s) v_sᵀ
+// Four matrix products, every accumulator in tensor memory; the state's fp32
+// master stays in registers over the whole walk.
+//
+// A CTA walks the chunks of one (b, h), or of one of its time segments.  Eight
+// warps compute: thread = token row (or state row) = tensor-memory lane, the
+// two warpgroups sharing the columns.  A ninth warp fetches tiles two chunks
+// ahead, issues the products and computes the decays of the next chunk.  A
+// chunk is a chain of waits (product -> elementwise -> product), so two CTAs
+// share an SM where they fit.
+//
+// Rounding: the masked scores and the copy of S that multiplies Q are bf16
+// operands (each term of y passes through exactly one of them, and y is
+// rounded to bf16 itself); b_s k_s enters as three bf16 terms, so the state
+// keeps fp32 accuracy over any number of chunks.
+//
+// Decays without an exponential per score: for a row t and a block of 32
+// columns left of its own, D_ts = 2^(L_t - L_e)·2^(L_e - L_s) with e the
+// block's last token; both factors are at most 1 and the second is shared by
+// all rows.  Only the diagonal blocks take one exponential per score.
+#include <cstdlib>
+#include <mutex>
+
+#include "kernels.h"
+#include "la_tc.cuh"
+
+namespace m2rnn {
+
+bool la_tensor_map(CUtensorMap* map, const void* x, int width, int T, size_t rows) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static Encode encode = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) ==
+                cudaSuccess &&
+            found == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<Encode>(fn);
+    });
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)T, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)width * 2 * T};
+    const cuuint32_t box[3] = {64, 128, 1}, step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+// FWD: the forward.  SUM: only the segment's own contribution to its final
+// state (from a zero start).  RSUM: the same backwards in time, with decays
+// from the segment's start: Σ_t a_t k_t v_tᵀ.
+enum Kind { FWD, SUM, RSUM };
+
+template <int KP, int VP>
+struct Cfg {
+    static constexpr int kThreads = 288;
+    static constexpr int kQ = KP / 64 * kTileBytes, kV = VP / 64 * kTileBytes, kStage = 2 * kQ + kV;
+    static constexpr int kOffS = 2 * kStage;                    // bf16 state operand [KP][VP]
+    static constexpr int kOffTab = kOffS + KP * VP * 2;
+    static constexpr int kOffBar = kOffTab + (int)sizeof(LaTables);
+    static constexpr int kBars = 12;
+    static constexpr int kSmem = kOffBar + kBars * 8 + 16;
+    static constexpr int kCtas = kSmem <= 113 * 1024 ? 2 : 1;
+    // tensor memory: scores, over which P (bf16) and, for 64 columns, the
+    // second half's product go once the scores are read; Q·S; the state's sum
+    static constexpr int kTmem = VP == 64 ? 256 : 512;
+    static constexpr int kPV = VP == 64 ? 64 : 128, kQS = VP == 64 ? 128 : 256, kDS = VP == 64 ? 192 : 384;
+    static constexpr int NS = KP == 128 ? VP / 2 : VP / 4;      // state columns per thread
+};
+
+// Tensor-memory column of the 16 columns of P that hold score block j (of 32):
+// inside the score columns of the warpgroup that computes it (block j belongs
+// to warpgroup j % 2), so that no warp writes over scores that another reads.
+__device__ __forceinline__ constexpr int p_col(int j) { return (j & 1) * 32 + (j >> 1) * 16; }
+
+template <int KP, int VP, Kind KIND>
+__global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
+    m2rnn_la_fwd_tc_kernel(const LaParams p, const __grid_constant__ Maps maps, float* seg_decay) {
+    using C = Cfg<KP, VP>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int bh = blockIdx.x / p.segs, seg = blockIdx.x % p.segs;
+    const int nchunks = (p.T + kLaChunk - 1) / kLaChunk;
+    const int c0 = seg * p.seg_chunks, n = min(nchunks - c0, p.seg_chunks);
+    if ((KIND == SUM && seg == p.segs - 1) || (KIND == RSUM && seg == 0)) return;   // no segment starts from this sum
+    auto chunk_of = [&](int i) { return KIND == RSUM ? c0 + n - 1 - i : c0 + i; };
+
+    LaTables* tab = reinterpret_cast<LaTables*>(smem + C::kOffTab);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    const uint32_t b_full = bar(0), b_sc = bar(2), r_k = bar(3), b_ds1 = bar(4), r_p = bar(5), b_pv = bar(6),
+                   r_lo = bar(7), b_ds2 = bar(8), r_s = bar(9), b_tab = bar(10), b_drain = bar(11);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint64_t limit = p.wait_limit_ns;
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar(0), 1);
+        mbar_init(bar(1), 1);
+        for (uint32_t b : {b_sc, b_ds1, b_pv, b_ds2, b_tab, b_drain}) mbar_init(b, 1);
+        for (uint32_t b : {r_k, r_p, r_lo, r_s}) mbar_init(b, 8);   // one arrival a warp
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_u32(tmem_slot), C::kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t sbase = smem_u32(smem);
+
+    if (warp == 8) {
+        // ------------------------------------------------------ copies, products, decays
+        const int qk = la_qk_pair(p, bh);
+        int loaded = 0;
+        auto load = [&](int i) {   // lane 0: the tiles of the walk's i-th chunk
+            if (p.fault == 1 && i > 0) return;   // injected: the copies stop after the first chunk
+            loaded = i + 1;
+            const int s = i & 1, t = chunk_of(i) * kLaChunk;
+            const uint32_t base = sbase + s * C::kStage, full = b_full + s * 8;
+            mbar_arrive_expect_tx(full, KIND == FWD ? C::kStage : C::kQ + C::kV);
+            for (int x = 0; x < KP / 64; ++x) {
+                if (KIND == FWD) tma_tile(base + x * kTileBytes, &maps.q, x * 64, t, qk, full);
+                tma_tile(base + C::kQ + x * kTileBytes, &maps.k, x * 64, t, qk, full);
+            }
+            for (int x = 0; x < VP / 64; ++x) tma_tile(base + 2 * C::kQ + x * kTileBytes, &maps.v, x * 64, t, bh, full);
+        };
+        if (lane == 0) {
+            load(0);
+            if (n > 1) load(1);
+        }
+        const float floor_ = KIND == RSUM ? kLogFloorBwd : kLogFloorFwd;
+        float fx[4];
+        la_load_f(p, bh, chunk_of(0), fx);
+        la_tables(tab, p, fx, p.T - chunk_of(0) * kLaChunk, floor_);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_tab);
+        if (n > 1) la_load_f(p, bh, chunk_of(1), fx);
+
+        constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, 0, 0), id_qs = idesc_bf16_f32(128, VP, 0, 1),
+                           id_pv = idesc_bf16_f32(128, VP, 0, 1), id_ds = idesc_bf16_f32(128, VP, 1, 1);
+        // the state's product: A = the scaled k tile, its rows (tokens) along the contraction; 64 state rows
+        // are computed twice (lbo 0: lanes 64..127 repeat lanes 0..63)
+        auto state_product = [&](uint32_t a, uint32_t v, bool first) {
+            for (int ks = 0; ks < 8; ++ks)
+                tc_mma_f16_ss(tmem + C::kDS, sw128_desc(a + ks * 2048, KP == 128 ? kTileBytes : 0),
+                              sw128_desc(v + ks * 2048, kTileBytes), id_ds, !(first && ks == 0));
+        };
+        bool ok = true;
+        int i = 0;
+        for (; i < n; ++i) {
+            const int s = i & 1, ph = i & 1;
+            const uint32_t q = sbase + s * C::kStage, k = q + C::kQ, v = k + C::kQ;
+            ok = la_wait(b_full + s * 8, (i >> 1) & 1, abort_flag, limit);
+            if (!ok) break;
+            if (KIND == FWD) {
+                ok = la_wait(r_s, ph, abort_flag, limit);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    for (int ks = 0; ks < KP / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * kTileBytes + (ks & 3) * 32;
+                        tc_mma_f16_ss(tmem, sw128_desc(q + off, 16), sw128_desc(k + off, 16), id_sc, ks > 0);
+                    }
+                    for (int ks = 0; ks < KP / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * kTileBytes + (ks & 3) * 32;
+                        tc_mma_f16_ss(tmem + C::kQS, sw128_desc(q + off, 16),
+                                      sw128_desc(sbase + C::kOffS + ks * 2048, KP * 128), id_qs, ks > 0);
+                    }
+                    tc_commit(b_sc);
+                }
+            }
+            ok = la_wait(r_k, ph, abort_flag, limit);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                state_product(k, v, true);
+                state_product(q, v, false);
+                tc_commit(b_ds1);
+            }
+            if (KIND == FWD) {
+                ok = la_wait(r_p, ph, abort_flag, limit);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc_mma_f16_ts(tmem + C::kPV, tmem + p_col(ks >> 1) + (ks & 1) * 8,
+                                      sw128_desc(v + ks * 2048, kTileBytes), id_pv, ks > 0);
+                    tc_commit(b_pv);
+                }
+            }
+            if (i + 1 < n) {   // the tables are no longer read
+                la_tables(tab, p, fx, p.T - chunk_of(i + 1) * kLaChunk, floor_);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_tab);
+                if (i + 2 < n) la_load_f(p, bh, chunk_of(i + 2), fx);
+            }
+            ok = la_wait(r_lo, ph, abort_flag, limit);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                state_product(k, v, false);
+                tc_commit(b_ds2);
+            }
+            if (KIND == FWD && !(ok = la_wait(b_pv, ph, abort_flag, limit))) break;
+            if (!(ok = la_wait(b_ds2, ph, abort_flag, limit))) break;
+            if (lane == 0 && i + 2 < n) load(i + 2);
+        }
+        if (!ok && lane == 0) {   // leave nothing in flight: the copies of this chunk and the next, the products
+            for (int j = i; j < loaded; ++j) la_drain(b_full + (j & 1) * 8, (j >> 1) & 1, limit);
+            tc_commit(b_drain);
+            la_drain(b_drain, 0, limit);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ elementwise work
+        const int wg = warp >> 2, quarter = warp & 3;
+        const int row = quarter * 32 + lane;                  // token of the chunk
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;   // tensor-memory lane base
+        // this thread's part of the state: row kap, columns [v0, v0 + NS)
+        const int kap = KP == 128 ? row : row & 63;
+        const int v0 = KP == 128 ? wg * C::NS : (wg * 2 + (row >> 6)) * C::NS;
+        const bool mine = kap < p.K;
+        float S[C::NS];
+        {
+            const float* src = KIND != FWD ? nullptr
+                               : p.segs > 1 ? p.seg_state + ((size_t)bh * p.segs + seg) * p.K * p.V
+                               : p.S0       ? p.S0 + (size_t)bh * p.K * p.V
+                                            : nullptr;
+#pragma unroll
+            for (int j = 0; j < C::NS; j += 4) {
+                const float4 x = src && mine && v0 + j < p.V
+                                     ? *reinterpret_cast<const float4*>(src + (size_t)kap * p.V + v0 + j)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+            }
+        }
+        auto arrive = [&](uint32_t b) {   // this warp's writes are done: shared memory for the products, tensor memory
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b);
+        };
+        auto store_state = [&](float* dst) {
+            if (!mine) return;
+#pragma unroll
+            for (int j = 0; j < C::NS; j += 4)
+                if (v0 + j < p.V)
+                    *reinterpret_cast<float4*>(dst + (size_t)kap * p.V + v0 + j) =
+                        make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        };
+        auto write_operand = [&]() {   // bf16 copy of S for Q·S
+            uint8_t* op = smem + C::kOffS + (v0 >> 6) * (KP * 128);
+#pragma unroll
+            for (int j = 0; j < C::NS; j += 8)
+                *reinterpret_cast<uint4*>(op + sw128(kap, ((v0 & 63) + j) >> 3)) =
+                    make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]), pack_bf16(S[j + 4], S[j + 5]),
+                               pack_bf16(S[j + 6], S[j + 7]));
+            arrive(r_s);
+        };
+        if (KIND == FWD) write_operand();
+        float decay = 1.f;
+
+        for (int i = 0; i < n; ++i) {
+            const int s = i & 1, ph = i & 1, c = chunk_of(i);
+            uint8_t* stage = smem + s * C::kStage;
+            if (KIND == FWD && p.ckpt) store_state(p.ckpt + ((size_t)bh * nchunks + c) * p.K * p.V);
+            if (!la_wait(b_tab, ph, abort_flag, limit)) break;
+            const float Ft = tab->F[row], It = tab->I[row], Fe = tab->F[127], Ie = tab->I[127];
+            const float at = ex2_approx(Ft + It), A = ex2_approx(Fe + Ie);
+            const float w = KIND == RSUM ? at : ex2_approx((Fe - Ft) + (Ie - It));
+            if (!la_wait(b_full + s * 8, (i >> 1) & 1, abort_flag, limit)) break;
+            if (KIND == FWD && !la_wait(b_sc, ph, abort_flag, limit)) break;
+            tc_fence_after();
+            // ---- w k in three bf16 terms: over the k tile, over the q tile, and kept
+            constexpr int kCh = KP / 16;                       // 16-byte chunks of this thread's half row
+            uint32_t lo[kCh][4];
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) {
+                const int ch = wg * kCh + j;
+                const uint32_t at_ = (ch >> 3) * kTileBytes + sw128(row, ch & 7);
+                uint4* kp = reinterpret_cast<uint4*>(stage + C::kQ + at_);
+                const uint4 x = *kp;
+                uint4 hi, mid;
+                split3(w * bf16lo_to_f32(x.x), w * bf16hi_to_f32(x.x), hi.x, mid.x, lo[j][0]);
+                split3(w * bf16lo_to_f32(x.y), w * bf16hi_to_f32(x.y), hi.y, mid.y, lo[j][1]);
+                split3(w * bf16lo_to_f32(x.z), w * bf16hi_to_f32(x.z), hi.z, mid.z, lo[j][2]);
+                split3(w * bf16lo_to_f32(x.w), w * bf16hi_to_f32(x.w), hi.w, mid.w, lo[j][3]);
+                *kp = hi;
+                *reinterpret_cast<uint4*>(stage + at_) = mid;
+            }
+            arrive(r_k);
+            if (KIND == FWD) {
+                // ---- P = masked, decayed scores in bf16, back to tensor memory
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                    const int j = 2 * jj + wg;                 // block of 32 columns
+                    uint32_t pk[16];
+                    if (j > quarter) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e] = 0;
+                    } else {
+                        uint32_t sc[32];
+                        tmem_ld_32x32b<32>(tmem + lanes + j * 32, sc);
+                        tc_wait_ld();
+                        reg_fence(sc);
+                        if (j < quarter) {
+                            const float r = ex2_approx((Ft - tab->F[j * 32 + 31]) + (It - tab->I[j * 32 + 31]));
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 cs = *reinterpret_cast<const float4*>(&tab->c[j * 32 + e]);
+                                pk[e / 2] = pack_bf16(__uint_as_float(sc[e]) * (r * cs.x),
+                                                      __uint_as_float(sc[e + 1]) * (r * cs.y));
+                                pk[e / 2 + 1] = pack_bf16(__uint_as_float(sc[e + 2]) * (r * cs.z),
+                                                          __uint_as_float(sc[e + 3]) * (r * cs.w));
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 fs = *reinterpret_cast<const float4*>(&tab->F[j * 32 + e]);
+                                const float4 is = *reinterpret_cast<const float4*>(&tab->I[j * 32 + e]);
+                                auto d = [&](int o, float f, float w_) {
+                                    return e + o <= lane ? __uint_as_float(sc[e + o]) * ex2_approx((Ft - f) + (It - w_))
+                                                         : 0.f;
+                                };
+                                pk[e / 2] = pack_bf16(d(0, fs.x, is.x), d(1, fs.y, is.y));
+                                pk[e / 2 + 1] = pack_bf16(d(2, fs.z, is.z), d(3, fs.w, is.w));
+                            }
+                        }
+                    }
+                    tmem_st16(tmem + lanes + p_col(j), pk);
+                }
+                tc_wait_st();
+                arrive(r_p);
+            }
+            // ---- the state's third term, once the first two are multiplied
+            if (!la_wait(b_ds1, ph, abort_flag, limit)) break;
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) {
+                const int ch = wg * kCh + j;
+                *reinterpret_cast<uint4*>(stage + C::kQ + (ch >> 3) * kTileBytes + sw128(row, ch & 7)) =
+                    make_uint4(lo[j][0], lo[j][1], lo[j][2], lo[j][3]);
+            }
+            arrive(r_lo);
+            if (KIND == FWD) {
+                // ---- y = a (Q S) + P V
+                if (!la_wait(b_pv, ph, abort_flag, limit)) break;
+                tc_fence_after();
+                const int t = c * kLaChunk + row;
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + ((size_t)bh * p.T + t) * p.V;
+#pragma unroll
+                for (int j = 0; j < VP / 2; j += 16) {
+                    const int col = wg * (VP / 2) + j;
+                    uint32_t pv[16], qs[16];
+                    tmem_ld_32x32b<16>(tmem + lanes + C::kPV + col, pv);
+                    tmem_ld_32x32b<16>(tmem + lanes + C::kQS + col, qs);
+                    tc_wait_ld();
+                    reg_fence(pv);
+                    reg_fence(qs);
+                    if (t < p.T && col < p.V) {
+                        uint32_t o[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o[e] = pack_bf16(fmaf(at, __uint_as_float(qs[2 * e]), __uint_as_float(pv[2 * e])),
+                                             fmaf(at, __uint_as_float(qs[2 * e + 1]), __uint_as_float(pv[2 * e + 1])));
+                        *reinterpret_cast<uint4*>(y + col) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(y + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+            }
+            // ---- S = A S + the chunk's sum
+            if (!la_wait(b_ds2, ph, abort_flag, limit)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < C::NS; j += 16) {
+                uint32_t d[16];
+                tmem_ld_32x32b<16>(tmem + lanes + C::kDS + v0 + j, d);
+                tc_wait_ld();
+                reg_fence(d);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) S[j + e] = fmaf(A, S[j + e], __uint_as_float(d[e]));
+            }
+            decay *= A;
+            if (KIND == FWD) {
+                if (i + 1 < n) write_operand();
+            } else {
+                tc_fence_before();   // ordered before the next chunk's r_k arrival
+            }
+        }
+        if (KIND != FWD) {
+            store_state(p.seg_state + ((size_t)bh * p.segs + seg) * p.K * p.V);
+            if (threadIdx.x == 0) seg_decay[(size_t)bh * p.segs + seg] = decay;
+        } else if (p.ST && c0 + n == nchunks) {
+            store_state(p.ST + (size_t)bh * p.K * p.V);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmem);
+    }
+}
+
+// Segment sums -> segment start states, in place: start_0 = init,
+// start_{i+1} = decay_i start_i + sum_i (reverse: from the last segment, for
+// the gradient at segment ends).  A thread takes four adjacent elements.
+__global__ void m2rnn_la_seg_scan_kernel(const LaParams p, const float* __restrict__ seg_decay, const float* init,
+                                         int reverse) {
+    const int kv4 = p.K * p.V / 4;
+    const size_t e = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
+    if (e >= (size_t)p.B * p.H * kv4) return;
+    const size_t bh = e / kv4, o = e % kv4;
+    float4* st = reinterpret_cast<float4*>(p.seg_state) + bh * p.segs * kv4 + o;
+    float4 s = init ? reinterpret_cast<const float4*>(init)[bh * kv4 + o] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < p.segs; ++i) {
+        const int g = reverse ? p.segs - 1 - i : i;
+        const float4 d = st[(size_t)g * kv4];
+        st[(size_t)g * kv4] = s;
+        const float a = seg_decay[bh * p.segs + g];
+        s.x = fmaf(a, s.x, d.x); s.y = fmaf(a, s.y, d.y); s.z = fmaf(a, s.z, d.z); s.w = fmaf(a, s.w, d.w);
+    }
+}
+
+template <int KP, int VP, Kind KIND>
+cudaError_t launch(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
+    using C = Cfg<KP, VP>;
+    auto kern = m2rnn_la_fwd_tc_kernel<KP, VP, KIND>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<p.B * p.H * p.segs, C::kThreads, C::kSmem, s>>>(p, m, seg_decay);
+    return cudaGetLastError();
+}
+template <Kind KIND>
+cudaError_t launch_shape(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
+    if (p.K <= 64)
+        return p.V <= 64 ? launch<64, 64, KIND>(p, m, seg_decay, s) : launch<64, 128, KIND>(p, m, seg_decay, s);
+    return p.V <= 64 ? launch<128, 64, KIND>(p, m, seg_decay, s) : launch<128, 128, KIND>(p, m, seg_decay, s);
+}
+
+float* decays_of(const LaParams& p) {   // behind the segment states in the workspace
+    return p.seg_state + (size_t)p.B * p.H * p.segs * p.K * p.V;
+}
+
+}  // namespace
+
+LaPlan la_fwd_plan(int B, int H, int T, int K, int V) {
+    const int chunks = (T + kLaChunk - 1) / kLaChunk, per_sm = K <= 64 && V <= 64 ? 2 : 1;
+    const long long pairs = (long long)B * H, slots = (long long)kNumSMs * per_sm;
+    long long segs = 1;
+    if (pairs * 2 <= slots && chunks >= 4) segs = slots / pairs;
+#ifdef LA_TUNE
+    if (const char* e = getenv("LA_SEGS")) segs = atoi(e);
+#endif
+    if (segs > chunks / 2) segs = chunks / 2;
+    if (segs < 1) segs = 1;
+    const int per = (int)((chunks + segs - 1) / segs);
+    return {(chunks + per - 1) / per, per};
+}
+
+size_t la_seg_bytes(const LaPlan& plan, int B, int H, int K, int V) {
+    return plan.segs <= 1 ? 0 : sizeof(float) * (size_t)B * H * plan.segs * ((size_t)K * V + 1);
+}
+
+cudaError_t launch_la_fwd_tc(const LaParams& p, cudaStream_t s) {
+    Maps m;
+    if (!la_tensor_map(&m.q, p.q, p.K, p.T, (size_t)p.B * p.G) || !la_tensor_map(&m.k, p.k, p.K, p.T, (size_t)p.B * p.G) ||
+        !la_tensor_map(&m.v, p.v, p.V, p.T, (size_t)p.B * p.H))
+        return cudaErrorNotSupported;
+    if (p.segs > 1) {
+        cudaError_t e = launch_shape<SUM>(p, m, decays_of(p), s);
+        if (e != cudaSuccess) return e;
+        const size_t n = (size_t)p.B * p.H * p.K * p.V / 4;
+        m2rnn_la_seg_scan_kernel<<<(unsigned)((n + 127) / 128), 128, 0, s>>>(p, decays_of(p), p.S0, 0);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return launch_shape<FWD>(p, m, nullptr, s);
+}
+
+// Reads and clears the status word of this file's kernels.
+cudaError_t la_fwd_tc_status(unsigned* word, cudaStream_t s) {
+    const unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_la_status, sizeof *word, 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && *word) {
+        e = cudaMemcpyToSymbolAsync(g_la_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
+    return e;
+}
+
+}  // namespace m2rnn

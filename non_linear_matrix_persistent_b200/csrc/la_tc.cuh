@@ -1,0 +1,169 @@
+// Pieces shared by the tensor-core kernels of linear attention: tiles of 128
+// tokens fetched by TMA into 128-byte-swizzled shared memory, their matrix
+// descriptors, decays, operand splitting and bounded waits.
+//
+// A tile [128 rows][64 columns] of bf16 takes 16 KB: row r at r·128 bytes, its
+// 16-byte chunk c at position c ^ (r & 7) (the 128-byte swizzle).  A width of
+// 128 is two such tiles; widths of 16 and 32 run as 64, with the columns and
+// the rows behind the last token filled with zeros by the copy.  The same tile
+// serves as a K-major operand (contraction along the columns) and as an
+// MN-major one (contraction along the rows), so no transposed copy exists.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "linear_attention.h"
+#include "ptx.cuh"
+
+namespace m2rnn {
+
+constexpr int kTileBytes = 128 * 128;   // 128 tokens x 64 bf16
+
+// The kernels' device status: one word per source file, read and cleared by
+// m2rnn_linear_attention_status.  A wait that runs out sets it.
+static __device__ unsigned g_la_status;
+
+// Floor of a gate's base-2 logarithm.  Forward: 2^-256, which every product of
+// decays flushes to 0, so a gate of 0 (or below 2^-126) discards the state.
+// Backward: 2^-64, so that the sums over paths through a gate of 0, divided by
+// the gate again, still give its gradient.
+constexpr float kLogFloorFwd = -256.f, kLogFloorBwd = -64.f;
+
+// log2 of a gate split into an integer and a fraction in [-1/2, 1/2]: sums of
+// the integers are exact, so differences of cumulative sums keep their
+// precision behind a gate close to 0.  A NaN stays a NaN.
+__device__ __forceinline__ void la_log2(const LaParams& p, float x, float floor_, float& whole, float& frac) {
+    float l = p.f_is_logit ? -1.4426950408889634f * log1pf(expf(-x)) : log2f(x);
+    l = l < floor_ ? floor_ : l;
+    whole = rintf(l);
+    frac = l - whole;
+}
+
+// Cumulative log-decays of a chunk's 128 tokens, from the chunk's start
+// through the token, by one warp (4 tokens a lane): F + I in shared memory,
+// and c[s] = the decay from s to the last token of its block of 32.
+struct LaTables {
+    float F[128], I[128], c[128];
+};
+__device__ __forceinline__ void la_tables(LaTables* tab, const LaParams& p, const float (&x)[4], int valid, float floor_) {
+    const int lane = threadIdx.x & 31;
+    float F[4], I[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        la_log2(p, x[i], floor_, I[i], F[i]);
+        if (lane * 4 + i >= valid) { F[i] = 0.f; I[i] = 0.f; }   // behind the last token: a gate of 1
+        if (i > 0) { F[i] += F[i - 1]; I[i] += I[i - 1]; }
+    }
+    float f = F[3], w = I[3];
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const float a = __shfl_up_sync(~0u, f, d), b = __shfl_up_sync(~0u, w, d);
+        if (lane >= d) { f += a; w += b; }
+    }
+    const float f0 = __shfl_up_sync(~0u, f, 1), w0 = __shfl_up_sync(~0u, w, 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        F[i] += lane ? f0 : 0.f;
+        I[i] += lane ? w0 : 0.f;
+    }
+    const float fe = __shfl_sync(~0u, F[3], lane | 7), we = __shfl_sync(~0u, I[3], lane | 7);   // the block's last token
+    *reinterpret_cast<float4*>(&tab->F[lane * 4]) = make_float4(F[0], F[1], F[2], F[3]);
+    *reinterpret_cast<float4*>(&tab->I[lane * 4]) = make_float4(I[0], I[1], I[2], I[3]);
+    *reinterpret_cast<float4*>(&tab->c[lane * 4]) =
+        make_float4(ex2_approx((fe - F[0]) + (we - I[0])), ex2_approx((fe - F[1]) + (we - I[1])),
+                    ex2_approx((fe - F[2]) + (we - I[2])), ex2_approx((fe - F[3]) + (we - I[3])));
+}
+// The f inputs of chunk c for la_tables; 0 behind the last token.
+__device__ __forceinline__ void la_load_f(const LaParams& p, int bh, int c, float (&x)[4]) {
+    const int t = c * kLaChunk + (threadIdx.x & 31) * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = t + i < p.T ? la_f_input(p, bh, t + i) : 0.f;
+}
+
+// ---------------------------------------------------------------- operands
+// Byte position of the 16-byte chunk `ch` (of 8) of row `row` in a swizzled tile.
+__device__ __forceinline__ uint32_t sw128(int row, int ch) { return row * 128 + ((ch ^ (row & 7)) << 4); }
+
+// Descriptor of a 128-byte-swizzled operand.  K-major: lbo unused, sbo = 1024
+// (8 rows).  MN-major: lbo = bytes from one 64-column tile to the next, sbo =
+// 1024 (8 contraction rows).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo) {
+    return smem_desc(saddr, lbo, 1024) | (2ull << 61);
+}
+
+// D[tmem] (+)= A[tmem] · B[smem], A: 128 lanes, two bf16 per 32-bit column.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Tensor-memory store of 16 columns (32x32b).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// x = hi + mid + lo to about 2^-26 of x: each term is what the bf16 before it
+// left over (exact in fp32), rounded to nearest.
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = pack_bf16(x0, x1);
+    x0 -= bf16lo_to_f32(hi);
+    x1 -= bf16hi_to_f32(hi);
+    mid = pack_bf16(x0, x1);
+    lo = pack_bf16(x0 - bf16lo_to_f32(mid), x1 - bf16hi_to_f32(mid));
+}
+
+// ---------------------------------------------------------------- TMA
+// Box of 128 tokens x 64 columns at column x, token t of row block z.
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int x, int t, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(t), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// ---------------------------------------------------------------- waits
+// Bounded mbarrier wait: false when it runs longer than the limit or another
+// thread of the CTA has given up.
+__device__ __forceinline__ bool la_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > limit_ns) {
+            *abort_flag = 1;
+            atomicOr(&g_la_status, 1u);
+            return false;
+        }
+    }
+}
+// The same without the abort flag: for copies and products in flight before the CTA exits.
+__device__ __forceinline__ void la_drain(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > limit_ns) {
+            atomicOr(&g_la_status, 1u);
+            return;
+        }
+}
+
+// ---------------------------------------------------------------- host
+// Tensor map of x [rows][T][width] bf16: boxes of 128 tokens x 64 columns.
+bool la_tensor_map(CUtensorMap* map, const void* x, int width, int T, size_t rows);
+
+}  // namespace m2rnn

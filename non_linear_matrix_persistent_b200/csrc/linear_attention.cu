@@ -44,6 +44,12 @@ size_t group_bytes(const m2rnn_la_dims* d) {
 // Per-token df before the sum over batch and time.
 size_t df_bytes(const m2rnn_la_dims* d) { return d->f_per_head ? round256(sizeof(float) * pairs(d) * d->T) : 0; }
 
+// Prompts run on the tensor cores; short ones, a chunk of which would be mostly
+// padding, token by token.
+bool fwd_on_tensor_cores(const m2rnn_la_dims* d) { return d->mode == M2RNN_MODE_BF16_TC && d->T > 16; }
+
+m2rnn::LaPlan fwd_plan(const m2rnn_la_dims* d) { return m2rnn::la_fwd_plan(d->B, d->H, d->T, d->K, d->V); }
+
 m2rnn::LaParams params(const m2rnn_la_dims* d) {
     m2rnn::LaParams p;
     std::memset(&p, 0, sizeof p);
@@ -52,6 +58,10 @@ m2rnn::LaParams params(const m2rnn_la_dims* d) {
     p.bf16 = d->mode == M2RNN_MODE_BF16_TC;
     p.f_is_logit = d->f_is_logit;
     p.f_per_head = d->f_per_head;
+    p.segs = 1;
+    p.seg_chunks = (d->T + m2rnn::kLaChunk - 1) / m2rnn::kLaChunk;
+    p.wait_limit_ns = m2rnn::wait_limit_ns();
+    p.fault = m2rnn::injected_fault();
     return p;
 }
 
@@ -70,7 +80,8 @@ extern "C" {
 
 size_t m2rnn_linear_attention_workspace(const m2rnn_la_dims* d, int backward) {
     if (check(d) != M2RNN_OK) return kRefused;
-    if (!backward || pairs(d) * d->T == 0) return 0;
+    if (pairs(d) * d->T == 0) return 0;
+    if (!backward) return fwd_on_tensor_cores(d) ? m2rnn::la_seg_bytes(fwd_plan(d), d->B, d->H, d->K, d->V) : 0;
     return group_bytes(d) + df_bytes(d);
 }
 
@@ -87,7 +98,11 @@ m2rnn_status m2rnn_linear_attention_forward(const m2rnn_la_dims* d, const void* 
     if (pairs(d) * d->T == 0) return pass_through(ST, S0, pairs(d) * d->K * d->V, s);
     m2rnn::LaParams p = params(d);
     p.k = k; p.v = v; p.q = q; p.f = f; p.S0 = S0; p.y = y; p.ST = ST; p.ckpt = ckpt;
-    return status_of(m2rnn::launch_la_rec(p, s));
+    if (!fwd_on_tensor_cores(d)) return status_of(m2rnn::launch_la_rec(p, s));
+    const m2rnn::LaPlan plan = fwd_plan(d);
+    p.segs = plan.segs; p.seg_chunks = plan.seg_chunks;
+    p.seg_state = static_cast<float*>(workspace);
+    return status_of(m2rnn::launch_la_fwd_tc(p, s));
 }
 
 m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void* k, const void* v, const void* q,
@@ -128,7 +143,10 @@ m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void*
 }
 
 m2rnn_status m2rnn_linear_attention_status(m2rnn_stream_t stream) {
-    return status_of(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    unsigned word = 0;
+    if (m2rnn::la_fwd_tc_status(&word, s) != cudaSuccess) return M2RNN_ERR_CUDA;
+    return word ? M2RNN_ERR_DEVICE_TIMEOUT : M2RNN_OK;
 }
 
 // ------------------------------------------------------------------ layer norm

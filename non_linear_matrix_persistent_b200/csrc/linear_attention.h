@@ -40,6 +40,13 @@ struct LaParams {
     int seg_chunks;         // chunks of 128 tokens per segment
     float* seg_state;       // [B*H][segs][K][V] (workspace)
     uint64_t wait_limit_ns;
+    int fault;              // injected fault (m2rnn_debug_set_fault), 0 = none
+};
+
+// Time segments of the tensor-core kernels: CTAs along T for each (b, h), and
+// their length in chunks.
+struct LaPlan {
+    int segs, seg_chunks;
 };
 
 // Row block of k and q that pair bh = b·H + h reads.
@@ -68,6 +75,12 @@ __device__ __forceinline__ __nv_bfloat16 la_from_f32<__nv_bfloat16>(float x) { r
 // Token-by-token forward on the CUDA cores, any T and both types: the decode
 // step, short prompts and the fp32 mode.
 cudaError_t launch_la_rec(const LaParams& p, cudaStream_t s);
+// Chunked tensor-core forward (bf16): y, ST and the checkpoints.
+cudaError_t launch_la_fwd_tc(const LaParams& p, cudaStream_t s);
+LaPlan la_fwd_plan(int B, int H, int T, int K, int V);
+// Workspace of a plan: segment states and decays.
+size_t la_seg_bytes(const LaPlan& plan, int B, int H, int K, int V);
+cudaError_t la_fwd_tc_status(unsigned* word, cudaStream_t s);
 // fp32-arithmetic backward on the CUDA cores, both types.
 cudaError_t launch_la_bwd_simt(const LaParams& p, cudaStream_t s);
 // dk, dq [B, G, T, K] (bf16 or fp32) = sums of fp32 per-head partials over each group's heads, ascending.

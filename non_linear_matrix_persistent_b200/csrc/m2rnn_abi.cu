@@ -54,6 +54,11 @@ m2rnn::Params base_params(const m2rnn_dims* d, void* ws) {
 
 }  // namespace
 
+namespace m2rnn {
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
+int injected_fault() { return g_fault.load(); }
+}  // namespace m2rnn
+
 extern "C" {
 
 size_t m2rnn_workspace_size(const m2rnn_dims* d, int backward) {
