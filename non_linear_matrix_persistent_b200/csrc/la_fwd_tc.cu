@@ -7,12 +7,12 @@
 // Four matrix products, every accumulator in tensor memory; the state's fp32
 // master stays in registers over the whole walk.
 //
-// A CTA walks the chunks of one (b, h), or of one of its time segments.  Eight
-// warps compute: thread = token row (or state row) = tensor-memory lane, the
-// two warpgroups sharing the columns.  A ninth warp fetches tiles two chunks
-// ahead, issues the products and computes the decays of the next chunk.  A
-// chunk is a chain of waits (product -> elementwise -> product), so two CTAs
-// share an SM where they fit.
+// A CTA walks the chunks of one (b, h), or of one of its time segments.  8 or
+// 16 warps compute: thread = token row (or state row) = tensor-memory lane, the
+// warpgroups sharing the columns.  One more warp issues the products, another
+// fetches tiles two chunks ahead, stores y and computes the next chunk's
+// decays.  A chunk is a chain of waits (product -> elementwise -> product):
+// two CTAs of 8 warps share an SM where they fit, else a CTA has 16.
 //
 // Rounding: the masked scores and the copy of S that multiplies Q are bf16
 // operands (each term of y passes through exactly one of them, and y is
@@ -57,7 +57,7 @@ bool la_tensor_map(CUtensorMap* map, const void* x, int width, int T, size_t row
 namespace {
 
 struct Maps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, y;
 };
 
 // FWD: the forward.  SUM: only the segment's own contribution to its final
@@ -65,32 +65,37 @@ struct Maps {
 // from the segment's start: Σ_t a_t k_t v_tᵀ.
 enum Kind { FWD, SUM, RSUM };
 
-template <int KP, int VP>
+// NW compute warps: 8 (two CTAs share an SM where they fit) or 16 (one CTA
+// that has an SM to itself).
+template <int KP, int VP, int NW>
 struct Cfg {
-    static constexpr int kThreads = 288;
+    static constexpr int kThreads = (NW + 2) * 32, WG = NW / 4;
     static constexpr int kQ = KP / 64 * kTileBytes, kV = VP / 64 * kTileBytes, kStage = 2 * kQ + kV;
     static constexpr int kOffS = 2 * kStage;                    // bf16 state operand [KP][VP]
     static constexpr int kOffTab = kOffS + KP * VP * 2;
     static constexpr int kOffBar = kOffTab + (int)sizeof(LaTables);
-    static constexpr int kBars = 12;
+    static constexpr int kBars = 13;
     static constexpr int kSmem = kOffBar + kBars * 8 + 16;
-    static constexpr int kCtas = kSmem <= 113 * 1024 ? 2 : 1;
-    // tensor memory: scores, over which P (bf16) and, for 64 columns, the
-    // second half's product go once the scores are read; Q·S; the state's sum
-    static constexpr int kTmem = VP == 64 ? 256 : 512;
-    static constexpr int kPV = VP == 64 ? 64 : 128, kQS = VP == 64 ? 128 : 256, kDS = VP == 64 ? 192 : 384;
-    static constexpr int NS = KP == 128 ? VP / 2 : VP / 4;      // state columns per thread
+    static constexpr int kCtas = NW == 8 && kSmem <= 113 * 1024 ? 2 : 1;
+    // tensor memory: scores (P in bf16 over them), P·V, Q·S, the state's sum.
+    // With two CTAs an SM, P·V takes the second half of the scores, which P leaves free.
+    static constexpr bool kPacked = kCtas == 2;
+    static constexpr int kTmem = kPacked ? 256 : 512;
+    static constexpr int kPV = kPacked ? 64 : 128, kQS = kPV + VP, kDS = kQS + VP;
+    static_assert(kDS + VP <= kTmem, "tensor memory");
+    static constexpr int NS = VP / WG / (KP == 128 ? 1 : 2);    // state columns per thread
+    static constexpr int NL = NS < 16 ? NS : 16;                // per tensor-memory load
+    static constexpr int NY = VP / WG;                          // columns of y per thread
+    // Tensor-memory column of the 16 columns of P that hold score block j (of
+    // 32 columns; warpgroup j % WG computes it): inside that warpgroup's own
+    // score columns, so that no warp writes over scores that another reads.
+    static constexpr __device__ int p_col(int j) { return kPacked ? (j & 1) * 32 + (j >> 1) * 16 : j * 32; }
 };
 
-// Tensor-memory column of the 16 columns of P that hold score block j (of 32):
-// inside the score columns of the warpgroup that computes it (block j belongs
-// to warpgroup j % 2), so that no warp writes over scores that another reads.
-__device__ __forceinline__ constexpr int p_col(int j) { return (j & 1) * 32 + (j >> 1) * 16; }
-
-template <int KP, int VP, Kind KIND>
-__global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
+template <int KP, int VP, int NW, Kind KIND>
+__global__ void __launch_bounds__(Cfg<KP, VP, NW>::kThreads, Cfg<KP, VP, NW>::kCtas)
     m2rnn_la_fwd_tc_kernel(const LaParams p, const __grid_constant__ Maps maps, float* seg_decay) {
-    using C = Cfg<KP, VP>;
+    using C = Cfg<KP, VP, NW>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bh = blockIdx.x / p.segs, seg = blockIdx.x % p.segs;
@@ -103,7 +108,7 @@ __global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const uint32_t b_full = bar(0), b_sc = bar(2), r_k = bar(3), b_ds1 = bar(4), r_p = bar(5), b_pv = bar(6),
-                   r_lo = bar(7), b_ds2 = bar(8), r_s = bar(9), b_tab = bar(10), b_drain = bar(11);
+                   r_lo = bar(7), b_ds2 = bar(8), r_s = bar(9), b_tab = bar(10), b_drain = bar(11), r_y = bar(12);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint64_t limit = p.wait_limit_ns;
@@ -112,11 +117,11 @@ __global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
         mbar_init(bar(0), 1);
         mbar_init(bar(1), 1);
         for (uint32_t b : {b_sc, b_ds1, b_pv, b_ds2, b_tab, b_drain}) mbar_init(b, 1);
-        for (uint32_t b : {r_k, r_p, r_lo, r_s}) mbar_init(b, 8);   // one arrival a warp
+        for (uint32_t b : {r_k, r_p, r_lo, r_s, r_y}) mbar_init(b, NW);   // one arrival a warp
         *abort_flag = 0;
         fence_mbarrier_init();
     }
-    if (warp == 8) {
+    if (warp == NW) {
         tmem_alloc(smem_u32(tmem_slot), C::kTmem);
         tmem_relinquish();
     }
@@ -126,8 +131,73 @@ __global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
     const uint32_t tmem = *tmem_slot;
     const uint32_t sbase = smem_u32(smem);
 
-    if (warp == 8) {
-        // ------------------------------------------------------ copies, products, decays
+    if (warp == NW) {
+        // ------------------------------------------------------ products
+        constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, 0, 0), id_qs = idesc_bf16_f32(128, VP, 0, 1),
+                           id_pv = idesc_bf16_f32(128, VP, 0, 1), id_ds = idesc_bf16_f32(KP, VP, 1, 1);
+        const uint64_t d_tile = sw128_desc(sbase, 16), d_mn = sw128_desc(sbase, kTileBytes),
+                       d_s = sw128_desc(sbase + C::kOffS, KP * 128);
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int s = i & 1, ph = i & 1;
+            // operand positions in units of 16 bytes
+            const uint32_t q = s * (C::kStage >> 4), k = q + (C::kQ >> 4), v = k + (C::kQ >> 4);
+            // the state's product: A = a scaled k tile, its rows (tokens) along the contraction
+            auto state_product = [&](uint32_t a, bool first) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    tc_mma_f16_ss(tmem + C::kDS, d_mn + a + ks * 128, d_mn + v + ks * 128, id_ds, !(first && ks == 0));
+            };
+            if (!(ok = la_wait(b_full + s * 8, (i >> 1) & 1, abort_flag, limit))) break;
+            if (KIND == FWD) {
+                if (!(ok = la_wait(r_s, ph, abort_flag, limit))) break;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int ks = 0; ks < KP / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * (kTileBytes >> 4) + (ks & 3) * 2;
+                        tc_mma_f16_ss(tmem, d_tile + q + off, d_tile + k + off, id_sc, ks > 0);
+                    }
+#pragma unroll
+                    for (int ks = 0; ks < KP / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * (kTileBytes >> 4) + (ks & 3) * 2;
+                        tc_mma_f16_ss(tmem + C::kQS, d_tile + q + off, d_s + ks * 128, id_qs, ks > 0);
+                    }
+                    tc_commit(b_sc);
+                }
+            }
+            if (!(ok = la_wait(r_k, ph, abort_flag, limit))) break;
+            tc_fence_after();
+            if (lane == 0) {
+                state_product(k, true);
+                state_product(q, false);
+                tc_commit(b_ds1);
+            }
+            if (KIND == FWD) {
+                if (!(ok = la_wait(r_p, ph, abort_flag, limit))) break;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc_mma_f16_ts(tmem + C::kPV, tmem + C::p_col(ks >> 1) + (ks & 1) * 8, d_mn + v + ks * 128, id_pv,
+                                      ks > 0);
+                    tc_commit(b_pv);
+                }
+            }
+            if (!(ok = la_wait(r_lo, ph, abort_flag, limit))) break;
+            tc_fence_after();
+            if (lane == 0) {
+                state_product(k, false);
+                tc_commit(b_ds2);
+            }
+        }
+        if (lane == 0) {   // nothing is in flight when the CTA ends
+            tc_commit(b_drain);
+            la_drain(b_drain, 0, limit);
+        }
+        __syncwarp();
+    } else if (warp == NW + 1) {
+        // ------------------------------------------------------ copies and decays
         const int qk = la_qk_pair(p, bh);
         int loaded = 0;
         auto load = [&](int i) {   // lane 0: the tiles of the walk's i-th chunk
@@ -136,10 +206,12 @@ __global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
             const int s = i & 1, t = chunk_of(i) * kLaChunk;
             const uint32_t base = sbase + s * C::kStage, full = b_full + s * 8;
             mbar_arrive_expect_tx(full, KIND == FWD ? C::kStage : C::kQ + C::kV);
+#pragma unroll
             for (int x = 0; x < KP / 64; ++x) {
                 if (KIND == FWD) tma_tile(base + x * kTileBytes, &maps.q, x * 64, t, qk, full);
                 tma_tile(base + C::kQ + x * kTileBytes, &maps.k, x * 64, t, qk, full);
             }
+#pragma unroll
             for (int x = 0; x < VP / 64; ++x) tma_tile(base + 2 * C::kQ + x * kTileBytes, &maps.v, x * 64, t, bh, full);
         };
         if (lane == 0) {
@@ -147,96 +219,53 @@ __global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
             if (n > 1) load(1);
         }
         const float floor_ = KIND == RSUM ? kLogFloorBwd : kLogFloorFwd;
-        float fx[4];
+        float fx[4], fnext[4];
         la_load_f(p, bh, chunk_of(0), fx);
+        la_load_f(p, bh, n > 1 ? chunk_of(1) : chunk_of(0), fnext);
         la_tables(tab, p, fx, p.T - chunk_of(0) * kLaChunk, floor_);
         __syncwarp();
         if (lane == 0) mbar_arrive(b_tab);
-        if (n > 1) la_load_f(p, bh, chunk_of(1), fx);
-
-        constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, 0, 0), id_qs = idesc_bf16_f32(128, VP, 0, 1),
-                           id_pv = idesc_bf16_f32(128, VP, 0, 1), id_ds = idesc_bf16_f32(128, VP, 1, 1);
-        // the state's product: A = the scaled k tile, its rows (tokens) along the contraction; 64 state rows
-        // are computed twice (lbo 0: lanes 64..127 repeat lanes 0..63)
-        auto state_product = [&](uint32_t a, uint32_t v, bool first) {
-            for (int ks = 0; ks < 8; ++ks)
-                tc_mma_f16_ss(tmem + C::kDS, sw128_desc(a + ks * 2048, KP == 128 ? kTileBytes : 0),
-                              sw128_desc(v + ks * 2048, kTileBytes), id_ds, !(first && ks == 0));
-        };
         bool ok = true;
         int i = 0;
         for (; i < n; ++i) {
-            const int s = i & 1, ph = i & 1;
-            const uint32_t q = sbase + s * C::kStage, k = q + C::kQ, v = k + C::kQ;
-            ok = la_wait(b_full + s * 8, (i >> 1) & 1, abort_flag, limit);
-            if (!ok) break;
-            if (KIND == FWD) {
-                ok = la_wait(r_s, ph, abort_flag, limit);
-                if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) {
-                    for (int ks = 0; ks < KP / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * kTileBytes + (ks & 3) * 32;
-                        tc_mma_f16_ss(tmem, sw128_desc(q + off, 16), sw128_desc(k + off, 16), id_sc, ks > 0);
-                    }
-                    for (int ks = 0; ks < KP / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * kTileBytes + (ks & 3) * 32;
-                        tc_mma_f16_ss(tmem + C::kQS, sw128_desc(q + off, 16),
-                                      sw128_desc(sbase + C::kOffS + ks * 2048, KP * 128), id_qs, ks > 0);
-                    }
-                    tc_commit(b_sc);
-                }
-            }
-            ok = la_wait(r_k, ph, abort_flag, limit);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-                state_product(k, v, true);
-                state_product(q, v, false);
-                tc_commit(b_ds1);
-            }
-            if (KIND == FWD) {
-                ok = la_wait(r_p, ph, abort_flag, limit);
-                if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) {
-                    for (int ks = 0; ks < 8; ++ks)
-                        tc_mma_f16_ts(tmem + C::kPV, tmem + p_col(ks >> 1) + (ks & 1) * 8,
-                                      sw128_desc(v + ks * 2048, kTileBytes), id_pv, ks > 0);
-                    tc_commit(b_pv);
-                }
-            }
-            if (i + 1 < n) {   // the tables are no longer read
+            const int ph = i & 1;
+            if (i + 1 < n) {   // the next chunk's decays, once this one's are no longer read
+#pragma unroll
+                for (int e = 0; e < 4; ++e) fx[e] = fnext[e];
+                if (i + 2 < n) la_load_f(p, bh, chunk_of(i + 2), fnext);
+                if (!(ok = la_wait(KIND == FWD ? r_p : r_k, ph, abort_flag, limit))) break;
                 la_tables(tab, p, fx, p.T - chunk_of(i + 1) * kLaChunk, floor_);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_tab);
-                if (i + 2 < n) la_load_f(p, bh, chunk_of(i + 2), fx);
             }
-            ok = la_wait(r_lo, ph, abort_flag, limit);
-            if (!ok) break;
-            tc_fence_after();
+            // the stage is free when its products are done and y, staged over its q (and k) tile, has left
+            if (!(ok = la_wait(KIND == FWD ? r_y : b_ds2, ph, abort_flag, limit))) break;
             if (lane == 0) {
-                state_product(k, v, false);
-                tc_commit(b_ds2);
+                if (KIND == FWD) {
+#pragma unroll
+                    for (int x = 0; x < VP / 64; ++x)
+                        if (x * 64 < p.V)
+                            tma_store_tile(&maps.y, sbase + (i & 1) * C::kStage + x * kTileBytes, x * 64,
+                                           chunk_of(i) * kLaChunk, bh);
+                    tma_store_commit();
+                    tma_store_wait_read();
+                }
+                if (i + 2 < n) load(i + 2);
             }
-            if (KIND == FWD && !(ok = la_wait(b_pv, ph, abort_flag, limit))) break;
-            if (!(ok = la_wait(b_ds2, ph, abort_flag, limit))) break;
-            if (lane == 0 && i + 2 < n) load(i + 2);
         }
-        if (!ok && lane == 0) {   // leave nothing in flight: the copies of this chunk and the next, the products
+        if (!ok && lane == 0)   // leave no copy in flight
             for (int j = i; j < loaded; ++j) la_drain(b_full + (j & 1) * 8, (j >> 1) & 1, limit);
-            tc_commit(b_drain);
-            la_drain(b_drain, 0, limit);
-        }
         __syncwarp();
     } else {
         // ------------------------------------------------------ elementwise work
         const int wg = warp >> 2, quarter = warp & 3;
-        const int row = quarter * 32 + lane;                  // token of the chunk
+        const int row = quarter * 32 + lane;                     // token of the chunk
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;   // tensor-memory lane base
-        // this thread's part of the state: row kap, columns [v0, v0 + NS)
-        const int kap = KP == 128 ? row : row & 63;
-        const int v0 = KP == 128 ? wg * C::NS : (wg * 2 + (row >> 6)) * C::NS;
+        // This thread's part of the state: row kap, columns [v0, v0 + NS).  The
+        // sum of 128 state rows has a lane for each; that of 64 rows has 16
+        // lanes in every quarter, which two half warps read.
+        const int kap = KP == 128 ? row : quarter * 16 + (lane & 15);
+        const int v0 = KP == 128 ? wg * C::NS : (wg * 2 + (lane >> 4)) * C::NS;
         const bool mine = kap < p.K;
         float S[C::NS];
         {
@@ -273,9 +302,11 @@ __global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
                 *reinterpret_cast<uint4*>(op + sw128(kap, ((v0 & 63) + j) >> 3)) =
                     make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]), pack_bf16(S[j + 4], S[j + 5]),
                                pack_bf16(S[j + 6], S[j + 7]));
-            arrive(r_s);
         };
-        if (KIND == FWD) write_operand();
+        if (KIND == FWD) {
+            write_operand();
+            arrive(r_s);
+        }
         float decay = 1.f;
 
         for (int i = 0; i < n; ++i) {
@@ -290,7 +321,7 @@ __global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
             if (KIND == FWD && !la_wait(b_sc, ph, abort_flag, limit)) break;
             tc_fence_after();
             // ---- w k in three bf16 terms: over the k tile, over the q tile, and kept
-            constexpr int kCh = KP / 16;                       // 16-byte chunks of this thread's half row
+            constexpr int kCh = KP / 8 / C::WG;                 // 16-byte chunks of the row for this thread
             uint32_t lo[kCh][4];
 #pragma unroll
             for (int j = 0; j < kCh; ++j) {
@@ -310,8 +341,7 @@ __global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
             if (KIND == FWD) {
                 // ---- P = masked, decayed scores in bf16, back to tensor memory
 #pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    const int j = 2 * jj + wg;                 // block of 32 columns
+                for (int j = wg; j < 4; j += C::WG) {          // block of 32 columns
                     uint32_t pk[16];
                     if (j > quarter) {
 #pragma unroll
@@ -345,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
                             }
                         }
                     }
-                    tmem_st16(tmem + lanes + p_col(j), pk);
+                    tmem_st16(tmem + lanes + C::p_col(j), pk);
                 }
                 tc_wait_st();
                 arrive(r_p);
@@ -359,47 +389,53 @@ __global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
                     make_uint4(lo[j][0], lo[j][1], lo[j][2], lo[j][3]);
             }
             arrive(r_lo);
+            // ---- y = a (Q S) + P V, kept until the stage is free
+            uint32_t o[C::NY / 2];
             if (KIND == FWD) {
-                // ---- y = a (Q S) + P V
                 if (!la_wait(b_pv, ph, abort_flag, limit)) break;
                 tc_fence_after();
-                const int t = c * kLaChunk + row;
-                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + ((size_t)bh * p.T + t) * p.V;
 #pragma unroll
-                for (int j = 0; j < VP / 2; j += 16) {
-                    const int col = wg * (VP / 2) + j;
+                for (int j = 0; j < C::NY; j += 16) {
                     uint32_t pv[16], qs[16];
-                    tmem_ld_32x32b<16>(tmem + lanes + C::kPV + col, pv);
-                    tmem_ld_32x32b<16>(tmem + lanes + C::kQS + col, qs);
+                    tmem_ld<16>(tmem + lanes + C::kPV + wg * C::NY + j, pv);
+                    tmem_ld<16>(tmem + lanes + C::kQS + wg * C::NY + j, qs);
                     tc_wait_ld();
                     reg_fence(pv);
                     reg_fence(qs);
-                    if (t < p.T && col < p.V) {
-                        uint32_t o[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            o[e] = pack_bf16(fmaf(at, __uint_as_float(qs[2 * e]), __uint_as_float(pv[2 * e])),
-                                             fmaf(at, __uint_as_float(qs[2 * e + 1]), __uint_as_float(pv[2 * e + 1])));
-                        *reinterpret_cast<uint4*>(y + col) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4*>(y + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        o[j / 2 + e] = pack_bf16(fmaf(at, __uint_as_float(qs[2 * e]), __uint_as_float(pv[2 * e])),
+                                                 fmaf(at, __uint_as_float(qs[2 * e + 1]), __uint_as_float(pv[2 * e + 1])));
                 }
             }
             // ---- S = A S + the chunk's sum
             if (!la_wait(b_ds2, ph, abort_flag, limit)) break;
             tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < C::NS; j += 16) {
-                uint32_t d[16];
-                tmem_ld_32x32b<16>(tmem + lanes + C::kDS + v0 + j, d);
+            for (int j = 0; j < C::NS; j += C::NL) {
+                uint32_t d[C::NL];
+                if constexpr (KP == 128)
+                    tmem_ld<C::NL>(tmem + lanes + C::kDS + wg * C::NS + j, d);
+                else   // threads 16..31: the same lanes, NS columns on
+                    tmem_ld_16x32bx2<C::NL, C::NS>(tmem + lanes + C::kDS + wg * 2 * C::NS + j, d);
                 tc_wait_ld();
                 reg_fence(d);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) S[j + e] = fmaf(A, S[j + e], __uint_as_float(d[e]));
+                for (int e = 0; e < C::NL; ++e) S[j + e] = fmaf(A, S[j + e], __uint_as_float(d[e]));
             }
             decay *= A;
             if (KIND == FWD) {
-                if (i + 1 < n) write_operand();
+                if (i + 1 < n) {
+                    write_operand();
+                    arrive(r_s);
+                }
+#pragma unroll
+                for (int j = 0; j < C::NY; j += 8) {
+                    const int col = wg * C::NY + j;
+                    *reinterpret_cast<uint4*>(stage + (col >> 6) * kTileBytes + sw128(row, (col & 63) >> 3)) =
+                        make_uint4(o[j / 2], o[j / 2 + 1], o[j / 2 + 2], o[j / 2 + 3]);
+                }
+                arrive(r_y);
             } else {
                 tc_fence_before();   // ordered before the next chunk's r_k arrival
             }
@@ -413,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<KP, VP>::kThreads, Cfg<KP, VP>::kCtas)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == NW) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmem);
     }
@@ -439,14 +475,21 @@ __global__ void m2rnn_la_seg_scan_kernel(const LaParams p, const float* __restri
     }
 }
 
-template <int KP, int VP, Kind KIND>
-cudaError_t launch(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
-    using C = Cfg<KP, VP>;
-    auto kern = m2rnn_la_fwd_tc_kernel<KP, VP, KIND>;
+template <int KP, int VP, int NW, Kind KIND>
+cudaError_t launch_nw(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
+    using C = Cfg<KP, VP, NW>;
+    auto kern = m2rnn_la_fwd_tc_kernel<KP, VP, NW, KIND>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     kern<<<p.B * p.H * p.segs, C::kThreads, C::kSmem, s>>>(p, m, seg_decay);
     return cudaGetLastError();
+}
+template <int KP, int VP, Kind KIND>
+cudaError_t launch(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
+    if constexpr (Cfg<KP, VP, 8>::kCtas == 2) {
+        if ((long long)p.B * p.H * p.segs > kNumSMs) return launch_nw<KP, VP, 8, KIND>(p, m, seg_decay, s);
+    }
+    return launch_nw<KP, VP, 16, KIND>(p, m, seg_decay, s);
 }
 template <Kind KIND>
 cudaError_t launch_shape(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
@@ -482,7 +525,7 @@ size_t la_seg_bytes(const LaPlan& plan, int B, int H, int K, int V) {
 cudaError_t launch_la_fwd_tc(const LaParams& p, cudaStream_t s) {
     Maps m;
     if (!la_tensor_map(&m.q, p.q, p.K, p.T, (size_t)p.B * p.G) || !la_tensor_map(&m.k, p.k, p.K, p.T, (size_t)p.B * p.G) ||
-        !la_tensor_map(&m.v, p.v, p.V, p.T, (size_t)p.B * p.H))
+        !la_tensor_map(&m.v, p.v, p.V, p.T, (size_t)p.B * p.H) || !la_tensor_map(&m.y, p.y, p.V, p.T, (size_t)p.B * p.H))
         return cudaErrorNotSupported;
     if (p.segs > 1) {
         cudaError_t e = launch_shape<SUM>(p, m, decays_of(p), s);

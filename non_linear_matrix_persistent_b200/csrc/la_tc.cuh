@@ -112,6 +112,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
+// Tensor-memory load of N (8, 16 or 32) adjacent columns of this thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+    tmem_ld_32x32b<N>(taddr, r);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -135,6 +141,16 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, i
         "l"(map), "r"(x), "r"(t), "r"(z), "r"(bar)
         : "memory");
 }
+
+// The same box from shared memory; columns and rows outside the tensor are left out.
+__device__ __forceinline__ void tma_store_tile(const CUtensorMap* map, uint32_t src, int x, int t, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+                 "r"(x), "r"(t), "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// The stores committed by this thread have read their shared memory.
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 // ---------------------------------------------------------------- waits
 // Bounded mbarrier wait: false when it runs longer than the limit or another
