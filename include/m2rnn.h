@@ -202,9 +202,10 @@ m2rnn_status m2rnn_backward_noalloc(const m2rnn_dims* d,
  * Tensors are dense and head-first as above: k, q, dk, dq [B][G][T][K];
  * v, y, dy, dv [B][H][T][V]; S0, ST, dST, dS0 [B][H][K][V] fp32; f, df fp32
  * [B][H][T], or [H] with f_per_head (one constant gate per head; df is then
- * the sum over batch and time).  ckpt [B][H][ceil(T/128)][K][V] fp32 holds the
- * states before tokens 0, 128, 256, …: the forward writes it, the backward
- * starts from it (there is no S0 argument: ckpt[.][.][0] is S0).
+ * the sum over batch and time).  ckpt, fp32 [B][H][ceil(T/128)][V/4][K][4],
+ * holds the states before tokens 0, 128, 256, … (element (i, j) of a state at
+ * [j/4][i][j%4]): the forward writes it, the backward starts from it (there is
+ * no S0 argument: the first state is S0).
  * Element types: with mode M2RNN_MODE_BF16_TC k, v, q, dy and the results y,
  * dk, dv, dq are bf16 (unlike the M²RNN recurrence, whose results are fp32:
  * here no later step amplifies a result's rounding, so it is rounded once,
@@ -212,9 +213,8 @@ m2rnn_status m2rnn_backward_noalloc(const m2rnn_dims* d,
  * M2RNN_MODE_FP32_DEBUG everything is fp32 and runs on the CUDA cores.  The
  * other modes are refused.  States, gates and their gradients are fp32.
  *
- * Gates lie in [0, 1].  A gate of exactly 0 discards the state before it.  In
- * the tensor-core kernels a gate below 2^-64 acts as 2^-64 (in the forward, the decay
- * over a stretch that falls to 2^-64 or below is taken as 0).  A state that
+ * Gates lie in [0, 1].  A gate of exactly 0 discards the state before it (in
+ * the tensor-core backward, one below 2^-100 does too).  A state that
  * holds an infinity or NaN is not discarded by a gate of 0 (0·inf = NaN, as in
  * the formula).
  *

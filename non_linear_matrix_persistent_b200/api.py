@@ -293,8 +293,9 @@ def linear_attention(k, v, q, f, S0=None, *, want_ST: bool = True, want_ckpt: bo
     k, q [B, G, T, K] and v [B, H, T, V] (bf16, or fp32 for the debug mode),
     f [B, H, T] fp32 in [0, 1] (or logits, with f_is_logit) or [H], one
     constant for each head; S0 [B, H, K, V] fp32 (None: zeros).  y has the
-    inputs' type, ST [B, H, K, V] is fp32.  ckpt [B, H, ceil(T/128), K, V]
-    holds the states that linear_attention_backward starts from.  `out` may
+    inputs' type, ST [B, H, K, V] is fp32.  ckpt [B, H, ceil(T/128), V/4, K, 4]
+    holds the states that linear_attention_backward starts from (element (i, j)
+    of a state at [j // 4, i, j % 4]).  `out` may
     hold buffers for y, ST and ckpt; ST may be S0's."""
     d = _la_dims(k, v, q, f, f_is_logit)
     dev, lp = k.device, k.dtype
@@ -303,7 +304,7 @@ def linear_attention(k, v, q, f, S0=None, *, want_ST: bool = True, want_ckpt: bo
     out = out or {}
     y = _output(out, "y", (B, H, T, V), lp, dev)
     ST = _output(out, "ST", (B, H, K, V), torch.float32, dev) if want_ST else None
-    ckpt = _output(out, "ckpt", (B, H, num_checkpoints(T, LA_CHUNK), K, V), torch.float32, dev) if want_ckpt else None
+    ckpt = _output(out, "ckpt", (B, H, num_checkpoints(T, LA_CHUNK), V // 4, K, 4), torch.float32, dev) if want_ckpt else None
     L = _lib.lib()
     ws = _scratch(L.m2rnn_linear_attention_workspace(d, 0), dev, "m2rnn_linear_attention_forward")
     _call("m2rnn_linear_attention_forward", dev, L.m2rnn_linear_attention_forward, d, _ptr(k), _ptr(v), _ptr(q),
@@ -339,7 +340,7 @@ def linear_attention_backward(k, v, q, f, ckpt, dy, dST=None, *, f_is_logit: boo
     _check("dST", dST, (B, H, K, V), torch.float32, dev)
     if ckpt is None:
         raise ValueError("linear_attention_backward needs the checkpoints of linear_attention(..., want_ckpt=True)")
-    _check("ckpt", ckpt, (B, H, num_checkpoints(T, LA_CHUNK), K, V), torch.float32, dev)
+    _check("ckpt", ckpt, (B, H, num_checkpoints(T, LA_CHUNK), V // 4, K, 4), torch.float32, dev)
     out = dict(out or {})
     for n, shape, t in (("dk", (B, G, T, K), lp), ("dv", (B, H, T, V), lp), ("dq", (B, G, T, K), lp),
                         ("df", tuple(f.shape), torch.float32), ("dS0", (B, H, K, V), torch.float32)):

@@ -1,0 +1,730 @@
+// Backward of linear attention in chunks of 128 tokens on the tensor cores
+// (bf16), walking from the last chunk to the first.
+//
+// With S the state at the chunk's start (a checkpoint), G = dL/dS at its end,
+// and a, b, D the decays of the forward,
+//   dq_t = a_t (dY Sᵀ)_t + (dP' K)_t          P'  = (Q Kᵀ) ∘ D
+//   dk_s = b_s (V Gᵀ)_s  + (dP'ᵀ Q)_s         dP' = (dY Vᵀ) ∘ D
+//   dv_s = b_s (K G)_s   + (P'ᵀ dY)_s
+//   G'   = a_end G + Σ_t (a_t q_t) dy_tᵀ
+// The scores are computed transposed (lane = source s, column = sink t): P'ᵀ
+// and dP'ᵀ then stay in tensor memory as the A operands of dv and dk, and only
+// dP' also goes to shared memory, for dq.
+//
+// The gate's gradient.  f_u df_u is the sum over all paths from a source
+// s < u (a token, or S) to a sink t >= u (a token, or G):
+//   Σ_{t>=u, s<u} D_ts (q_t·k_s)(dy_t·v_s) + Σ_{t>=u} q_t·(a_t S dy_t)
+//   + Σ_{s<u} k_s·(b_s G v_s) + a_end <S, G>
+// It is summed as it stands (suffix sums over t in registers, sums over s
+// across lanes), never as a difference of running totals: those cancel, and
+// for a gate near 0 the division by f_u would amplify what is left.  Gates
+// below 2^-100 act as 2^-100 there, which keeps that quotient; in every other
+// gradient a path through such a gate is left out.
+//
+// Rounding: P', dP' and the copy of G that gives dv are bf16 operands; S and G
+// enter the products that df also reads, and a_t q_t enters G, as three bf16
+// terms (fp32 accuracy).
+//
+// One CTA per (b, h) or time segment of it.  16 warps compute (thread = token
+// or state row = tensor-memory lane, the four warpgroups sharing the columns),
+// one issues the products, one moves tiles, one computes decays and df.
+#include "kernels.h"
+#include "la_tc.cuh"
+
+namespace m2rnn {
+namespace {
+
+struct BwdMaps {
+    CUtensorMap q, k, v, dy, dq, dk, dv;
+};
+
+template <int KP, int VP>
+struct BCfg {
+    static constexpr int NW = 16, kThreads = (NW + 3) * 32;
+    static constexpr int kQ = KP / 64 * kTileBytes, kV = VP / 64 * kTileBytes, kStage = 2 * kQ + 2 * kV;
+    static constexpr int kStages = KP == 64 && VP == 64 ? 2 : 1;
+    static constexpr int kOp = KP * VP * 2;                     // one bf16 term of a state
+    static constexpr int kOffX = kStages * kStage;              // two terms; the third over dP'
+    static constexpr int kOffP = kOffX + 2 * kOp;               // dP'ᵀ [s][t], 32 KB
+    static constexpr int kOffTab = kOffP + 2 * kTileBytes;
+    static constexpr int kOffBar = kOffTab + (int)sizeof(LaTablesZ);
+    static constexpr int kBars = 18;
+    static constexpr int kSmem = kOffBar + kBars * 8 + 16;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(2 * kOp >= kQ && kOp <= 2 * kTileBytes, "third terms");
+    // tensor memory: the scores, the accumulators.  For K = 128 the sum of dv
+    // starts, over dY·Vᵀ, when the scores have been read, and the state's
+    // gradient goes over dq once that has been read.
+    static constexpr bool kOwnDv = KP == 64;
+    static constexpr int kP = 0, kDP = 128, kDQ = 256, kDK = kDQ + KP, kDV = kOwnDv ? kDK + KP : kDP,
+                         kDG = KP == 128 ? kDQ : VP == 64 ? kDV + VP : kDP;
+    static constexpr int NS = KP * VP / 512;                    // state elements per thread
+    static constexpr int NL = NS < 16 ? NS : 16;
+    static constexpr int NQ = KP / 4, NV = VP / 4;              // columns of dq, dk and of dv per thread
+};
+
+// What the threads leave for df, over the v tile (no longer read by then).
+struct DfScratch {
+    float alpha[4][128], beta[4][128];   // parts of the dot products, by warpgroup
+    float total[4][128];                 // by source: its paths to each block of 32 sinks
+    float cut[4][128];                   // by gate u: paths from each block of sources to sinks u.. of u's block
+    float gamma[16];                     // parts of a_end <S, G>, by warp
+};
+static_assert(sizeof(DfScratch) <= kTileBytes, "scratch");
+
+// Column sums over the 32 lanes of 16 values a lane: lane 2c + {0, 1} gets column c's.
+__device__ __forceinline__ float column_sums(float (&r)[16]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int w = 8; w; w >>= 1) {
+        const int d = 2 * w;
+        const bool up = lane & d;
+#pragma unroll
+        for (int e = 0; e < w; ++e) {
+            const float send = up ? r[e] : r[e + w], keep = up ? r[e + w] : r[e];
+            r[e] = keep + __shfl_xor_sync(~0u, send, d);
+        }
+    }
+    return r[0] + __shfl_xor_sync(~0u, r[0], 1);
+}
+
+template <int KP, int VP>
+__global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
+    m2rnn_la_bwd_tc_kernel(const LaParams p, const __grid_constant__ BwdMaps maps) {
+    using C = BCfg<KP, VP>;
+    constexpr int NW = C::NW;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int bh = blockIdx.x / p.segs, seg = blockIdx.x % p.segs;
+    const int nchunks = (p.T + kLaChunk - 1) / kLaChunk;
+    const int c0 = seg * p.seg_chunks, n = min(nchunks - c0, p.seg_chunks);
+    auto chunk_of = [&](int i) { return c0 + n - 1 - i; };
+    auto stage_of = [&](int i) { return i % C::kStages; };
+    auto stage_phase = [&](int i) { return (uint32_t)(i / C::kStages) & 1u; };
+
+    LaTablesZ* tab = reinterpret_cast<LaTablesZ*>(smem + C::kOffTab);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    const uint32_t b_full = bar(0), r_s = bar(2), b_in = bar(3), r_g = bar(4), b_g = bar(5), r_p = bar(6),
+                   b_dv = bar(7), r_dv = bar(8), b_out = bar(9), r_aq = bar(10), b_dg = bar(11), r_out = bar(12),
+                   b_free = bar(13), b_tab = bar(14), r_df = bar(15), b_drain = bar(16);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint64_t limit = p.wait_limit_ns;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 17; ++i) mbar_init(bar(i), 1);
+        for (uint32_t b : {r_s, r_g, r_p, r_dv, r_aq, r_out}) mbar_init(b, NW);   // one arrival a warp
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == NW) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t sbase = smem_u32(smem);
+
+    if (warp == NW) {
+        // ------------------------------------------------------ products
+        constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, 0, 0),     // scores
+            id_ki = idesc_bf16_f32(128, KP, 0, 0),                     // dY Sᵀ, V Gᵀ
+            id_vi = idesc_bf16_f32(128, VP, 0, 1),                     // K G; P'ᵀ dY
+            id_dq = idesc_bf16_f32(128, KP, 1, 1),                     // dP' K
+            id_dk = idesc_bf16_f32(128, KP, 0, 1),                     // dP'ᵀ Q
+            id_dg = idesc_bf16_f32(KP, VP, 1, 1);                      // (a Q)ᵀ dY
+        const uint64_t d_tile = sw128_desc(sbase, 16), d_mn = sw128_desc(sbase, kTileBytes),
+                       d_op = sw128_desc(sbase, KP * 128);
+        constexpr uint32_t X0 = C::kOffX >> 4, X1 = X0 + (C::kOp >> 4), XP = C::kOffP >> 4;
+        auto kmajor = [](int ks, int rows) { return (uint32_t)((ks >> 2) * (rows * 128 >> 4) + (ks & 3) * 2); };
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int ph = i & 1;
+            const uint32_t q = stage_of(i) * (C::kStage >> 4), k = q + (C::kQ >> 4), v = k + (C::kQ >> 4),
+                           dy = v + (C::kV >> 4);
+            if (!(ok = la_wait(b_full + stage_of(i) * 8, stage_phase(i), abort_flag, limit))) break;
+            if (!(ok = la_wait(r_s, ph, abort_flag, limit))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {       // dY Sᵀ, the terms of S
+                    const uint32_t op = x == 0 ? X0 : x == 1 ? X1 : XP;
+#pragma unroll
+                    for (int ks = 0; ks < VP / 16; ++ks)
+                        tc_mma_f16_ss(tmem + C::kDQ, d_tile + dy + kmajor(ks, 128), d_op + op + kmajor(ks, KP), id_ki,
+                                      x > 0 || ks > 0);
+                }
+                tc_commit(b_in);
+#pragma unroll
+                for (int ks = 0; ks < KP / 16; ++ks)
+                    tc_mma_f16_ss(tmem + C::kP, d_tile + k + kmajor(ks, 128), d_tile + q + kmajor(ks, 128), id_sc, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < VP / 16; ++ks)
+                    tc_mma_f16_ss(tmem + C::kDP, d_tile + v + kmajor(ks, 128), d_tile + dy + kmajor(ks, 128), id_sc,
+                                  ks > 0);
+            }
+            if (!(ok = la_wait(r_g, ph, abort_flag, limit))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {       // V Gᵀ, the terms of G
+                    const uint32_t op = x == 0 ? X0 : x == 1 ? X1 : XP;
+#pragma unroll
+                    for (int ks = 0; ks < VP / 16; ++ks)
+                        tc_mma_f16_ss(tmem + C::kDK, d_tile + v + kmajor(ks, 128), d_op + op + kmajor(ks, KP), id_ki,
+                                      x > 0 || ks > 0);
+                }
+                if (C::kOwnDv) {
+#pragma unroll
+                    for (int ks = 0; ks < KP / 16; ++ks)
+                        tc_mma_f16_ss(tmem + C::kDV, d_tile + k + kmajor(ks, 128), d_op + X0 + ks * 128, id_vi, ks > 0);
+                }
+                tc_commit(b_g);
+            }
+            if (!(ok = la_wait(r_p, ph, abort_flag, limit))) break;
+            tc_fence_after();
+            if (lane == 0) {
+                if (!C::kOwnDv) {
+#pragma unroll
+                    for (int ks = 0; ks < KP / 16; ++ks)
+                        tc_mma_f16_ss(tmem + C::kDV, d_tile + k + kmajor(ks, 128), d_op + X0 + ks * 128, id_vi, ks > 0);
+                    tc_commit(b_dv);
+                }
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)      // contraction over s, the rows of the dP'ᵀ and k tiles
+                    tc_mma_f16_ss(tmem + C::kDQ, d_mn + XP + ks * 128, d_mn + k + ks * 128, id_dq, 1);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)      // over t: dP'ᵀ beside P'ᵀ in each block of 32 score columns
+                    tc_mma_f16_ts(tmem + C::kDK, tmem + C::kP + (ks >> 1) * 32 + 16 + (ks & 1) * 8, d_mn + q + ks * 128,
+                                  id_dk, 1);
+            }
+            if (!C::kOwnDv) {
+                if (!(ok = la_wait(r_dv, ph, abort_flag, limit))) break;
+                tc_fence_after();
+            }
+            if (lane == 0) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    tc_mma_f16_ts(tmem + C::kDV, tmem + C::kP + (ks >> 1) * 32 + (ks & 1) * 8, d_mn + dy + ks * 128, id_vi,
+                                  1);
+                tc_commit(b_out);
+            }
+            if (!(ok = la_wait(r_aq, ph, abort_flag, limit))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {       // the terms of a q: over the q tile, the k tile, the states' terms
+                    const uint32_t op = x == 0 ? q : x == 1 ? k : X0;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc_mma_f16_ss(tmem + C::kDG, d_mn + op + ks * 128, d_mn + dy + ks * 128, id_dg, x > 0 || ks > 0);
+                }
+                tc_commit(b_dg);
+            }
+        }
+        if (lane == 0) {   // nothing is in flight when the CTA ends
+            tc_commit(b_drain);
+            la_drain(b_drain, 0, limit);
+        }
+        __syncwarp();
+    } else if (warp == NW + 1) {
+        // ------------------------------------------------------ copies
+        if (lane == 0) {
+            const int qk = la_qk_pair(p, bh);
+            int loaded = 0;
+            auto load = [&](int i) {
+                if (p.fault == 1 && i > 0) return;   // injected: the copies stop after the first chunk
+                loaded = i + 1;
+                const int t = chunk_of(i) * kLaChunk;
+                const uint32_t base = sbase + stage_of(i) * C::kStage, full = b_full + stage_of(i) * 8;
+                mbar_arrive_expect_tx(full, C::kStage);
+#pragma unroll
+                for (int x = 0; x < VP / 64; ++x)
+                    tma_tile(base + 2 * C::kQ + C::kV + x * kTileBytes, &maps.dy, x * 64, t, bh, full);
+#pragma unroll
+                for (int x = 0; x < KP / 64; ++x) {
+                    tma_tile(base + x * kTileBytes, &maps.q, x * 64, t, qk, full);
+                    tma_tile(base + C::kQ + x * kTileBytes, &maps.k, x * 64, t, qk, full);
+                }
+#pragma unroll
+                for (int x = 0; x < VP / 64; ++x)
+                    tma_tile(base + 2 * C::kQ + x * kTileBytes, &maps.v, x * 64, t, bh, full);
+            };
+            for (int i = 0; i < C::kStages && i < n; ++i) load(i);
+            bool ok = true;
+            int i = 0;
+            for (; i < n; ++i) {
+                const int ph = i & 1, t = chunk_of(i) * kLaChunk;
+                const uint32_t base = sbase + stage_of(i) * C::kStage;
+                if (!(ok = la_wait(r_out, ph, abort_flag, limit))) break;
+                if (!p.dkq_fp32)
+                    for (int x = 0; x < KP / 64; ++x)
+                        if (x * 64 < p.K) {
+                            tma_store_tile(&maps.dq, sbase + C::kOffP + x * kTileBytes, x * 64, t, bh);
+                            tma_store_tile(&maps.dk, base + x * kTileBytes, x * 64, t, bh);
+                        }
+                for (int x = 0; x < VP / 64; ++x)
+                    if (x * 64 < p.V)
+                        tma_store_tile(&maps.dv, base + 2 * C::kQ + C::kV + x * kTileBytes, x * 64, t, bh);
+                tma_store_commit();
+                tma_store_wait_read();
+                mbar_arrive(b_free);
+                if (!(ok = la_wait(r_df, ph, abort_flag, limit))) break;
+                if (i + C::kStages < n) load(i + C::kStages);
+            }
+            if (!ok)   // leave no copy in flight
+                for (int j = i; j < loaded; ++j) la_drain(b_full + stage_of(j) * 8, stage_phase(j), limit);
+        }
+        __syncwarp();
+    } else if (warp == NW + 2) {
+        // ------------------------------------------------------ decays and df: four tokens a lane
+        float fx[4], fnext[4];
+        la_load_f(p, bh, chunk_of(0), fx);
+        if (n > 1) la_load_f(p, bh, chunk_of(1), fnext);
+        la_tables<true>(tab, p, fx, p.T - chunk_of(0) * kLaChunk, kLogFloorBwd);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_tab);
+        for (int i = 0; i < n; ++i) {
+            const int ph = i & 1, c = chunk_of(i);
+            if (!la_wait(r_p, ph, abort_flag, limit)) break;
+            const DfScratch* sc = reinterpret_cast<const DfScratch*>(smem + stage_of(i) * C::kStage + 2 * C::kQ);
+            const int block = lane >> 3, t0 = lane * 4;
+            float x[4] = {0.f, 0.f, 0.f, 0.f}, al[4], be[4], past[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                al[e] = be[e] = 0.f;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    al[e] += sc->alpha[g][t0 + e];
+                    be[e] += sc->beta[g][t0 + e];
+                    x[e] += g <= block ? sc->cut[g][t0 + e] : 0.f;
+                }
+                // this source's paths to sinks beyond block J
+                past[2][e] = sc->total[3][t0 + e];
+                past[1][e] = past[2][e] + sc->total[2][t0 + e];
+                past[0][e] = past[1][e] + sc->total[1][t0 + e];
+            }
+            float gamma = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) gamma += sc->gamma[w];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(r_df);
+            // sums over sources before each token of this lane (exclusive)
+            auto before = [&](const float (&v)[4], float (&o)[4]) {
+                float s[4] = {v[0], v[0] + v[1], v[0] + v[1] + v[2], v[0] + v[1] + v[2] + v[3]};
+                float run = s[3];
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const float y = __shfl_up_sync(~0u, run, d);
+                    if (lane >= d) run += y;
+                }
+                const float pre = __shfl_up_sync(~0u, run, 1);
+                o[0] = lane ? pre : 0.f;
+#pragma unroll
+                for (int e = 1; e < 4; ++e) o[e] = o[0] + s[e - 1];
+            };
+            float o[4];
+            before(be, o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] += o[e] + gamma;
+#pragma unroll
+            for (int J = 0; J < 3; ++J) {
+                before(past[J], o);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] += block == J ? o[e] : 0.f;
+            }
+            // sums over sinks from each token on (inclusive)
+            float s[4] = {al[0] + al[1] + al[2] + al[3], al[1] + al[2] + al[3], al[2] + al[3], al[3]}, run = s[0];
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const float y = __shfl_down_sync(~0u, run, d);
+                if (lane + d < 32) run += y;
+            }
+            float post = __shfl_down_sync(~0u, run, 1);
+            post = lane < 31 ? post : 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] += s[e] + post;
+                const int t = c * kLaChunk + t0 + e;
+                if (t < p.T) {
+                    // x = f df: the gate's gradient, or the logit's, df f (1 - f) with 1 - f = 1/(1 + e^a)
+                    // (a gate at the floor: df times the gate itself)
+                    const float f = la_gate(p, fx[e]), g = f < kGateFloorBwd ? kGateFloorBwd : f;
+                    p.df[(size_t)bh * p.T + t] =
+                        !p.f_is_logit ? x[e] / g : x[e] * (f < kGateFloorBwd ? f / g : 1.f) / (1.f + expf(fx[e]));
+                }
+            }
+            if (i + 1 < n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) fx[e] = fnext[e];
+                if (i + 2 < n) la_load_f(p, bh, chunk_of(i + 2), fnext);
+                la_tables<true>(tab, p, fx, p.T - chunk_of(i + 1) * kLaChunk, kLogFloorBwd);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_tab);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ elementwise work
+        const int wg = warp >> 2, quarter = warp & 3;
+        const int row = quarter * 32 + lane;                     // token of the chunk
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;   // tensor-memory lane base
+        const uint32_t mylane = tmem + lanes;
+        // this thread's part of S and G: row kap, columns [v0, v0 + NS)
+        const int kap = KP == 128 ? row : quarter * 16 + (lane & 15);
+        const int v0 = KP == 128 ? wg * C::NS : (wg * 2 + (lane >> 4)) * C::NS;
+        const bool mine = kap < p.K;
+        float G[C::NS];
+        {
+            const float* src = p.segs > 1 ? p.seg_state + ((size_t)bh * p.segs + seg) * p.K * p.V
+                               : p.dST    ? p.dST + (size_t)bh * p.K * p.V
+                                          : nullptr;
+#pragma unroll
+            for (int j = 0; j < C::NS; j += 4) {
+                const float4 x = src && mine && v0 + j < p.V
+                                     ? *reinterpret_cast<const float4*>(src + (size_t)kap * p.V + v0 + j)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                G[j] = x.x; G[j + 1] = x.y; G[j + 2] = x.z; G[j + 3] = x.w;
+            }
+        }
+        auto arrive = [&](uint32_t b) {   // this warp's writes are done: shared memory for the products, tensor memory
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b);
+        };
+        // three bf16 terms of a state's elements j..j+7 into the operand slots
+        auto put_terms = [&](const float (&x)[8], int j) {
+            uint4 hi, mid, lo;
+            split3(x[0], x[1], hi.x, mid.x, lo.x);
+            split3(x[2], x[3], hi.y, mid.y, lo.y);
+            split3(x[4], x[5], hi.z, mid.z, lo.z);
+            split3(x[6], x[7], hi.w, mid.w, lo.w);
+            const uint32_t at = (v0 >> 6) * (KP * 128) + sw128(kap, ((v0 & 63) + j) >> 3);
+            *reinterpret_cast<uint4*>(smem + C::kOffX + at) = hi;
+            *reinterpret_cast<uint4*>(smem + C::kOffX + C::kOp + at) = mid;
+            *reinterpret_cast<uint4*>(smem + C::kOffP + at) = lo;
+        };
+        auto tile_at = [&](int col) { return (col >> 6) * kTileBytes + sw128(row, (col & 63) >> 3); };
+
+        for (int i = 0; i < n; ++i) {
+            const int ph = i & 1, c = chunk_of(i);
+            uint8_t* stage = smem + stage_of(i) * C::kStage;
+            // ---- S: its terms, and this thread's part of <S, G>
+            if (i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
+            float gamma = 0.f;
+            {
+                const float* ck = p.ckpt + ((size_t)bh * nchunks + c) * p.K * p.V;
+#pragma unroll
+                for (int j = 0; j < C::NS; j += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int h = 0; h < 8; h += 4) {
+                        const float4 s4 = mine && v0 + j + h < p.V
+                                              ? *reinterpret_cast<const float4*>(ck + ((size_t)((v0 + j + h) >> 2) * p.K + kap) * 4)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x[h] = s4.x; x[h + 1] = s4.y; x[h + 2] = s4.z; x[h + 3] = s4.w;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) gamma = fmaf(x[e], G[j + e], gamma);
+                    put_terms(x, j);
+                }
+            }
+            arrive(r_s);
+            if (!la_wait(b_tab, ph, abort_flag, limit)) break;
+            const float Ft = tab->F[row], It = tab->I[row], Fe = tab->F[127], Ie = tab->I[127];
+            const float Zt = tab->Z[row], Ze = tab->Z[127];
+            // decays for df, and for everything else (paths through gates at the floor left out)
+            const float at0 = ex2_approx(Ft + It), bt0 = ex2_approx((Fe - Ft) + (Ie - It)), A0 = ex2_approx(Fe + Ie);
+            const float at = Zt != 0.f ? 0.f : at0, bt = Zt != Ze ? 0.f : bt0, A = Ze != 0.f ? 0.f : A0;
+            gamma *= A0;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) gamma += __shfl_xor_sync(~0u, gamma, d);
+            if (!la_wait(b_full + stage_of(i) * 8, stage_phase(i), abort_flag, limit)) break;
+            if (!la_wait(b_in, ph, abort_flag, limit)) break;
+            tc_fence_after();
+            // ---- G: its terms, over those of S
+#pragma unroll
+            for (int j = 0; j < C::NS; j += 8) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = G[j + e];
+                put_terms(x, j);
+            }
+            arrive(r_g);
+            // ---- a_t (S dy_t) and b_s (G v_s) in place, and their dot products with q and k
+            auto scale_rows = [&](uint32_t col0, float w0, float w, const uint8_t* tile) {
+                float dot = 0.f;
+#pragma unroll
+                for (int j = 0; j < C::NQ; j += 16) {
+                    const int col = wg * C::NQ + j;
+                    uint32_t x[16];
+                    tmem_ld<16>(mylane + col0 + col, x);
+                    const uint4 y0 = *reinterpret_cast<const uint4*>(tile + tile_at(col)),
+                                y1 = *reinterpret_cast<const uint4*>(tile + tile_at(col + 8));
+                    const uint32_t y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+                    tc_wait_ld();
+                    reg_fence(x);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float s = __uint_as_float(x[e]);
+                        dot = fmaf(s, e & 1 ? bf16hi_to_f32(y[e / 2]) : bf16lo_to_f32(y[e / 2]), dot);
+                        x[e] = __float_as_uint(w * s);
+                    }
+                    tmem_st16(mylane + col0 + col, x);
+                }
+                return w0 * dot;
+            };
+            auto scale_dv = [&]() {
+#pragma unroll
+                for (int j = 0; j < C::NV; j += 16) {
+                    const int col = wg * C::NV + j;
+                    uint32_t x[16];
+                    tmem_ld<16>(mylane + C::kDV + col, x);
+                    tc_wait_ld();
+                    reg_fence(x);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(bt * __uint_as_float(x[e]));
+                    tmem_st16(mylane + C::kDV + col, x);
+                }
+            };
+            const float alpha = scale_rows(C::kDQ, at0, at, stage);
+            if (!la_wait(b_g, ph, abort_flag, limit)) break;
+            tc_fence_after();
+            const float beta = scale_rows(C::kDK, bt0, bt, stage + C::kQ);
+            if (C::kOwnDv) scale_dv();
+            // every product that reads the v tile and the states' third terms is done
+            DfScratch* sc = reinterpret_cast<DfScratch*>(stage + 2 * C::kQ);
+            sc->alpha[wg][row] = alpha;
+            sc->beta[wg][row] = beta;
+            if (lane == 0) sc->gamma[warp] = gamma;
+            // ---- P'ᵀ, dP'ᵀ and df's sums: source s = row, sinks of block wg
+            uint8_t* dp = smem + C::kOffP;
+            float run = 0.f;
+            if (wg < quarter) {   // sinks before the source
+                const uint32_t z[16] = {};
+                tmem_st16(mylane + C::kP + wg * 32, z);
+                tmem_st16(mylane + C::kP + wg * 32 + 16, z);
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(dp + tile_at(wg * 32 + e)) = make_uint4(0, 0, 0, 0);
+            } else {
+                const bool diag = wg == quarter;
+                const float r = diag ? 1.f : ex2_approx((tab->F[wg * 32 - 1] - Ft) + (tab->I[wg * 32 - 1] - It));
+                uint32_t pp[16], pd[16];
+#pragma unroll
+                for (int h = 16; h >= 0; h -= 16) {
+                    uint32_t x[16], y[16];
+                    tmem_ld<16>(mylane + C::kP + wg * 32 + h, x);
+                    tmem_ld<16>(mylane + C::kDP + wg * 32 + h, y);
+                    tc_wait_ld();
+                    reg_fence(x);
+                    reg_fence(y);
+                    float R[16];
+#pragma unroll
+                    for (int e = 12; e >= 0; e -= 4) {
+                        float d[4];
+                        if (diag) {
+                            const float4 fs = *reinterpret_cast<const float4*>(&tab->F[wg * 32 + h + e]);
+                            const float4 is = *reinterpret_cast<const float4*>(&tab->I[wg * 32 + h + e]);
+                            const float f4[4] = {fs.x, fs.y, fs.z, fs.w}, i4[4] = {is.x, is.y, is.z, is.w};
+#pragma unroll
+                            for (int o = 0; o < 4; ++o)
+                                d[o] = h + e + o >= lane ? ex2_approx((f4[o] - Ft) + (i4[o] - It)) : 0.f;
+                        } else {
+                            const float4 cs = *reinterpret_cast<const float4*>(&tab->c[wg * 32 + h + e]);
+                            d[0] = r * cs.x; d[1] = r * cs.y; d[2] = r * cs.z; d[3] = r * cs.w;
+                        }
+#pragma unroll
+                        for (int o = 3; o >= 0; --o) {
+                            const float P = __uint_as_float(x[e + o]), Q = __uint_as_float(y[e + o]);
+                            run = fmaf(P * d[o], Q, run);
+                            R[e + o] = !diag || h + e + o > lane ? run : 0.f;   // sources strictly before the gate
+                        }
+                        if (Ze != 0.f) {
+                            const float4 zs = *reinterpret_cast<const float4*>(&tab->Z[wg * 32 + h + e]);
+                            d[0] = zs.x != Zt ? 0.f : d[0]; d[1] = zs.y != Zt ? 0.f : d[1];
+                            d[2] = zs.z != Zt ? 0.f : d[2]; d[3] = zs.w != Zt ? 0.f : d[3];
+                        }
+#pragma unroll
+                        for (int o = 0; o < 4; ++o) {
+                            x[e + o] = __float_as_uint(__uint_as_float(x[e + o]) * d[o]);
+                            y[e + o] = __float_as_uint(__uint_as_float(y[e + o]) * d[o]);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        pp[(h + e) / 2] = pack_bf16(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                        pd[(h + e) / 2] = pack_bf16(__uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+                    }
+                    const float cut = column_sums(R);
+                    if (!(lane & 1)) sc->cut[quarter][wg * 32 + h + (lane >> 1)] = cut;
+                }
+                tmem_st16(mylane + C::kP + wg * 32, pp);
+                tmem_st16(mylane + C::kP + wg * 32 + 16, pd);
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                    *reinterpret_cast<uint4*>(dp + tile_at(wg * 32 + e)) =
+                        make_uint4(pd[e / 2], pd[e / 2 + 1], pd[e / 2 + 2], pd[e / 2 + 3]);
+            }
+            sc->total[wg][row] = run;
+            tc_wait_st();
+            arrive(r_p);
+            if (!C::kOwnDv) {
+                if (!la_wait(b_dv, ph, abort_flag, limit)) break;
+                tc_fence_after();
+                scale_dv();
+                tc_wait_st();
+                arrive(r_dv);
+            }
+            if (!la_wait(b_out, ph, abort_flag, limit)) break;
+            tc_fence_after();
+            const int t = c * kLaChunk + row;
+            // ---- dq, over dP'
+            auto rows_out = [&](uint32_t col0, void* out, uint32_t (&o)[C::NQ / 2]) {
+#pragma unroll
+                for (int j = 0; j < C::NQ; j += 16) {
+                    const int col = wg * C::NQ + j;
+                    uint32_t x[16];
+                    tmem_ld<16>(mylane + col0 + col, x);
+                    tc_wait_ld();
+                    reg_fence(x);
+                    if (p.dkq_fp32 && t < p.T && col < p.K) {   // per-head parts of a shared q's or k's gradient
+                        uint4* g = reinterpret_cast<uint4*>(static_cast<float*>(out) + ((size_t)bh * p.T + t) * p.K + col);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) g[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        o[j / 2 + e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                }
+            };
+            {
+                uint32_t o[C::NQ / 2];
+                rows_out(C::kDQ, p.dq, o);
+#pragma unroll
+                for (int j = 0; j < C::NQ; j += 8)
+                    *reinterpret_cast<uint4*>(dp + tile_at(wg * C::NQ + j)) =
+                        make_uint4(o[j / 2], o[j / 2 + 1], o[j / 2 + 2], o[j / 2 + 3]);
+            }
+            // ---- a_t q_t in three terms: over q, over k, over the states' terms
+#pragma unroll
+            for (int j = 0; j < C::NQ; j += 8) {
+                const uint32_t pos = tile_at(wg * C::NQ + j);
+                const uint4 x = *reinterpret_cast<const uint4*>(stage + pos);
+                uint4 hi, mid, lo;
+                split3(at * bf16lo_to_f32(x.x), at * bf16hi_to_f32(x.x), hi.x, mid.x, lo.x);
+                split3(at * bf16lo_to_f32(x.y), at * bf16hi_to_f32(x.y), hi.y, mid.y, lo.y);
+                split3(at * bf16lo_to_f32(x.z), at * bf16hi_to_f32(x.z), hi.z, mid.z, lo.z);
+                split3(at * bf16lo_to_f32(x.w), at * bf16hi_to_f32(x.w), hi.w, mid.w, lo.w);
+                *reinterpret_cast<uint4*>(stage + pos) = hi;
+                *reinterpret_cast<uint4*>(stage + C::kQ + pos) = mid;
+                *reinterpret_cast<uint4*>(smem + C::kOffX + pos) = lo;
+            }
+            arrive(r_aq);
+            // ---- dk and dv, kept until their tiles are free
+            uint32_t ok_[C::NQ / 2], ov[C::NV / 2];
+            rows_out(C::kDK, p.dk, ok_);
+#pragma unroll
+            for (int j = 0; j < C::NV; j += 16) {
+                uint32_t x[16];
+                tmem_ld<16>(mylane + C::kDV + wg * C::NV + j, x);
+                tc_wait_ld();
+                reg_fence(x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    ov[j / 2 + e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+            }
+            // ---- G = A G + the chunk's sum
+            if (!la_wait(b_dg, ph, abort_flag, limit)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < C::NS; j += C::NL) {
+                uint32_t d[C::NL];
+                if constexpr (KP == 128)
+                    tmem_ld<C::NL>(mylane + C::kDG + wg * C::NS + j, d);
+                else   // threads 16..31: the same lanes, NS columns on
+                    tmem_ld_16x32bx2<C::NL, C::NS>(mylane + C::kDG + wg * 2 * C::NS + j, d);
+                tc_wait_ld();
+                reg_fence(d);
+#pragma unroll
+                for (int e = 0; e < C::NL; ++e) G[j + e] = fmaf(A, G[j + e], __uint_as_float(d[e]));
+            }
+            if (!p.dkq_fp32) {
+#pragma unroll
+                for (int j = 0; j < C::NQ; j += 8)
+                    *reinterpret_cast<uint4*>(stage + tile_at(wg * C::NQ + j)) =
+                        make_uint4(ok_[j / 2], ok_[j / 2 + 1], ok_[j / 2 + 2], ok_[j / 2 + 3]);
+            }
+#pragma unroll
+            for (int j = 0; j < C::NV; j += 8)
+                *reinterpret_cast<uint4*>(stage + 2 * C::kQ + C::kV + tile_at(wg * C::NV + j)) =
+                    make_uint4(ov[j / 2], ov[j / 2 + 1], ov[j / 2 + 2], ov[j / 2 + 3]);
+            arrive(r_out);
+        }
+        if (c0 == 0 && mine) {
+#pragma unroll
+            for (int j = 0; j < C::NS; j += 4)
+                if (v0 + j < p.V)
+                    *reinterpret_cast<float4*>(p.dS0 + (size_t)bh * p.K * p.V + (size_t)kap * p.V + v0 + j) =
+                        make_float4(G[j], G[j + 1], G[j + 2], G[j + 3]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == NW) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int KP, int VP>
+cudaError_t launch(const LaParams& p, const BwdMaps& m, cudaStream_t s) {
+    using C = BCfg<KP, VP>;
+    auto kern = m2rnn_la_bwd_tc_kernel<KP, VP>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<p.B * p.H * p.segs, C::kThreads, C::kSmem, s>>>(p, m);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+LaPlan la_bwd_plan(int B, int H, int T, int, int) {
+    const int chunks = (T + kLaChunk - 1) / kLaChunk;
+    const long long pairs = (long long)B * H;
+    long long segs = 1;
+    if (pairs * 2 <= kNumSMs && chunks >= 4) segs = kNumSMs / pairs;
+#ifdef LA_TUNE
+    if (const char* e = getenv("LA_BSEGS")) segs = atoi(e);
+#endif
+    if (segs > chunks / 2) segs = chunks / 2;
+    if (segs < 1) segs = 1;
+    const int per = (int)((chunks + segs - 1) / segs);
+    return {(chunks + per - 1) / per, per};
+}
+
+cudaError_t launch_la_bwd_tc(const LaParams& p, cudaStream_t s) {
+    const size_t qk = (size_t)p.B * p.G, vy = (size_t)p.B * p.H;
+    BwdMaps m;
+    if (!la_tensor_map(&m.q, p.q, p.K, p.T, qk) || !la_tensor_map(&m.k, p.k, p.K, p.T, qk) ||
+        !la_tensor_map(&m.v, p.v, p.V, p.T, vy) || !la_tensor_map(&m.dy, p.dy, p.V, p.T, vy) ||
+        !la_tensor_map(&m.dv, p.dv, p.V, p.T, vy))
+        return cudaErrorNotSupported;
+    m.dq = m.dk = m.dv;   // not used for per-head parts
+    if (!p.dkq_fp32 && (!la_tensor_map(&m.dq, p.dq, p.K, p.T, vy) || !la_tensor_map(&m.dk, p.dk, p.K, p.T, vy)))
+        return cudaErrorNotSupported;
+    if (p.segs > 1) {
+        const cudaError_t e = launch_la_seg_grads(p, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.K <= 64) return p.V <= 64 ? launch<64, 64>(p, m, s) : launch<64, 128>(p, m, s);
+    return p.V <= 64 ? launch<128, 64>(p, m, s) : launch<128, 128>(p, m, s);
+}
+
+// Reads and clears the status word of this file's kernels.
+cudaError_t la_bwd_tc_status(unsigned* word, cudaStream_t s) { return la_read_status(word, s); }
+
+}  // namespace m2rnn

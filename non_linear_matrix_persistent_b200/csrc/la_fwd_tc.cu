@@ -218,11 +218,10 @@ __global__ void __launch_bounds__(Cfg<KP, VP, NW>::kThreads, Cfg<KP, VP, NW>::kC
             load(0);
             if (n > 1) load(1);
         }
-        const float floor_ = KIND == RSUM ? kLogFloorBwd : kLogFloorFwd;
         float fx[4], fnext[4];
         la_load_f(p, bh, chunk_of(0), fx);
         la_load_f(p, bh, n > 1 ? chunk_of(1) : chunk_of(0), fnext);
-        la_tables(tab, p, fx, p.T - chunk_of(0) * kLaChunk, floor_);
+        la_tables(tab, p, fx, p.T - chunk_of(0) * kLaChunk, kLogFloorFwd);
         __syncwarp();
         if (lane == 0) mbar_arrive(b_tab);
         bool ok = true;
@@ -234,7 +233,7 @@ __global__ void __launch_bounds__(Cfg<KP, VP, NW>::kThreads, Cfg<KP, VP, NW>::kC
                 for (int e = 0; e < 4; ++e) fx[e] = fnext[e];
                 if (i + 2 < n) la_load_f(p, bh, chunk_of(i + 2), fnext);
                 if (!(ok = la_wait(KIND == FWD ? r_p : r_k, ph, abort_flag, limit))) break;
-                la_tables(tab, p, fx, p.T - chunk_of(i + 1) * kLaChunk, floor_);
+                la_tables(tab, p, fx, p.T - chunk_of(i + 1) * kLaChunk, kLogFloorFwd);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_tab);
             }
@@ -312,7 +311,14 @@ __global__ void __launch_bounds__(Cfg<KP, VP, NW>::kThreads, Cfg<KP, VP, NW>::kC
         for (int i = 0; i < n; ++i) {
             const int s = i & 1, ph = i & 1, c = chunk_of(i);
             uint8_t* stage = smem + s * C::kStage;
-            if (KIND == FWD && p.ckpt) store_state(p.ckpt + ((size_t)bh * nchunks + c) * p.K * p.V);
+            if (KIND == FWD && p.ckpt && mine) {   // [V/4][K][4]: a warp's rows are adjacent
+                float* ck = p.ckpt + ((size_t)bh * nchunks + c) * p.K * p.V;
+#pragma unroll
+                for (int j = 0; j < C::NS; j += 4)
+                    if (v0 + j < p.V)
+                        *reinterpret_cast<float4*>(ck + ((size_t)((v0 + j) >> 2) * p.K + kap) * 4) =
+                            make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+            }
             if (!la_wait(b_tab, ph, abort_flag, limit)) break;
             const float Ft = tab->F[row], It = tab->I[row], Fe = tab->F[127], Ie = tab->I[127];
             const float at = ex2_approx(Ft + It), A = ex2_approx(Fe + Ie);
@@ -508,7 +514,7 @@ LaPlan la_fwd_plan(int B, int H, int T, int K, int V) {
     const int chunks = (T + kLaChunk - 1) / kLaChunk, per_sm = K <= 64 && V <= 64 ? 2 : 1;
     const long long pairs = (long long)B * H, slots = (long long)kNumSMs * per_sm;
     long long segs = 1;
-    if (pairs * 2 <= slots && chunks >= 4) segs = slots / pairs;
+    if (pairs * 2 <= kNumSMs && chunks >= 4) segs = slots / pairs;
 #ifdef LA_TUNE
     if (const char* e = getenv("LA_SEGS")) segs = atoi(e);
 #endif
@@ -538,16 +544,22 @@ cudaError_t launch_la_fwd_tc(const LaParams& p, cudaStream_t s) {
     return launch_shape<FWD>(p, m, nullptr, s);
 }
 
-// Reads and clears the status word of this file's kernels.
-cudaError_t la_fwd_tc_status(unsigned* word, cudaStream_t s) {
-    const unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_la_status, sizeof *word, 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess && *word) {
-        e = cudaMemcpyToSymbolAsync(g_la_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
+// The same sums for the gradient: what a segment's tokens add to dL/dS at its
+// start, then dL/dS at every segment's end.
+cudaError_t launch_la_seg_grads(const LaParams& p, cudaStream_t s) {
+    Maps m;
+    if (!la_tensor_map(&m.k, p.q, p.K, p.T, (size_t)p.B * p.G) || !la_tensor_map(&m.v, p.dy, p.V, p.T, (size_t)p.B * p.H))
+        return cudaErrorNotSupported;
+    m.q = m.k;
+    m.y = m.v;
+    cudaError_t e = launch_shape<RSUM>(p, m, decays_of(p), s);
+    if (e != cudaSuccess) return e;
+    const size_t n = (size_t)p.B * p.H * p.K * p.V / 4;
+    m2rnn_la_seg_scan_kernel<<<(unsigned)((n + 127) / 128), 128, 0, s>>>(p, decays_of(p), p.dST, 1);
+    return cudaGetLastError();
 }
+
+// Reads and clears the status word of this file's kernels.
+cudaError_t la_fwd_tc_status(unsigned* word, cudaStream_t s) { return la_read_status(word, s); }
 
 }  // namespace m2rnn

@@ -50,9 +50,9 @@ __global__ void __launch_bounds__(RecCfg<IO, K, VS>::kThreads) m2rnn_la_rec_kern
     const int nck = (p.T + kLaChunk - 1) / kLaChunk;
     for (int t = 0; t < p.T; ++t) {
         if (p.ckpt && t % kLaChunk == 0) {
-            float* ck = p.ckpt + ((size_t)bh * nck + t / kLaChunk) * K * p.V + (size_t)grp * p.V + col;
+            float* ck = p.ckpt + ((size_t)bh * nck + t / kLaChunk) * K * p.V + ((size_t)(col >> 2) * K + grp) * 4;
 #pragma unroll
-            for (int r = 0; r < C::R; ++r) *reinterpret_cast<float4*>(ck + (size_t)r * C::kGroups * p.V) = S[r];
+            for (int r = 0; r < C::R; ++r) *reinterpret_cast<float4*>(ck + r * C::kGroups * 4) = S[r];
         }
         const float f = la_gate(p, la_f_input(p, bh, t));
         float vv[4];
@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(kBwdThreads) m2rnn_la_bwd_simt_kernel(const La
         __syncthreads();
         // S at the block's start: the checkpoint advanced token by token
         for (int i = tid; i < K * V; i += kBwdThreads) {
-            float s = p.ckpt[((size_t)bh * nck + c) * K * V + i];
             const int row = i / V, colv = i % V;
+            float s = p.ckpt[((size_t)bh * nck + c) * K * V + ((colv >> 2) * K + row) * 4 + (colv & 3)];
             for (int t = c * kLaChunk; t < t0; ++t)
                 s = fmaf(la_gate(p, la_f_input(p, bh, t)), s,
                          la_to_f32(static_cast<const IO*>(p.k)[qk0 + (size_t)t * K + row]) *

@@ -25,9 +25,10 @@ static __device__ unsigned g_la_status;
 
 // Floor of a gate's base-2 logarithm.  Forward: 2^-256, which every product of
 // decays flushes to 0, so a gate of 0 (or below 2^-126) discards the state.
-// Backward: 2^-64, so that the sums over paths through a gate of 0, divided by
-// the gate again, still give its gradient.
-constexpr float kLogFloorFwd = -256.f, kLogFloorBwd = -64.f;
+// Backward: 2^-100, so that the sums over paths through a gate of 0, divided
+// by the gate again, still give its gradient; the other gradients leave such
+// paths out (LaTables::Z).
+constexpr float kLogFloorFwd = -256.f, kLogFloorBwd = -100.f, kGateFloorBwd = 7.888609052210118e-31f;
 
 // log2 of a gate split into an integer and a fraction in [-1/2, 1/2]: sums of
 // the integers are exact, so differences of cumulative sums keep their
@@ -41,17 +42,23 @@ __device__ __forceinline__ void la_log2(const LaParams& p, float x, float floor_
 
 // Cumulative log-decays of a chunk's 128 tokens, from the chunk's start
 // through the token, by one warp (4 tokens a lane): F + I in shared memory,
-// and c[s] = the decay from s to the last token of its block of 32.
+// and c[t] = the decay from t to the last token of its block of 32 or, with
+// FROM_PREV, from the last token of the block before through t.
 struct LaTables {
     float F[128], I[128], c[128];
 };
-__device__ __forceinline__ void la_tables(LaTables* tab, const LaParams& p, const float (&x)[4], int valid, float floor_) {
+struct LaTablesZ : LaTables {
+    float Z[128];   // gates at the floor, from the chunk's start through the token
+};
+template <bool FROM_PREV = false, class Tab = LaTables>
+__device__ __forceinline__ void la_tables(Tab* tab, const LaParams& p, const float (&x)[4], int valid, float floor_) {
     const int lane = threadIdx.x & 31;
-    float F[4], I[4];
+    float F[4], I[4], Z[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         la_log2(p, x[i], floor_, I[i], F[i]);
         if (lane * 4 + i >= valid) { F[i] = 0.f; I[i] = 0.f; }   // behind the last token: a gate of 1
+        Z[i] = (I[i] + F[i] <= floor_ ? 1.f : 0.f) + (i > 0 ? Z[i > 0 ? i - 1 : 0] : 0.f);
         if (i > 0) { F[i] += F[i - 1]; I[i] += I[i - 1]; }
     }
     float f = F[3], w = I[3];
@@ -66,12 +73,29 @@ __device__ __forceinline__ void la_tables(LaTables* tab, const LaParams& p, cons
         F[i] += lane ? f0 : 0.f;
         I[i] += lane ? w0 : 0.f;
     }
-    const float fe = __shfl_sync(~0u, F[3], lane | 7), we = __shfl_sync(~0u, I[3], lane | 7);   // the block's last token
+    if constexpr (FROM_PREV) {
+        float z = Z[3];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const float a = __shfl_up_sync(~0u, z, d);
+            if (lane >= d) z += a;
+        }
+        z -= Z[3];
+        *reinterpret_cast<float4*>(&tab->Z[lane * 4]) = make_float4(z + Z[0], z + Z[1], z + Z[2], z + Z[3]);
+    }
+    // the block's last token, or the one before the block
+    float fe = __shfl_sync(~0u, F[3], FROM_PREV ? (lane & ~7) - 1 : lane | 7),
+          we = __shfl_sync(~0u, I[3], FROM_PREV ? (lane & ~7) - 1 : lane | 7);
+    float sign = 1.f;
+    if (FROM_PREV) {
+        if (lane < 8) { fe = 0.f; we = 0.f; }
+        sign = -1.f;
+    }
     *reinterpret_cast<float4*>(&tab->F[lane * 4]) = make_float4(F[0], F[1], F[2], F[3]);
     *reinterpret_cast<float4*>(&tab->I[lane * 4]) = make_float4(I[0], I[1], I[2], I[3]);
     *reinterpret_cast<float4*>(&tab->c[lane * 4]) =
-        make_float4(ex2_approx((fe - F[0]) + (we - I[0])), ex2_approx((fe - F[1]) + (we - I[1])),
-                    ex2_approx((fe - F[2]) + (we - I[2])), ex2_approx((fe - F[3]) + (we - I[3])));
+        make_float4(ex2_approx(sign * ((fe - F[0]) + (we - I[0]))), ex2_approx(sign * ((fe - F[1]) + (we - I[1]))),
+                    ex2_approx(sign * ((fe - F[2]) + (we - I[2]))), ex2_approx(sign * ((fe - F[3]) + (we - I[3]))));
 }
 // The f inputs of chunk c for la_tables; 0 behind the last token.
 __device__ __forceinline__ void la_load_f(const LaParams& p, int bh, int c, float (&x)[4]) {
@@ -179,6 +203,17 @@ __device__ __forceinline__ void la_drain(uint32_t bar, uint32_t parity, uint64_t
 }
 
 // ---------------------------------------------------------------- host
+// Reads and clears this source file's status word.
+static inline cudaError_t la_read_status(unsigned* word, cudaStream_t s) {
+    const unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_la_status, sizeof *word, 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && *word) {
+        e = cudaMemcpyToSymbolAsync(g_la_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
+    return e;
+}
 // Tensor map of x [rows][T][width] bf16: boxes of 128 tokens x 64 columns.
 bool la_tensor_map(CUtensorMap* map, const void* x, int width, int T, size_t rows);
 

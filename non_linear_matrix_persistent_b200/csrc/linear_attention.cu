@@ -50,6 +50,12 @@ bool fwd_on_tensor_cores(const m2rnn_la_dims* d) { return d->mode == M2RNN_MODE_
 
 m2rnn::LaPlan fwd_plan(const m2rnn_la_dims* d) { return m2rnn::la_fwd_plan(d->B, d->H, d->T, d->K, d->V); }
 
+bool bwd_on_tensor_cores(const m2rnn_la_dims* d) { return d->mode == M2RNN_MODE_BF16_TC; }
+m2rnn::LaPlan bwd_plan(const m2rnn_la_dims* d) { return m2rnn::la_bwd_plan(d->B, d->H, d->T, d->K, d->V); }
+size_t bwd_seg_bytes(const m2rnn_la_dims* d) {
+    return bwd_on_tensor_cores(d) ? m2rnn::la_seg_bytes(bwd_plan(d), d->B, d->H, d->K, d->V) : 0;
+}
+
 m2rnn::LaParams params(const m2rnn_la_dims* d) {
     m2rnn::LaParams p;
     std::memset(&p, 0, sizeof p);
@@ -82,7 +88,7 @@ size_t m2rnn_linear_attention_workspace(const m2rnn_la_dims* d, int backward) {
     if (check(d) != M2RNN_OK) return kRefused;
     if (pairs(d) * d->T == 0) return 0;
     if (!backward) return fwd_on_tensor_cores(d) ? m2rnn::la_seg_bytes(fwd_plan(d), d->B, d->H, d->K, d->V) : 0;
-    return group_bytes(d) + df_bytes(d);
+    return group_bytes(d) + df_bytes(d) + bwd_seg_bytes(d);
 }
 
 m2rnn_status m2rnn_linear_attention_forward(const m2rnn_la_dims* d, const void* k, const void* v, const void* q,
@@ -135,7 +141,15 @@ m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void*
         p.dq = reinterpret_cast<float*>(ws) + pairs(d) * d->T * d->K;
     }
     if (d->f_per_head) p.df = reinterpret_cast<float*>(ws + group_bytes(d));
-    cudaError_t e = m2rnn::launch_la_bwd_simt(p, s);
+    cudaError_t e;
+    if (bwd_on_tensor_cores(d)) {
+        const m2rnn::LaPlan plan = bwd_plan(d);
+        p.segs = plan.segs; p.seg_chunks = plan.seg_chunks;
+        p.seg_state = reinterpret_cast<float*>(ws + group_bytes(d) + df_bytes(d));
+        e = m2rnn::launch_la_bwd_tc(p, s);
+    } else {
+        e = m2rnn::launch_la_bwd_simt(p, s);
+    }
     if (e == cudaSuccess && group_bytes(d))
         e = m2rnn::launch_la_group_sum(p, static_cast<const float*>(p.dk), static_cast<const float*>(p.dq), dk, dq, s);
     if (e == cudaSuccess && d->f_per_head) e = m2rnn::launch_la_df_sum(p, p.df, df, s);
@@ -144,9 +158,10 @@ m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void*
 
 m2rnn_status m2rnn_linear_attention_status(m2rnn_stream_t stream) {
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    unsigned word = 0;
-    if (m2rnn::la_fwd_tc_status(&word, s) != cudaSuccess) return M2RNN_ERR_CUDA;
-    return word ? M2RNN_ERR_DEVICE_TIMEOUT : M2RNN_OK;
+    unsigned word = 0, bwd = 0;
+    if (m2rnn::la_fwd_tc_status(&word, s) != cudaSuccess || m2rnn::la_bwd_tc_status(&bwd, s) != cudaSuccess)
+        return M2RNN_ERR_CUDA;
+    return word | bwd ? M2RNN_ERR_DEVICE_TIMEOUT : M2RNN_OK;
 }
 
 // ------------------------------------------------------------------ layer norm

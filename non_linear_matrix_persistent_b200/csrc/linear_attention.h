@@ -26,7 +26,7 @@ struct LaParams {
     const float* S0;        // forward: initial state, may be null
     void* y;
     float* ST;              // may be null; may alias S0
-    float* ckpt;            // [B*H][ceil(T/128)][K][V]: S before token 128c; forward: output, may be null; backward: input
+    float* ckpt;            // [B*H][ceil(T/128)][V/4][K][4]: S before token 128c; forward: output, may be null; backward: input
     // backward
     const void* dy;
     const float* dST;       // may be null
@@ -81,6 +81,12 @@ LaPlan la_fwd_plan(int B, int H, int T, int K, int V);
 // Workspace of a plan: segment states and decays.
 size_t la_seg_bytes(const LaPlan& plan, int B, int H, int K, int V);
 cudaError_t la_fwd_tc_status(unsigned* word, cudaStream_t s);
+// Chunked tensor-core backward (bf16).
+cudaError_t launch_la_bwd_tc(const LaParams& p, cudaStream_t s);
+LaPlan la_bwd_plan(int B, int H, int T, int K, int V);
+// dL/dS at the segments' ends, into p.seg_state.
+cudaError_t launch_la_seg_grads(const LaParams& p, cudaStream_t s);
+cudaError_t la_bwd_tc_status(unsigned* word, cudaStream_t s);
 // fp32-arithmetic backward on the CUDA cores, both types.
 cudaError_t launch_la_bwd_simt(const LaParams& p, cudaStream_t s);
 // dk, dq [B, G, T, K] (bf16 or fp32) = sums of fp32 per-head partials over each group's heads, ascending.

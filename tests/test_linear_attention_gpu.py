@@ -74,7 +74,7 @@ def check(x, logit, bwd=True):
     close("y", y, wy, by, T, dtype)
     close("ST", ST, wS, bS, T, dtype)
     for c in range(ckpt.shape[2]):
-        close("ckpt", ckpt[:, :, c], states[128 * c], bstates[128 * c], T, dtype)
+        close("ckpt", ckpt[:, :, c].permute(0, 1, 3, 2, 4).reshape(states[0].shape), states[128 * c], bstates[128 * c], T, dtype)
     if not bwd:
         return y, ST
     got = a.linear_attention_backward(*args, ckpt, x["dy"], x["dST"], f_is_logit=logit)
