@@ -38,32 +38,7 @@ struct BwdMaps {
     CUtensorMap q, k, v, dy, dq, dk, dv;
 };
 
-template <int KP, int VP>
-struct BCfg {
-    static constexpr int NW = 16, kThreads = (NW + 3) * 32;
-    static constexpr int kQ = KP / 64 * kTileBytes, kV = VP / 64 * kTileBytes, kStage = 2 * kQ + 2 * kV;
-    static constexpr int kStages = KP == 64 && VP == 64 ? 2 : 1;
-    static constexpr int kOp = KP * VP * 2;                     // one bf16 term of a state
-    static constexpr int kOffX = kStages * kStage;              // two terms; the third over dP'
-    static constexpr int kOffP = kOffX + 2 * kOp;               // dP'ᵀ [s][t], 32 KB
-    static constexpr int kOffTab = kOffP + 2 * kTileBytes;
-    static constexpr int kOffBar = kOffTab + (int)sizeof(LaTablesZ);
-    static constexpr int kBars = 18;
-    static constexpr int kSmem = kOffBar + kBars * 8 + 16;
-    static_assert(kSmem <= 227 * 1024, "shared memory");
-    static_assert(2 * kOp >= kQ && kOp <= 2 * kTileBytes, "third terms");
-    // tensor memory: the scores, the accumulators.  For K = 128 the sum of dv
-    // starts, over dY·Vᵀ, when the scores have been read, and the state's
-    // gradient goes over dq once that has been read.
-    static constexpr bool kOwnDv = KP == 64;
-    static constexpr int kP = 0, kDP = 128, kDQ = 256, kDK = kDQ + KP, kDV = kOwnDv ? kDK + KP : kDP,
-                         kDG = KP == 128 ? kDQ : VP == 64 ? kDV + VP : kDP;
-    static constexpr int NS = KP * VP / 512;                    // state elements per thread
-    static constexpr int NL = NS < 16 ? NS : 16;
-    static constexpr int NQ = KP / 4, NV = VP / 4;              // columns of dq, dk and of dv per thread
-};
-
-// What the threads leave for df, over the v tile (no longer read by then).
+// What the threads leave for df.
 struct DfScratch {
     float alpha[4][128], beta[4][128];   // parts of the dot products, by warpgroup
     float total[4][128];                 // by source: its paths to each block of 32 sinks
@@ -71,6 +46,46 @@ struct DfScratch {
     float gamma[16];                     // parts of a_end <S, G>, by warp
 };
 static_assert(sizeof(DfScratch) <= kTileBytes, "scratch");
+
+// Two schedules.  Up to 64 x 128 and 128 x 64 (kRoomy) the terms of S, of G
+// and of a q have shared memory of their own: both states' products run while
+// the scores are worked on, and the sum for G while the outputs' products do.
+// For 128 x 128 the terms of S, then those of G, share two buffers and the
+// place of dP', and those of a q take tiles that are no longer read.
+template <int KP, int VP>
+struct BCfg {
+    static constexpr int NW = 16, kThreads = (NW + 3) * 32;
+    static constexpr int kQ = KP / 64 * kTileBytes, kV = VP / 64 * kTileBytes, kStage = 2 * kQ + 2 * kV;
+    static constexpr int kStages = KP == 64 && VP == 64 ? 2 : 1;
+    static constexpr bool kRoomy = KP * VP < 128 * 128;
+    static constexpr int kOp = KP * VP * 2;                     // one bf16 term of a state
+    static constexpr int kOffX = kStages * kStage;              // the states' terms
+    static constexpr int kX = (kRoomy ? 6 : 2) * kOp;
+    static constexpr int kOffP = kOffX + kX;                    // dP'ᵀ [s][t], 32 KB
+    // df's scratch: its own place, or the v tile once V Gᵀ is done
+    static constexpr bool kOwnScratch = KP == 64 && VP == 64;
+    static constexpr int kOffScratch = kOffP + 2 * kTileBytes;
+    static constexpr int kOffTab = kOffScratch + (kOwnScratch ? (int)sizeof(DfScratch) : 0);
+    static constexpr int kOffBar = kOffTab + (int)sizeof(LaTablesZ);
+    static constexpr int kBars = 19;
+    static constexpr int kSmem = kOffBar + kBars * 8 + 16;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(kX >= (kRoomy ? 3 : 1) * kQ && kOp <= 2 * kTileBytes, "terms of a q; third terms");
+    // where the terms of S, G and a q go, from kOffX; for the tight schedule
+    // the third terms of S and G at kOffP and a q's first two over q and k
+    static constexpr int kG0 = kRoomy ? 3 * kOp : 0;
+    // Tensor memory: the two score matrices, dq, dk, dv and the sum for G.
+    // Where the last two do not fit beside the others they go over dY·Vᵀ once
+    // the scores have been read (for 128 x 128 the sum for G over dq instead).
+    static constexpr bool kOwnDv = KP == 64;
+    static constexpr int kP = 0, kDP = 128, kDQ = 256, kDK = kDQ + KP, kDV = kOwnDv ? kDK + KP : kDP,
+                         kDG = KP == 128 ? (VP == 64 ? kDP + 64 : kDQ) : VP == 64 ? kDV + VP : kDP;
+    // the scores' columns are free for the next chunk once the products that read them are done
+    static constexpr bool kEarly = KP == 64 && VP == 64;
+    static constexpr int NS = KP * VP / 512;                    // state elements per thread
+    static constexpr int NL = NS < 16 ? NS : 16;
+    static constexpr int NQ = KP / 4, NV = VP / 4;              // columns of dq, dk and of dv per thread
+};
 
 // Column sums over the 32 lanes of 16 values a lane: lane 2c + {0, 1} gets column c's.
 __device__ __forceinline__ float column_sums(float (&r)[16]) {
@@ -107,13 +122,13 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const uint32_t b_full = bar(0), r_s = bar(2), b_in = bar(3), r_g = bar(4), b_g = bar(5), r_p = bar(6),
                    b_dv = bar(7), r_dv = bar(8), b_out = bar(9), r_aq = bar(10), b_dg = bar(11), r_out = bar(12),
-                   b_free = bar(13), b_tab = bar(14), r_df = bar(15), b_drain = bar(16);
+                   b_free = bar(13), b_tab = bar(14), r_df = bar(15), b_drain = bar(16), b_sc = bar(17);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint64_t limit = p.wait_limit_ns;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 17; ++i) mbar_init(bar(i), 1);
+        for (int i = 0; i < 18; ++i) mbar_init(bar(i), 1);
         for (uint32_t b : {r_s, r_g, r_p, r_dv, r_aq, r_out}) mbar_init(b, NW);   // one arrival a warp
         *abort_flag = 0;
         fence_mbarrier_init();
@@ -138,59 +153,77 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             id_dg = idesc_bf16_f32(KP, VP, 1, 1);                      // (a Q)ᵀ dY
         const uint64_t d_tile = sw128_desc(sbase, 16), d_mn = sw128_desc(sbase, kTileBytes),
                        d_op = sw128_desc(sbase, KP * 128);
-        constexpr uint32_t X0 = C::kOffX >> 4, X1 = X0 + (C::kOp >> 4), XP = C::kOffP >> 4;
+        constexpr uint32_t X = C::kOffX >> 4, OP = C::kOp >> 4, XP = C::kOffP >> 4;
         auto kmajor = [](int ks, int rows) { return (uint32_t)((ks >> 2) * (rows * 128 >> 4) + (ks & 3) * 2); };
+        // rows (128 tokens) times a state in three terms, the first two at x
+        auto times_state = [&](uint32_t d, uint32_t rows, uint32_t x) {
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                const uint32_t op = e < 2 || C::kRoomy ? x + e * OP : XP;
+#pragma unroll
+                for (int ks = 0; ks < VP / 16; ++ks)
+                    tc_mma_f16_ss(tmem + d, d_tile + rows + kmajor(ks, 128), d_op + op + kmajor(ks, KP), id_ki,
+                                  e > 0 || ks > 0);
+            }
+        };
+        auto tiles = [&](int i, uint32_t& q, uint32_t& k, uint32_t& v, uint32_t& dy) {
+            q = stage_of(i) * (C::kStage >> 4);
+            k = q + (C::kQ >> 4);
+            v = k + (C::kQ >> 4);
+            dy = v + (C::kV >> 4);
+        };
+        auto scores = [&](int i) {
+            uint32_t q, k, v, dy;
+            tiles(i, q, k, v, dy);
+#pragma unroll
+            for (int ks = 0; ks < KP / 16; ++ks)
+                tc_mma_f16_ss(tmem + C::kP, d_tile + k + kmajor(ks, 128), d_tile + q + kmajor(ks, 128), id_sc, ks > 0);
+#pragma unroll
+            for (int ks = 0; ks < VP / 16; ++ks)
+                tc_mma_f16_ss(tmem + C::kDP, d_tile + v + kmajor(ks, 128), d_tile + dy + kmajor(ks, 128), id_sc, ks > 0);
+            tc_commit(b_sc);
+        };
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             const int ph = i & 1;
-            const uint32_t q = stage_of(i) * (C::kStage >> 4), k = q + (C::kQ >> 4), v = k + (C::kQ >> 4),
-                           dy = v + (C::kV >> 4);
+            uint32_t q, k, v, dy;
+            tiles(i, q, k, v, dy);
+            auto inter_dv = [&]() {
+#pragma unroll
+                for (int ks = 0; ks < KP / 16; ++ks)
+                    tc_mma_f16_ss(tmem + C::kDV, d_tile + k + kmajor(ks, 128), d_op + X + (C::kG0 >> 4) + ks * 128, id_vi,
+                                  ks > 0);
+            };
             if (!(ok = la_wait(b_full + stage_of(i) * 8, stage_phase(i), abort_flag, limit))) break;
+            if (C::kEarly) {
+                if (i > 0 && !(ok = la_wait(b_out, ph ^ 1, abort_flag, limit))) break;
+                if (lane == 0) scores(i);
+            }
             if (!(ok = la_wait(r_s, ph, abort_flag, limit))) break;
             tc_fence_after();
             if (lane == 0) {
-#pragma unroll
-                for (int x = 0; x < 3; ++x) {       // dY Sᵀ, the terms of S
-                    const uint32_t op = x == 0 ? X0 : x == 1 ? X1 : XP;
-#pragma unroll
-                    for (int ks = 0; ks < VP / 16; ++ks)
-                        tc_mma_f16_ss(tmem + C::kDQ, d_tile + dy + kmajor(ks, 128), d_op + op + kmajor(ks, KP), id_ki,
-                                      x > 0 || ks > 0);
+                if (!C::kEarly && C::kRoomy) scores(i);
+                times_state(C::kDQ, dy, X);                     // dY Sᵀ
+                if (C::kRoomy) {
+                    times_state(C::kDK, v, X + (C::kG0 >> 4));  // V Gᵀ
+                    if (C::kOwnDv) inter_dv();
                 }
                 tc_commit(b_in);
-#pragma unroll
-                for (int ks = 0; ks < KP / 16; ++ks)
-                    tc_mma_f16_ss(tmem + C::kP, d_tile + k + kmajor(ks, 128), d_tile + q + kmajor(ks, 128), id_sc, ks > 0);
-#pragma unroll
-                for (int ks = 0; ks < VP / 16; ++ks)
-                    tc_mma_f16_ss(tmem + C::kDP, d_tile + v + kmajor(ks, 128), d_tile + dy + kmajor(ks, 128), id_sc,
-                                  ks > 0);
+                if (!C::kRoomy) scores(i);
             }
-            if (!(ok = la_wait(r_g, ph, abort_flag, limit))) break;
-            tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-                for (int x = 0; x < 3; ++x) {       // V Gᵀ, the terms of G
-                    const uint32_t op = x == 0 ? X0 : x == 1 ? X1 : XP;
-#pragma unroll
-                    for (int ks = 0; ks < VP / 16; ++ks)
-                        tc_mma_f16_ss(tmem + C::kDK, d_tile + v + kmajor(ks, 128), d_op + op + kmajor(ks, KP), id_ki,
-                                      x > 0 || ks > 0);
+            if (!C::kRoomy) {
+                if (!(ok = la_wait(r_g, ph, abort_flag, limit))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    times_state(C::kDK, v, X);
+                    tc_commit(b_g);
                 }
-                if (C::kOwnDv) {
-#pragma unroll
-                    for (int ks = 0; ks < KP / 16; ++ks)
-                        tc_mma_f16_ss(tmem + C::kDV, d_tile + k + kmajor(ks, 128), d_op + X0 + ks * 128, id_vi, ks > 0);
-                }
-                tc_commit(b_g);
             }
             if (!(ok = la_wait(r_p, ph, abort_flag, limit))) break;
             tc_fence_after();
             if (lane == 0) {
                 if (!C::kOwnDv) {
-#pragma unroll
-                    for (int ks = 0; ks < KP / 16; ++ks)
-                        tc_mma_f16_ss(tmem + C::kDV, d_tile + k + kmajor(ks, 128), d_op + X0 + ks * 128, id_vi, ks > 0);
+                    inter_dv();
                     tc_commit(b_dv);
                 }
 #pragma unroll
@@ -216,8 +249,8 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
-                for (int x = 0; x < 3; ++x) {       // the terms of a q: over the q tile, the k tile, the states' terms
-                    const uint32_t op = x == 0 ? q : x == 1 ? k : X0;
+                for (int x = 0; x < 3; ++x) {       // the terms of a q
+                    const uint32_t op = C::kRoomy ? X + x * (C::kQ >> 4) : x == 0 ? q : x == 1 ? k : X;
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         tc_mma_f16_ss(tmem + C::kDG, d_mn + op + ks * 128, d_mn + dy + ks * 128, id_dg, x > 0 || ks > 0);
@@ -253,10 +286,28 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 for (int x = 0; x < VP / 64; ++x)
                     tma_tile(base + 2 * C::kQ + x * kTileBytes, &maps.v, x * 64, t, bh, full);
             };
+            // into L2 a chunk before its load: the tiles and the checkpoint
+            auto prefetch = [&](int i) {
+                if (i >= n || p.fault) return;
+                const int c = chunk_of(i), t = c * kLaChunk;
+                bulk_prefetch(p.ckpt + ((size_t)bh * nchunks + c) * p.K * p.V, p.K * p.V * 4);
+                if (i < C::kStages) return;
+#pragma unroll
+                for (int x = 0; x < VP / 64; ++x) tma_prefetch_tile(&maps.dy, x * 64, t, bh);
+#pragma unroll
+                for (int x = 0; x < KP / 64; ++x) {
+                    tma_prefetch_tile(&maps.q, x * 64, t, qk);
+                    tma_prefetch_tile(&maps.k, x * 64, t, qk);
+                }
+#pragma unroll
+                for (int x = 0; x < VP / 64; ++x) tma_prefetch_tile(&maps.v, x * 64, t, bh);
+            };
             for (int i = 0; i < C::kStages && i < n; ++i) load(i);
+            prefetch(1);
             bool ok = true;
             int i = 0;
             for (; i < n; ++i) {
+                prefetch(i + 2);
                 const int ph = i & 1, t = chunk_of(i) * kLaChunk;
                 const uint32_t base = sbase + stage_of(i) * C::kStage;
                 if (!(ok = la_wait(r_out, ph, abort_flag, limit))) break;
@@ -290,7 +341,8 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
         for (int i = 0; i < n; ++i) {
             const int ph = i & 1, c = chunk_of(i);
             if (!la_wait(r_p, ph, abort_flag, limit)) break;
-            const DfScratch* sc = reinterpret_cast<const DfScratch*>(smem + stage_of(i) * C::kStage + 2 * C::kQ);
+            const DfScratch* sc = reinterpret_cast<const DfScratch*>(
+                smem + (C::kOwnScratch ? C::kOffScratch : stage_of(i) * C::kStage + 2 * C::kQ));
             const int block = lane >> 3, t0 = lane * 4;
             float x[4] = {0.f, 0.f, 0.f, 0.f}, al[4], be[4], past[3][4];
 #pragma unroll
@@ -396,43 +448,58 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(b);
         };
-        // three bf16 terms of a state's elements j..j+7 into the operand slots
-        auto put_terms = [&](const float (&x)[8], int j) {
+        // three bf16 terms of a state's elements j..j+7, the first two from x on
+        auto put_terms = [&](const float (&v)[8], int j, int x) {
             uint4 hi, mid, lo;
-            split3(x[0], x[1], hi.x, mid.x, lo.x);
-            split3(x[2], x[3], hi.y, mid.y, lo.y);
-            split3(x[4], x[5], hi.z, mid.z, lo.z);
-            split3(x[6], x[7], hi.w, mid.w, lo.w);
+            split3(v[0], v[1], hi.x, mid.x, lo.x);
+            split3(v[2], v[3], hi.y, mid.y, lo.y);
+            split3(v[4], v[5], hi.z, mid.z, lo.z);
+            split3(v[6], v[7], hi.w, mid.w, lo.w);
             const uint32_t at = (v0 >> 6) * (KP * 128) + sw128(kap, ((v0 & 63) + j) >> 3);
-            *reinterpret_cast<uint4*>(smem + C::kOffX + at) = hi;
-            *reinterpret_cast<uint4*>(smem + C::kOffX + C::kOp + at) = mid;
-            *reinterpret_cast<uint4*>(smem + C::kOffP + at) = lo;
+            *reinterpret_cast<uint4*>(smem + x + at) = hi;
+            *reinterpret_cast<uint4*>(smem + x + C::kOp + at) = mid;
+            *reinterpret_cast<uint4*>(smem + (C::kRoomy ? x + 2 * C::kOp : C::kOffP) + at) = lo;
         };
+        auto put_G = [&]() {
+#pragma unroll
+            for (int j = 0; j < C::NS; j += 8) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = G[j + e];
+                put_terms(x, j, C::kOffX + C::kG0);
+            }
+        };
+        float Sn[C::NS];   // the next chunk's S
+        auto load_S = [&](int c) {
+            const float* ck = p.ckpt + ((size_t)bh * nchunks + c) * p.K * p.V;
+#pragma unroll
+            for (int j = 0; j < C::NS; j += 4) {
+                const float4 s4 = mine && v0 + j < p.V
+                                      ? *reinterpret_cast<const float4*>(ck + ((size_t)((v0 + j) >> 2) * p.K + kap) * 4)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                Sn[j] = s4.x; Sn[j + 1] = s4.y; Sn[j + 2] = s4.z; Sn[j + 3] = s4.w;
+            }
+        };
+        load_S(chunk_of(0));
         auto tile_at = [&](int col) { return (col >> 6) * kTileBytes + sw128(row, (col & 63) >> 3); };
 
         for (int i = 0; i < n; ++i) {
             const int ph = i & 1, c = chunk_of(i);
             uint8_t* stage = smem + stage_of(i) * C::kStage;
-            // ---- S: its terms, and this thread's part of <S, G>
-            if (i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
+            // ---- the terms of S (and of G), and this thread's part of <S, G>
+            if (!C::kRoomy && i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
             float gamma = 0.f;
-            {
-                const float* ck = p.ckpt + ((size_t)bh * nchunks + c) * p.K * p.V;
 #pragma unroll
-                for (int j = 0; j < C::NS; j += 8) {
-                    float x[8];
+            for (int j = 0; j < C::NS; j += 8) {
+                float x[8];
 #pragma unroll
-                    for (int h = 0; h < 8; h += 4) {
-                        const float4 s4 = mine && v0 + j + h < p.V
-                                              ? *reinterpret_cast<const float4*>(ck + ((size_t)((v0 + j + h) >> 2) * p.K + kap) * 4)
-                                              : make_float4(0.f, 0.f, 0.f, 0.f);
-                        x[h] = s4.x; x[h + 1] = s4.y; x[h + 2] = s4.z; x[h + 3] = s4.w;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) gamma = fmaf(x[e], G[j + e], gamma);
-                    put_terms(x, j);
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = Sn[j + e];
+                    gamma = fmaf(x[e], G[j + e], gamma);
                 }
+                put_terms(x, j, C::kOffX);
             }
+            if (C::kRoomy) put_G();
             arrive(r_s);
             if (!la_wait(b_tab, ph, abort_flag, limit)) break;
             const float Ft = tab->F[row], It = tab->I[row], Fe = tab->F[127], Ie = tab->I[127];
@@ -444,17 +511,12 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
 #pragma unroll
             for (int d = 16; d; d >>= 1) gamma += __shfl_xor_sync(~0u, gamma, d);
             if (!la_wait(b_full + stage_of(i) * 8, stage_phase(i), abort_flag, limit)) break;
-            if (!la_wait(b_in, ph, abort_flag, limit)) break;
-            tc_fence_after();
-            // ---- G: its terms, over those of S
-#pragma unroll
-            for (int j = 0; j < C::NS; j += 8) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = G[j + e];
-                put_terms(x, j);
+            if (!C::kRoomy) {
+                if (!la_wait(b_in, ph, abort_flag, limit)) break;
+                tc_fence_after();
+                put_G();             // over the terms of S
+                arrive(r_g);
             }
-            arrive(r_g);
             // ---- a_t (S dy_t) and b_s (G v_s) in place, and their dot products with q and k
             auto scale_rows = [&](uint32_t col0, float w0, float w, const uint8_t* tile) {
                 float dot = 0.f;
@@ -491,16 +553,30 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                     tmem_st16(mylane + C::kDV + col, x);
                 }
             };
-            const float alpha = scale_rows(C::kDQ, at0, at, stage);
-            if (!la_wait(b_g, ph, abort_flag, limit)) break;
+            DfScratch* sc = reinterpret_cast<DfScratch*>(C::kOwnScratch ? smem + C::kOffScratch : stage + 2 * C::kQ);
+            auto scale_all = [&]() -> bool {
+                if (!la_wait(b_in, ph, abort_flag, limit)) return false;
+                tc_fence_after();
+                const float alpha = scale_rows(C::kDQ, at0, at, stage);
+                if (!C::kRoomy && !la_wait(b_g, ph, abort_flag, limit)) return false;
+                tc_fence_after();
+                const float beta = scale_rows(C::kDK, bt0, bt, stage + C::kQ);
+                if (C::kOwnDv) scale_dv();
+                sc->alpha[wg][row] = alpha;
+                sc->beta[wg][row] = beta;
+                if (lane == 0) sc->gamma[warp] = gamma;
+                return true;
+            };
+            if (!C::kRoomy) {
+                if (!scale_all()) break;
+            } else {
+                // the scratch and dP' may be written: V Gᵀ is done or df has been read, dq has left
+                if (!C::kOwnScratch && !la_wait(b_in, ph, abort_flag, limit)) break;
+                if (C::kOwnScratch && i > 0 && !la_wait(r_df, ph ^ 1, abort_flag, limit)) break;
+                if (i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
+            }
+            if (!la_wait(b_sc, ph, abort_flag, limit)) break;
             tc_fence_after();
-            const float beta = scale_rows(C::kDK, bt0, bt, stage + C::kQ);
-            if (C::kOwnDv) scale_dv();
-            // every product that reads the v tile and the states' third terms is done
-            DfScratch* sc = reinterpret_cast<DfScratch*>(stage + 2 * C::kQ);
-            sc->alpha[wg][row] = alpha;
-            sc->beta[wg][row] = beta;
-            if (lane == 0) sc->gamma[warp] = gamma;
             // ---- P'ᵀ, dP'ᵀ and df's sums: source s = row, sinks of block wg
             uint8_t* dp = smem + C::kOffP;
             float run = 0.f;
@@ -570,8 +646,10 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                         make_uint4(pd[e / 2], pd[e / 2 + 1], pd[e / 2 + 2], pd[e / 2 + 3]);
             }
             sc->total[wg][row] = run;
+            if (C::kRoomy && !scale_all()) break;
             tc_wait_st();
             arrive(r_p);
+            if (i + 1 < n) load_S(chunk_of(i + 1));
             if (!C::kOwnDv) {
                 if (!la_wait(b_dv, ph, abort_flag, limit)) break;
                 tc_fence_after();
@@ -579,6 +657,25 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 tc_wait_st();
                 arrive(r_dv);
             }
+            // ---- a_t q_t in three terms
+            auto put_aq = [&]() {
+#pragma unroll
+                for (int j = 0; j < C::NQ; j += 8) {
+                    const uint32_t pos = tile_at(wg * C::NQ + j);
+                    const uint4 x = *reinterpret_cast<const uint4*>(stage + pos);
+                    uint4 hi, mid, lo;
+                    split3(at * bf16lo_to_f32(x.x), at * bf16hi_to_f32(x.x), hi.x, mid.x, lo.x);
+                    split3(at * bf16lo_to_f32(x.y), at * bf16hi_to_f32(x.y), hi.y, mid.y, lo.y);
+                    split3(at * bf16lo_to_f32(x.z), at * bf16hi_to_f32(x.z), hi.z, mid.z, lo.z);
+                    split3(at * bf16lo_to_f32(x.w), at * bf16hi_to_f32(x.w), hi.w, mid.w, lo.w);
+                    uint8_t* X = smem + C::kOffX + pos;
+                    *reinterpret_cast<uint4*>(C::kRoomy ? X : stage + pos) = hi;
+                    *reinterpret_cast<uint4*>(C::kRoomy ? X + C::kQ : stage + C::kQ + pos) = mid;
+                    *reinterpret_cast<uint4*>(C::kRoomy ? X + 2 * C::kQ : X) = lo;
+                }
+                arrive(r_aq);
+            };
+            if (C::kRoomy) put_aq();   // over the states' terms, whose products are done
             if (!la_wait(b_out, ph, abort_flag, limit)) break;
             tc_fence_after();
             const int t = c * kLaChunk + row;
@@ -609,21 +706,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                     *reinterpret_cast<uint4*>(dp + tile_at(wg * C::NQ + j)) =
                         make_uint4(o[j / 2], o[j / 2 + 1], o[j / 2 + 2], o[j / 2 + 3]);
             }
-            // ---- a_t q_t in three terms: over q, over k, over the states' terms
-#pragma unroll
-            for (int j = 0; j < C::NQ; j += 8) {
-                const uint32_t pos = tile_at(wg * C::NQ + j);
-                const uint4 x = *reinterpret_cast<const uint4*>(stage + pos);
-                uint4 hi, mid, lo;
-                split3(at * bf16lo_to_f32(x.x), at * bf16hi_to_f32(x.x), hi.x, mid.x, lo.x);
-                split3(at * bf16lo_to_f32(x.y), at * bf16hi_to_f32(x.y), hi.y, mid.y, lo.y);
-                split3(at * bf16lo_to_f32(x.z), at * bf16hi_to_f32(x.z), hi.z, mid.z, lo.z);
-                split3(at * bf16lo_to_f32(x.w), at * bf16hi_to_f32(x.w), hi.w, mid.w, lo.w);
-                *reinterpret_cast<uint4*>(stage + pos) = hi;
-                *reinterpret_cast<uint4*>(stage + C::kQ + pos) = mid;
-                *reinterpret_cast<uint4*>(smem + C::kOffX + pos) = lo;
-            }
-            arrive(r_aq);
+            if (!C::kRoomy) put_aq();  // over q, over k, over the states' terms
             // ---- dk and dv, kept until their tiles are free
             uint32_t ok_[C::NQ / 2], ov[C::NV / 2];
             rows_out(C::kDK, p.dk, ok_);
