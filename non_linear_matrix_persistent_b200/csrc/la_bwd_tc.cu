@@ -80,6 +80,8 @@ struct BCfg {
     static constexpr bool kOwnDv = KP == 64;
     static constexpr int kP = 0, kDP = 128, kDQ = 256, kDK = kDQ + KP, kDV = kOwnDv ? kDK + KP : kDP,
                          kDG = KP == 128 ? (VP == 64 ? kDP + 64 : kDQ) : VP == 64 ? kDV + VP : kDP;
+    // the sum for G comes before the outputs' products
+    static constexpr bool kAqFirst = kRoomy && kOwnDv;
     // the scores' columns are free for the next chunk once the products that read them are done
     static constexpr bool kEarly = KP == 64 && VP == 64;
     static constexpr int NS = KP * VP / 512;                    // state elements per thread
@@ -87,12 +89,14 @@ struct BCfg {
     static constexpr int NQ = KP / 4, NV = VP / 4;              // columns of dq, dk and of dv per thread
 };
 
-// Column sums over the 32 lanes of 16 values a lane: lane 2c + {0, 1} gets column c's.
-__device__ __forceinline__ float column_sums(float (&r)[16]) {
+// Column sums over the 32 lanes of N = 16 or 32 values a lane: lane l gets
+// column l·N/32's.
+template <int N>
+__device__ __forceinline__ float column_sums(float (&r)[N]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int w = 8; w; w >>= 1) {
-        const int d = 2 * w;
+    for (int w = N / 2; w; w >>= 1) {
+        const int d = w * 32 / N;
         const bool up = lane & d;
 #pragma unroll
         for (int e = 0; e < w; ++e) {
@@ -100,7 +104,83 @@ __device__ __forceinline__ float column_sums(float (&r)[16]) {
             r[e] = keep + __shfl_xor_sync(~0u, send, d);
         }
     }
-    return r[0] + __shfl_xor_sync(~0u, r[0], 1);
+    return N == 32 ? r[0] : r[0] + __shfl_xor_sync(~0u, r[0], 1);
+}
+
+// One source's block of 32 sinks: from the raw scores (lane = source s, 32
+// columns of sinks t0..t0+31) P'ᵀ and dP'ᵀ in bf16, back over the scores in
+// tensor memory and, dP'ᵀ, to its place `dp(column)` in shared memory; returns
+// the source's sum of paths into the block, and leaves in cut[] by gate u the
+// sums over the warp's sources before u of the paths to sinks u.. of the block.
+// DIAG: the source's own block (sinks t >= s, an exponential each); otherwise
+// the decay is r·c[t].  ZERO: the chunk has gates at the floor, paths through
+// which count for df alone.
+template <bool DIAG, bool ZERO, int NSUM, class Place>
+__device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const LaTablesZ* tab, int t0, float Fs, float Is,
+                                             float Zs, float r, float* cut, Place dp) {
+    const int lane = threadIdx.x & 31;
+    float run = 0.f;
+    float R[NSUM];
+#pragma unroll
+    for (int h = 16; h >= 0; h -= 16) {
+        uint32_t x[16], y[16];
+        tmem_ld<16>(tp + h, x);
+        tmem_ld<16>(tdp + h, y);
+        float d[16], z[ZERO ? 16 : 1];
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            if constexpr (DIAG) {
+                const float4 f = *reinterpret_cast<const float4*>(&tab->F[t0 + h + e]);
+                const float4 w = *reinterpret_cast<const float4*>(&tab->I[t0 + h + e]);
+                d[e] = ex2_approx((f.x - Fs) + (w.x - Is)); d[e + 1] = ex2_approx((f.y - Fs) + (w.y - Is));
+                d[e + 2] = ex2_approx((f.z - Fs) + (w.z - Is)); d[e + 3] = ex2_approx((f.w - Fs) + (w.w - Is));
+#pragma unroll
+                for (int o = 0; o < 4; ++o) d[e + o] = h + e + o >= lane ? d[e + o] : 0.f;
+            } else {
+                const float4 c = *reinterpret_cast<const float4*>(&tab->c[t0 + h + e]);
+                d[e] = r * c.x; d[e + 1] = r * c.y; d[e + 2] = r * c.z; d[e + 3] = r * c.w;
+            }
+            if constexpr (ZERO) {
+                const float4 zs = *reinterpret_cast<const float4*>(&tab->Z[t0 + h + e]);
+                z[e] = zs.x != Zs ? 0.f : d[e]; z[e + 1] = zs.y != Zs ? 0.f : d[e + 1];
+                z[e + 2] = zs.z != Zs ? 0.f : d[e + 2]; z[e + 3] = zs.w != Zs ? 0.f : d[e + 3];
+            }
+        }
+        tc_wait_ld();
+        reg_fence(x);
+        reg_fence(y);
+        uint32_t pp[8], pd[8];
+#pragma unroll
+        for (int e = 14; e >= 0; e -= 2) {
+            const float2 P = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                         Q = make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), D = make_float2(d[e], d[e + 1]);
+            float2 PD = __fmul2_rn(P, D);
+            const float2 W = __fmul2_rn(PD, Q);
+            float2 QD = __fmul2_rn(Q, D);
+            if constexpr (ZERO) {
+                const float2 Zd = make_float2(z[e], z[e + 1]);
+                PD = __fmul2_rn(P, Zd);
+                QD = __fmul2_rn(Q, Zd);
+            }
+            pp[e / 2] = pack_bf16(PD.x, PD.y);
+            pd[e / 2] = pack_bf16(QD.x, QD.y);
+            const int at = NSUM == 32 ? h + e : e;
+            run += W.y;
+            R[at + 1] = !DIAG || h + e + 1 > lane ? run : 0.f;   // sources strictly before the gate
+            run += W.x;
+            R[at] = !DIAG || h + e > lane ? run : 0.f;
+        }
+        tmem_st_32x32b<8>(tp + h, pp);       // inside the half that has been read
+        tmem_st_32x32b<8>(tp + h + 8, pd);
+        *reinterpret_cast<uint4*>(dp(t0 + h)) = make_uint4(pd[0], pd[1], pd[2], pd[3]);
+        *reinterpret_cast<uint4*>(dp(t0 + h + 8)) = make_uint4(pd[4], pd[5], pd[6], pd[7]);
+        if constexpr (NSUM == 16) {
+            const float c = column_sums(R);
+            if (!(lane & 1)) cut[t0 + h + (lane >> 1)] = c;
+        }
+    }
+    if constexpr (NSUM == 32) cut[t0 + lane] = column_sums(R);
+    return run;
 }
 
 template <int KP, int VP>
@@ -219,6 +299,23 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                     tc_commit(b_g);
                 }
             }
+            auto sum_for_G = [&]() -> bool {
+                if (!la_wait(r_aq, ph, abort_flag, limit)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) {       // the terms of a q
+                        const uint32_t op = C::kRoomy ? X + x * (C::kQ >> 4) : x == 0 ? q : x == 1 ? k : X;
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            tc_mma_f16_ss(tmem + C::kDG, d_mn + op + ks * 128, d_mn + dy + ks * 128, id_dg,
+                                          x > 0 || ks > 0);
+                    }
+                    tc_commit(b_dg);
+                }
+                return true;
+            };
+            if (C::kAqFirst && !(ok = sum_for_G())) break;
             if (!(ok = la_wait(r_p, ph, abort_flag, limit))) break;
             tc_fence_after();
             if (lane == 0) {
@@ -230,9 +327,8 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 for (int ks = 0; ks < 8; ++ks)      // contraction over s, the rows of the dP'ᵀ and k tiles
                     tc_mma_f16_ss(tmem + C::kDQ, d_mn + XP + ks * 128, d_mn + k + ks * 128, id_dq, 1);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)      // over t: dP'ᵀ beside P'ᵀ in each block of 32 score columns
-                    tc_mma_f16_ts(tmem + C::kDK, tmem + C::kP + (ks >> 1) * 32 + 16 + (ks & 1) * 8, d_mn + q + ks * 128,
-                                  id_dk, 1);
+                for (int ks = 0; ks < 8; ++ks)      // over t: P'ᵀ and dP'ᵀ of 16 sinks over their 16 score columns
+                    tc_mma_f16_ts(tmem + C::kDK, tmem + C::kP + ks * 16 + 8, d_mn + q + ks * 128, id_dk, 1);
             }
             if (!C::kOwnDv) {
                 if (!(ok = la_wait(r_dv, ph, abort_flag, limit))) break;
@@ -241,22 +337,10 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             if (lane == 0) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                    tc_mma_f16_ts(tmem + C::kDV, tmem + C::kP + (ks >> 1) * 32 + (ks & 1) * 8, d_mn + dy + ks * 128, id_vi,
-                                  1);
+                    tc_mma_f16_ts(tmem + C::kDV, tmem + C::kP + ks * 16, d_mn + dy + ks * 128, id_vi, 1);
                 tc_commit(b_out);
             }
-            if (!(ok = la_wait(r_aq, ph, abort_flag, limit))) break;
-            tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-                for (int x = 0; x < 3; ++x) {       // the terms of a q
-                    const uint32_t op = C::kRoomy ? X + x * (C::kQ >> 4) : x == 0 ? q : x == 1 ? k : X;
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        tc_mma_f16_ss(tmem + C::kDG, d_mn + op + ks * 128, d_mn + dy + ks * 128, id_dg, x > 0 || ks > 0);
-                }
-                tc_commit(b_dg);
-            }
+            if (!C::kAqFirst && !(ok = sum_for_G())) break;
         }
         if (lane == 0) {   // nothing is in flight when the CTA ends
             tc_commit(b_drain);
@@ -314,7 +398,8 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 if (!p.dkq_fp32)
                     for (int x = 0; x < KP / 64; ++x)
                         if (x * 64 < p.K) {
-                            tma_store_tile(&maps.dq, sbase + C::kOffP + x * kTileBytes, x * 64, t, bh);
+                            tma_store_tile(&maps.dq, (C::kOwnScratch ? base + 2 * C::kQ : sbase + C::kOffP) + x * kTileBytes,
+                                           x * 64, t, bh);
                             tma_store_tile(&maps.dk, base + x * kTileBytes, x * 64, t, bh);
                         }
                 for (int x = 0; x < VP / 64; ++x)
@@ -487,6 +572,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             const int ph = i & 1, c = chunk_of(i);
             uint8_t* stage = smem + stage_of(i) * C::kStage;
             // ---- the terms of S (and of G), and this thread's part of <S, G>
+            // (their place: the products of the last chunk's terms are done, since its sum for G is)
             if (!C::kRoomy && i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
             float gamma = 0.f;
 #pragma unroll
@@ -570,93 +656,13 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             if (!C::kRoomy) {
                 if (!scale_all()) break;
             } else {
-                // the scratch and dP' may be written: V Gᵀ is done or df has been read, dq has left
+                // the scratch and dP' may be written: df has been read, or V Gᵀ is done and dq has left
                 if (!C::kOwnScratch && !la_wait(b_in, ph, abort_flag, limit)) break;
                 if (C::kOwnScratch && i > 0 && !la_wait(r_df, ph ^ 1, abort_flag, limit)) break;
-                if (i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
+                if (!C::kOwnScratch && i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
             }
             if (!la_wait(b_sc, ph, abort_flag, limit)) break;
             tc_fence_after();
-            // ---- P'ᵀ, dP'ᵀ and df's sums: source s = row, sinks of block wg
-            uint8_t* dp = smem + C::kOffP;
-            float run = 0.f;
-            if (wg < quarter) {   // sinks before the source
-                const uint32_t z[16] = {};
-                tmem_st16(mylane + C::kP + wg * 32, z);
-                tmem_st16(mylane + C::kP + wg * 32 + 16, z);
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(dp + tile_at(wg * 32 + e)) = make_uint4(0, 0, 0, 0);
-            } else {
-                const bool diag = wg == quarter;
-                const float r = diag ? 1.f : ex2_approx((tab->F[wg * 32 - 1] - Ft) + (tab->I[wg * 32 - 1] - It));
-                uint32_t pp[16], pd[16];
-#pragma unroll
-                for (int h = 16; h >= 0; h -= 16) {
-                    uint32_t x[16], y[16];
-                    tmem_ld<16>(mylane + C::kP + wg * 32 + h, x);
-                    tmem_ld<16>(mylane + C::kDP + wg * 32 + h, y);
-                    tc_wait_ld();
-                    reg_fence(x);
-                    reg_fence(y);
-                    float R[16];
-#pragma unroll
-                    for (int e = 12; e >= 0; e -= 4) {
-                        float d[4];
-                        if (diag) {
-                            const float4 fs = *reinterpret_cast<const float4*>(&tab->F[wg * 32 + h + e]);
-                            const float4 is = *reinterpret_cast<const float4*>(&tab->I[wg * 32 + h + e]);
-                            const float f4[4] = {fs.x, fs.y, fs.z, fs.w}, i4[4] = {is.x, is.y, is.z, is.w};
-#pragma unroll
-                            for (int o = 0; o < 4; ++o)
-                                d[o] = h + e + o >= lane ? ex2_approx((f4[o] - Ft) + (i4[o] - It)) : 0.f;
-                        } else {
-                            const float4 cs = *reinterpret_cast<const float4*>(&tab->c[wg * 32 + h + e]);
-                            d[0] = r * cs.x; d[1] = r * cs.y; d[2] = r * cs.z; d[3] = r * cs.w;
-                        }
-#pragma unroll
-                        for (int o = 3; o >= 0; --o) {
-                            const float P = __uint_as_float(x[e + o]), Q = __uint_as_float(y[e + o]);
-                            run = fmaf(P * d[o], Q, run);
-                            R[e + o] = !diag || h + e + o > lane ? run : 0.f;   // sources strictly before the gate
-                        }
-                        if (Ze != 0.f) {
-                            const float4 zs = *reinterpret_cast<const float4*>(&tab->Z[wg * 32 + h + e]);
-                            d[0] = zs.x != Zt ? 0.f : d[0]; d[1] = zs.y != Zt ? 0.f : d[1];
-                            d[2] = zs.z != Zt ? 0.f : d[2]; d[3] = zs.w != Zt ? 0.f : d[3];
-                        }
-#pragma unroll
-                        for (int o = 0; o < 4; ++o) {
-                            x[e + o] = __float_as_uint(__uint_as_float(x[e + o]) * d[o]);
-                            y[e + o] = __float_as_uint(__uint_as_float(y[e + o]) * d[o]);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        pp[(h + e) / 2] = pack_bf16(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                        pd[(h + e) / 2] = pack_bf16(__uint_as_float(y[e]), __uint_as_float(y[e + 1]));
-                    }
-                    const float cut = column_sums(R);
-                    if (!(lane & 1)) sc->cut[quarter][wg * 32 + h + (lane >> 1)] = cut;
-                }
-                tmem_st16(mylane + C::kP + wg * 32, pp);
-                tmem_st16(mylane + C::kP + wg * 32 + 16, pd);
-#pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    *reinterpret_cast<uint4*>(dp + tile_at(wg * 32 + e)) =
-                        make_uint4(pd[e / 2], pd[e / 2 + 1], pd[e / 2 + 2], pd[e / 2 + 3]);
-            }
-            sc->total[wg][row] = run;
-            if (C::kRoomy && !scale_all()) break;
-            tc_wait_st();
-            arrive(r_p);
-            if (i + 1 < n) load_S(chunk_of(i + 1));
-            if (!C::kOwnDv) {
-                if (!la_wait(b_dv, ph, abort_flag, limit)) break;
-                tc_fence_after();
-                scale_dv();
-                tc_wait_st();
-                arrive(r_dv);
-            }
             // ---- a_t q_t in three terms
             auto put_aq = [&]() {
 #pragma unroll
@@ -675,11 +681,50 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 }
                 arrive(r_aq);
             };
-            if (C::kRoomy) put_aq();   // over the states' terms, whose products are done
+            // ---- P'ᵀ, dP'ᵀ and df's sums: source s = row, sinks of block wg
+            uint8_t* dp = smem + C::kOffP;
+            float run = 0.f;
+            if (wg < quarter) {   // sinks before the source
+                const uint32_t z[16] = {};
+                tmem_st16(mylane + C::kP + wg * 32, z);
+                tmem_st16(mylane + C::kP + wg * 32 + 16, z);
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(dp + tile_at(wg * 32 + e)) = make_uint4(0, 0, 0, 0);
+            } else {
+                const uint32_t tp = mylane + C::kP + wg * 32, tdp = mylane + C::kDP + wg * 32;
+                float* cut = sc->cut[quarter];
+                auto place = [&](int col) { return dp + tile_at(col); };
+                const bool diag = wg == quarter;
+                const float r = diag ? 1.f : ex2_approx((tab->F[wg * 32 - 1] - Ft) + (tab->I[wg * 32 - 1] - It));
+                constexpr int N = C::NS <= 16 ? 32 : 16;   // registers
+                if (Ze != 0.f)
+                    run = diag ? score_block<true, true, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, cut, place)
+                               : score_block<false, true, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, cut, place);
+                else
+                    run = diag ? score_block<true, false, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, cut, place)
+                               : score_block<false, false, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, cut, place);
+            }
+            sc->total[wg][row] = run;
+            if (C::kAqFirst) {   // over the states' terms: the sum for G runs while the rows are scaled
+                if (!la_wait(b_in, ph, abort_flag, limit)) break;
+                put_aq();
+            }
+            if (C::kRoomy && !scale_all()) break;
+            tc_wait_st();
+            arrive(r_p);
+            if (i + 1 < n) load_S(chunk_of(i + 1));
+            if (!C::kOwnDv) {
+                if (!la_wait(b_dv, ph, abort_flag, limit)) break;
+                tc_fence_after();
+                scale_dv();
+                tc_wait_st();
+                arrive(r_dv);
+            }
+            if (C::kRoomy && !C::kAqFirst) put_aq();   // over the states' terms, whose products are done
             if (!la_wait(b_out, ph, abort_flag, limit)) break;
             tc_fence_after();
             const int t = c * kLaChunk + row;
-            // ---- dq, over dP'
+            // ---- dq, over dP' or the v tile
             auto rows_out = [&](uint32_t col0, void* out, uint32_t (&o)[C::NQ / 2]) {
 #pragma unroll
                 for (int j = 0; j < C::NQ; j += 16) {
@@ -703,7 +748,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 rows_out(C::kDQ, p.dq, o);
 #pragma unroll
                 for (int j = 0; j < C::NQ; j += 8)
-                    *reinterpret_cast<uint4*>(dp + tile_at(wg * C::NQ + j)) =
+                    *reinterpret_cast<uint4*>((C::kOwnScratch ? stage + 2 * C::kQ : dp) + tile_at(wg * C::NQ + j)) =
                         make_uint4(o[j / 2], o[j / 2 + 1], o[j / 2 + 2], o[j / 2 + 3]);
             }
             if (!C::kRoomy) put_aq();  // over q, over k, over the states' terms
