@@ -81,7 +81,7 @@ struct BCfg {
     static constexpr int kP = 0, kDP = 128, kDQ = 256, kDK = kDQ + KP, kDV = kOwnDv ? kDK + KP : kDP,
                          kDG = KP == 128 ? (VP == 64 ? kDP + 64 : kDQ) : VP == 64 ? kDV + VP : kDP;
     // the sum for G comes before the outputs' products
-    static constexpr bool kAqFirst = kRoomy && kOwnDv;
+    static constexpr bool kAqFirst = false;
     // the scores' columns are free for the next chunk once the products that read them are done
     static constexpr bool kEarly = KP == 64 && VP == 64;
     static constexpr int NS = KP * VP / 512;                    // state elements per thread
@@ -565,28 +565,38 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 Sn[j] = s4.x; Sn[j + 1] = s4.y; Sn[j + 2] = s4.z; Sn[j + 3] = s4.w;
             }
         };
-        load_S(chunk_of(0));
-        auto tile_at = [&](int col) { return (col >> 6) * kTileBytes + sw128(row, (col & 63) >> 3); };
-
-        for (int i = 0; i < n; ++i) {
-            const int ph = i & 1, c = chunk_of(i);
-            uint8_t* stage = smem + stage_of(i) * C::kStage;
-            // ---- the terms of S (and of G), and this thread's part of <S, G>
-            // (their place: the products of the last chunk's terms are done, since its sum for G is)
-            if (!C::kRoomy && i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
-            float gamma = 0.f;
+        // the terms of S (and of G) for the chunk to come, and this thread's part of <S, G>
+        float gamma_next = 0.f;
+        auto put_S = [&]() {
+            gamma_next = 0.f;
 #pragma unroll
             for (int j = 0; j < C::NS; j += 8) {
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     x[e] = Sn[j + e];
-                    gamma = fmaf(x[e], G[j + e], gamma);
+                    gamma_next = fmaf(x[e], G[j + e], gamma_next);
                 }
                 put_terms(x, j, C::kOffX);
             }
             if (C::kRoomy) put_G();
             arrive(r_s);
+        };
+        load_S(chunk_of(0));
+        if (C::kRoomy) put_S();
+        constexpr bool kLoadEarly = C::NS <= 16;   // registers
+        auto tile_at = [&](int col) { return (col >> 6) * kTileBytes + sw128(row, (col & 63) >> 3); };
+
+        for (int i = 0; i < n; ++i) {
+            const int ph = i & 1, c = chunk_of(i);
+            uint8_t* stage = smem + stage_of(i) * C::kStage;
+            if (!C::kRoomy) {
+                // (their place: the last chunk's products of terms are done, since its sum for G is)
+                if (i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
+                put_S();
+            }
+            float gamma = gamma_next;
+            if (kLoadEarly && i + 1 < n) load_S(chunk_of(i + 1));
             if (!la_wait(b_tab, ph, abort_flag, limit)) break;
             const float Ft = tab->F[row], It = tab->I[row], Fe = tab->F[127], Ie = tab->I[127];
             const float Zt = tab->Z[row], Ze = tab->Z[127];
@@ -712,7 +722,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             if (C::kRoomy && !scale_all()) break;
             tc_wait_st();
             arrive(r_p);
-            if (i + 1 < n) load_S(chunk_of(i + 1));
+            if (!kLoadEarly && i + 1 < n) load_S(chunk_of(i + 1));
             if (!C::kOwnDv) {
                 if (!la_wait(b_dv, ph, abort_flag, limit)) break;
                 tc_fence_after();
@@ -780,6 +790,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < C::NL; ++e) G[j + e] = fmaf(A, G[j + e], __uint_as_float(d[e]));
             }
+            if (C::kRoomy && i + 1 < n) put_S();   // every read of this chunk's sums is done
             if (!p.dkq_fp32) {
 #pragma unroll
                 for (int j = 0; j < C::NQ; j += 8)
