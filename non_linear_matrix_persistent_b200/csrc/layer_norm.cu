@@ -15,12 +15,14 @@
 // The gradients of the weight and the bias are sums over rows: every thread
 // keeps its columns' sums in registers over the rows of its CTA's block of one
 // (b, h), the CTA's row groups are added through shared memory, and a second
-// kernel adds the blocks in ascending order: no atomics, the same bits every
+// kernel adds the blocks in a fixed order: no atomics, the same bits every
 // time.
 #include "kernels.h"
 #include "layer_norm.h"
 
 #include <cuda_bf16.h>
+
+#include <cstdlib>
 
 namespace m2rnn {
 namespace {
@@ -49,6 +51,34 @@ __device__ __forceinline__ void load(const float* p, float (&v)[VEC]) {
         v[0] = *p;
     }
 }
+// VEC values as they lie in memory, to be unpacked when they are used: what a
+// prefetch holds.
+template <class T, int VEC>
+struct Raw {
+    static constexpr int kWords = VEC == 1 ? 1 : VEC * (int)sizeof(T) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void get(const T* p) {
+        if constexpr (VEC == 1) {
+            if constexpr (sizeof(T) == 2) w[0] = *reinterpret_cast<const uint16_t*>(p);
+            else w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 x = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+                w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ float operator[](int e) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+        else return VEC == 1 || !(e & 1) ? bf16lo_to_f32(w[e / 2]) : bf16hi_to_f32(w[e / 2]);
+    }
+};
+
 template <int VEC>
 __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[VEC]) {
     if constexpr (VEC == 8) {
@@ -71,109 +101,153 @@ __device__ __forceinline__ void store(float* p, const float (&v)[VEC]) {
     }
 }
 
-// Sum over the LPR threads of a row, the same value in each of them.  `buf`:
-// a slot per warp, not the one of the previous call (for LPR > 32).
-template <int LPR>
-__device__ __forceinline__ float row_sum(float x, float* buf) {
+// Sums over the LPR threads of a row of U values, the same in each of them.
+// `buf`: U slots per warp, not those of the previous call (for LPR > 32).
+template <int LPR, int U>
+__device__ __forceinline__ void row_sums(float (&x)[U], float (*buf)[U]) {
 #pragma unroll
-    for (int d = (LPR < 32 ? LPR : 32) / 2; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
+    for (int d = (LPR < 32 ? LPR : 32) / 2; d; d >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] += __shfl_xor_sync(~0u, x[u], d);
     if constexpr (LPR > 32) {
         static_assert(LPR == kThreads, "a row takes part of a warp or the whole CTA");
-        if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = x;
+        if (threadIdx.x % 32 == 0)
+#pragma unroll
+            for (int u = 0; u < U; ++u) buf[threadIdx.x / 32][u] = x[u];
         __syncthreads();
-        x = buf[0];
 #pragma unroll
-        for (int w = 1; w < kThreads / 32; ++w) x += buf[w];
+        for (int u = 0; u < U; ++u) {
+            x[u] = buf[0][u];
+#pragma unroll
+            for (int w = 1; w < kThreads / 32; ++w) x[u] += buf[w][u];
+        }
     }
-    return x;
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x, float (*buf)[1]) {
+    float v[1] = {x};
+    row_sums<LPR, 1>(v, buf);
+    return v[0];
 }
 
-__device__ __forceinline__ size_t token_row(const NormParams& p, size_t r) {   // x's row (b, h, t) -> y's (b, t, h)
-    if (p.H == 1) return r;
-    const size_t bh = r / p.T, t = r % p.T;
-    return ((bh / p.H) * p.T + t) * p.H + bh % p.H;
+// Row t of pair bh: x's row is bh·T + t, y's this.
+__device__ __forceinline__ size_t token_row(const NormParams& p, int bh, int t) {
+    return ((size_t)(bh / p.H) * p.T + t) * p.H + bh % p.H;
 }
 
-// LPR threads per row, CH groups of VEC values per thread: N <= LPR·VEC·CH.
-template <class X, class Y, int VEC, int LPR, int CH>
+// Work items are pairs (row block of a (b, h)); `per` rows per block.
+struct Block {
+    int bh, t0, t1;
+};
+__device__ __forceinline__ Block block_of(const NormParams& p) {
+    const int chunk = blockIdx.x % p.chunks, per = (p.T + p.chunks - 1) / p.chunks;
+    return {(int)(blockIdx.x / p.chunks), chunk * per, min(p.T, (chunk + 1) * per)};
+}
+
+// LPR threads per row, CH groups of VEC values per thread (N <= LPR·VEC·CH), U
+// rows at a time.  A CTA takes items of kGroups·U consecutive rows of one
+// (b, h), blockIdx.x and every gridDim.x-th from there, and has the next one's
+// loads in flight while it works on one.
+template <class X, class Y, int VEC, int LPR, int CH, int U>
 __global__ void __launch_bounds__(kThreads) m2rnn_norm_fwd_kernel(const NormParams p) {
-    __shared__ float buf[2][kThreads / 32];
-    const int lane = threadIdx.x % LPR, N = p.N;
-    const size_t rows = (size_t)p.B * p.H * p.T, step = (size_t)gridDim.x * (kThreads / LPR);
+    constexpr int kGroups = kThreads / LPR, kRows = kGroups * U;
+    __shared__ float buf[2][kThreads / 32][U];
+    const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, N = p.N;
     const float inv = 1.f / (float)N;
-    // every thread of a warp takes part in the shuffles: the loop bound is the CTA's
-    for (size_t r0 = (size_t)blockIdx.x * (kThreads / LPR); r0 < rows; r0 += step) {
-        const size_t r = r0 + threadIdx.x / LPR;
-        const bool live = r < rows;
-        const X* x = static_cast<const X*>(p.x) + (live ? r : 0) * N;
-        float v[CH][VEC];
-        float s = 0.f;
+    const unsigned per = (p.T + kRows - 1) / kRows, items = (unsigned)(p.B * p.H) * per;
+    Raw<X, VEC> next[U][CH];
+    auto fetch = [&](unsigned item) {
+        const unsigned bh = item / per;
+        const int t0 = (int)(item % per) * kRows + grp;
+        const X* x = static_cast<const X*>(p.x) + ((size_t)bh * p.T + t0) * N;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int i = (c * LPR + lane) * VEC;
-            if (live && i < N) {
-                load<VEC>(x + i, v[c]);
-            } else {
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) v[c][e] = 0.f;
+            for (int c = 0; c < CH; ++c) {
+                const int i = (c * LPR + lane) * VEC;
+                if (item < items && t0 + u * kGroups < p.T && i < N) next[u][c].get(x + (size_t)u * kGroups * N + i);
+                else next[u][c].zero();
             }
+    };
+    fetch(blockIdx.x);
+    for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {   // the same count for every thread
+        const int bh = (int)(item / per), t0 = (int)(item % per) * kRows + grp;
+        float v[U][CH][VEC], s[U], m[U];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s += v[c][e];
+        for (int u = 0; u < U; ++u) {
+            s[u] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    v[u][c][e] = next[u][c][e];
+                    s[u] += v[u][c][e];
+                }
         }
-        const float m = p.rms ? 0.f : row_sum<LPR>(s, buf[0]) * inv;
-        s = 0.f;
+        fetch(item + gridDim.x);
+        if (!p.rms) row_sums<LPR, U>(s, buf[0]);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const bool in = (c * LPR + lane) * VEC < N;
+        for (int u = 0; u < U; ++u) {
+            m[u] = p.rms ? 0.f : s[u] * inv;
+            s[u] = 0.f;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                v[c][e] -= m;
-                s = in ? fmaf(v[c][e], v[c][e], s) : s;
+            for (int c = 0; c < CH; ++c) {
+                const bool in = (c * LPR + lane) * VEC < N;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    v[u][c][e] -= m[u];
+                    s[u] = in ? fmaf(v[u][c][e], v[u][c][e], s[u]) : s[u];
+                }
             }
         }
-        const float rs = 1.f / sqrtf(row_sum<LPR>(s, buf[1]) * inv + p.eps);
-        if constexpr (LPR > 32) __syncthreads();   // buf[] is free for the next row
-        if (!live) continue;
-        if (lane == 0) {
-            if (p.mean && !p.rms) p.mean[r] = m;
-            if (p.rstd) p.rstd[r] = rs;
+        row_sums<LPR, U>(s, buf[1]);
+        if constexpr (LPR > 32) __syncthreads();   // buf[] is free for the next rows
+        float rs[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            rs[u] = 1.f / sqrtf(s[u] * inv + p.eps);
+            const int t = t0 + u * kGroups;
+            if (lane == 0 && t < p.T) {
+                const size_t r = (size_t)bh * p.T + t;
+                if (p.mean && !p.rms) p.mean[r] = m[u];
+                if (p.rstd) p.rstd[r] = rs[u];
+            }
         }
-        const size_t wrow = (size_t)(p.H == 1 ? 0 : (r / p.T) % p.H) * N;
-        Y* y = static_cast<Y*>(p.y) + token_row(p, r) * N;
+        const size_t wrow = (size_t)(bh % p.H) * N;
+        Y* y = static_cast<Y*>(p.y) + token_row(p, bh, t0) * N;
+        const size_t ystep = (size_t)kGroups * p.H * N;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int i = (c * LPR + lane) * VEC;
             if (i >= N) continue;
-            float w[VEC], o[VEC];
+            float w[VEC], b[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = v[c][e] * rs;
-            if (p.weight) {
-                load<VEC>(p.weight + wrow + i, w);
+            for (int e = 0; e < VEC; ++e) { w[e] = 1.f; b[e] = 0.f; }
+            if (p.weight) load<VEC>(p.weight + wrow + i, w);
+            if (p.bias) load<VEC>(p.bias + wrow + i, b);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] *= w[e];
+            for (int u = 0; u < U; ++u) {
+                if (t0 + u * kGroups >= p.T) continue;
+                float o[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) o[e] = fmaf(v[u][c][e] * rs[u], w[e], b[e]);
+                store<VEC>(y + u * ystep + i, o);
             }
-            if (p.bias) {
-                load<VEC>(p.bias + wrow + i, w);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] += w[e];
-            }
-            store<VEC>(y + i, o);
         }
     }
 }
 
-// One CTA per row block of one (b, h).
-template <class X, class Y, class DX, int VEC, int LPR, int CH>
+// A CTA takes a block of rows of one (b, h), U·kGroups at a time, the next ones
+// in flight.
+template <class X, class Y, class DX, int VEC, int LPR, int CH, int U>
 __global__ void __launch_bounds__(kThreads) m2rnn_norm_bwd_kernel(const NormParams p) {
-    constexpr int kGroups = kThreads / LPR;                 // rows at a time
-    __shared__ float buf[2][kThreads / 32];
+    constexpr int kGroups = kThreads / LPR, kRows = kGroups * U;
+    __shared__ float buf[kThreads / 32][2 * U];
     __shared__ float sums[LPR > 32 ? 1 : kThreads * VEC];   // row groups' partial sums, one chunk at a time
     const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, N = p.N;
-    const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
-    const int per = (p.T + p.chunks - 1) / p.chunks;
-    const int t0 = chunk * per, t1 = min(p.T, t0 + per);
+    const Block b = block_of(p);
     const float inv = 1.f / (float)N;
-    const size_t wrow = (size_t)(bh % p.H) * N;
+    const size_t wrow = (size_t)(b.bh % p.H) * N, xrow = (size_t)b.bh * p.T;
     float w[CH][VEC], dw[CH][VEC], db[CH][VEC];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -182,48 +256,74 @@ __global__ void __launch_bounds__(kThreads) m2rnn_norm_bwd_kernel(const NormPara
         for (int e = 0; e < VEC; ++e) { w[c][e] = 1.f; dw[c][e] = 0.f; db[c][e] = 0.f; }
         if (p.weight && i < N) load<VEC>(p.weight + wrow + i, w[c]);
     }
-    for (int tb = t0; tb < t1; tb += kGroups) {
-        const int t = tb + grp;
-        const bool live = t < t1;
-        const size_t r = (size_t)bh * p.T + (live ? t : t0);
-        const X* x = static_cast<const X*>(p.x) + r * N;
-        const Y* dy = static_cast<const Y*>(p.dy) + token_row(p, r) * N;
-        const float m = p.rms ? 0.f : p.mean[r], rs = p.rstd[r];
-        float n[CH][VEC], g[CH][VEC];
-        float s1 = 0.f, s2 = 0.f;
+    Raw<X, VEC> nx[U][CH];
+    Raw<Y, VEC> ny[U][CH];
+    float nm[U], nr[U];
+    auto fetch = [&](int t0) {
+        const X* x = static_cast<const X*>(p.x) + (xrow + t0) * N;
+        const Y* dy = static_cast<const Y*>(p.dy) + token_row(p, b.bh, t0) * N;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int i = (c * LPR + lane) * VEC;
-            if (live && i < N) {
-                load<VEC>(x + i, n[c]);
-                load<VEC>(dy + i, g[c]);
-            } else {
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + u * kGroups;
+            const bool live = t < b.t1;
+            nm[u] = live && !p.rms ? p.mean[xrow + t] : 0.f;
+            nr[u] = live ? p.rstd[xrow + t] : 0.f;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) { n[c][e] = m; g[c][e] = 0.f; }
-            }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                n[c][e] = (n[c][e] - m) * rs;
-                dw[c][e] = fmaf(g[c][e], n[c][e], dw[c][e]);
-                db[c][e] += g[c][e];
-                g[c][e] *= w[c][e];
-                s1 += g[c][e];
-                s2 = fmaf(g[c][e], n[c][e], s2);
+            for (int c = 0; c < CH; ++c) {
+                const int i = (c * LPR + lane) * VEC;
+                if (live && i < N) {
+                    nx[u][c].get(x + (size_t)u * kGroups * N + i);
+                    ny[u][c].get(dy + (size_t)u * kGroups * p.H * N + i);
+                } else {
+                    nx[u][c].zero();
+                    ny[u][c].zero();
+                }
             }
         }
-        const float m1 = p.rms ? 0.f : row_sum<LPR>(s1, buf[0]) * inv;
-        const float m2 = row_sum<LPR>(s2, buf[1]) * inv;
+    };
+    fetch(b.t0 + grp);
+    for (int tb = b.t0; tb < b.t1; tb += kRows) {
+        float n[U][CH][VEC], g[U][CH][VEC], s[2 * U], rs[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool live = tb + u * kGroups + grp < b.t1;
+            rs[u] = nr[u];
+            float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const bool in = live && (c * LPR + lane) * VEC < N;   // nothing of a NaN mean beside the row
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    n[u][c][e] = in ? (nx[u][c][e] - nm[u]) * rs[u] : 0.f;
+                    g[u][c][e] = ny[u][c][e];
+                    dw[c][e] = fmaf(g[u][c][e], n[u][c][e], dw[c][e]);
+                    db[c][e] += g[u][c][e];
+                    g[u][c][e] *= w[c][e];
+                    s1 += g[u][c][e];
+                    s2 = fmaf(g[u][c][e], n[u][c][e], s2);
+                }
+            }
+            s[2 * u] = s1;
+            s[2 * u + 1] = s2;
+        }
+        fetch(tb + kRows + grp);
+        row_sums<LPR, 2 * U>(s, buf);
         if constexpr (LPR > 32) __syncthreads();
-        if (!live) continue;
-        DX* dx = static_cast<DX*>(p.dx) + r * N;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int i = (c * LPR + lane) * VEC;
-            if (i >= N) continue;
-            float o[VEC];
+        for (int u = 0; u < U; ++u) {
+            const int t = tb + u * kGroups + grp;
+            if (t >= b.t1) continue;
+            const float m1 = p.rms ? 0.f : s[2 * u] * inv, m2 = s[2 * u + 1] * inv;
+            DX* dx = static_cast<DX*>(p.dx) + (xrow + t) * N;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = rs * (g[c][e] - m1 - n[c][e] * m2);
-            store<VEC>(dx + i, o);
+            for (int c = 0; c < CH; ++c) {
+                const int i = (c * LPR + lane) * VEC;
+                if (i >= N) continue;
+                float o[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) o[e] = rs[u] * (g[u][c][e] - m1 - n[u][c][e] * m2);
+                store<VEC>(dx + i, o);
+            }
         }
     }
     if (!p.part) return;
@@ -233,11 +333,8 @@ __global__ void __launch_bounds__(kThreads) m2rnn_norm_bwd_kernel(const NormPara
         for (int c = 0; c < CH; ++c) {
             const int i = (c * LPR + lane) * VEC;
             if (i >= N) continue;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                part[i + e] = dw[c][e];
-                part[N + i + e] = db[c][e];
-            }
+            store<VEC>(part + i, dw[c]);   // both 32-byte aligned where VEC is 8: N is a multiple of 8
+            store<VEC>(part + N + i, db[c]);
         }
     } else {
 #pragma unroll
@@ -249,11 +346,11 @@ __global__ void __launch_bounds__(kThreads) m2rnn_norm_bwd_kernel(const NormPara
                 for (int e = 0; e < VEC; ++e) sums[(grp * LPR + lane) * VEC + e] = which ? db[c][e] : dw[c][e];
                 __syncthreads();
                 for (int i = threadIdx.x; i < LPR * VEC; i += kThreads) {
-                    float s = sums[i];
+                    float a = sums[i];
 #pragma unroll 8
-                    for (int gg = 1; gg < kGroups; ++gg) s += sums[gg * LPR * VEC + i];
+                    for (int gg = 1; gg < kGroups; ++gg) a += sums[gg * LPR * VEC + i];
                     const int col = c * LPR * VEC + i;
-                    if (col < N) part[which * N + col] = s;
+                    if (col < N) part[which * N + col] = a;
                 }
             }
     }
@@ -268,6 +365,7 @@ __global__ void __launch_bounds__(256) m2rnn_norm_dw_kernel(const NormParams p) 
     const int n = p.B * p.chunks;
     float a = 0.f;
     if (e < 2 * N)
+#pragma unroll 8
         for (int j = grp; j < n; j += 8)
             a += p.part[((size_t)((j / p.chunks) * p.H + h) * p.chunks + j % p.chunks) * 2 * N + e];
     s[grp][lane] = a;
@@ -284,11 +382,12 @@ __global__ void __launch_bounds__(256) m2rnn_norm_dw_kernel(const NormParams p) 
 // for each pass.
 template <class X, class Y>
 __global__ void __launch_bounds__(kThreads) m2rnn_norm_fwd_long_kernel(const NormParams p) {
-    __shared__ float buf[2][kThreads / 32];
+    __shared__ float buf[2][kThreads / 32][1];
     const int N = p.N;
-    const size_t rows = (size_t)p.B * p.H * p.T;
     const float inv = 1.f / (float)N;
-    for (size_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const Block b = block_of(p);
+    for (int t = b.t0; t < b.t1; ++t) {
+        const size_t r = (size_t)b.bh * p.T + t;
         const X* x = static_cast<const X*>(p.x) + r * N;
         float s = 0.f;
         if (!p.rms)
@@ -305,8 +404,8 @@ __global__ void __launch_bounds__(kThreads) m2rnn_norm_fwd_long_kernel(const Nor
             if (p.mean && !p.rms) p.mean[r] = m;
             if (p.rstd) p.rstd[r] = rs;
         }
-        const size_t wrow = (size_t)(p.H == 1 ? 0 : (r / p.T) % p.H) * N;
-        Y* y = static_cast<Y*>(p.y) + token_row(p, r) * N;
+        const size_t wrow = (size_t)(b.bh % p.H) * N;
+        Y* y = static_cast<Y*>(p.y) + token_row(p, b.bh, t) * N;
         for (int i = threadIdx.x; i < N; i += kThreads) {
             float o[1] = {(to_f32(x[i]) - m) * rs};
             if (p.weight) o[0] *= p.weight[wrow + i];
@@ -321,19 +420,18 @@ __global__ void __launch_bounds__(kThreads) m2rnn_norm_fwd_long_kernel(const Nor
 // is only ever touched by one thread).
 template <class X, class Y, class DX>
 __global__ void __launch_bounds__(kThreads) m2rnn_norm_bwd_long_kernel(const NormParams p) {
-    __shared__ float buf[2][kThreads / 32];
-    const int N = p.N, bh = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
-    const int per = (p.T + p.chunks - 1) / p.chunks;
-    const int t0 = chunk * per, t1 = min(p.T, t0 + per);
+    __shared__ float buf[2][kThreads / 32][1];
+    const int N = p.N;
+    const Block b = block_of(p);
     const float inv = 1.f / (float)N;
-    const float* w = p.weight ? p.weight + (size_t)(bh % p.H) * N : nullptr;
+    const float* w = p.weight ? p.weight + (size_t)(b.bh % p.H) * N : nullptr;
     float* part = p.part ? p.part + (size_t)blockIdx.x * 2 * N : nullptr;
     if (part)
         for (int i = threadIdx.x; i < N; i += kThreads) part[i] = part[N + i] = 0.f;
-    for (int t = t0; t < t1; ++t) {
-        const size_t r = (size_t)bh * p.T + t;
+    for (int t = b.t0; t < b.t1; ++t) {
+        const size_t r = (size_t)b.bh * p.T + t;
         const X* x = static_cast<const X*>(p.x) + r * N;
-        const Y* dy = static_cast<const Y*>(p.dy) + token_row(p, r) * N;
+        const Y* dy = static_cast<const Y*>(p.dy) + token_row(p, b.bh, t) * N;
         DX* dx = static_cast<DX*>(p.dx) + r * N;
         const float m = p.rms ? 0.f : p.mean[r], rs = p.rstd[r];
         float s1 = 0.f, s2 = 0.f;
@@ -357,12 +455,8 @@ __global__ void __launch_bounds__(kThreads) m2rnn_norm_bwd_long_kernel(const Nor
     }
 }
 
-unsigned capped(size_t want, int per_sm) {
-    const size_t cap = (size_t)kNumSMs * per_sm;
-    return (unsigned)(want < cap ? want : cap);
-}
-
-// Which layout a row length takes: f<VEC, LPR, CH>(), or false for rows too long for registers.
+// Which layout a row length takes, f<VEC, LPR, CH>(), or false for rows too
+// long for registers.
 template <class F>
 bool by_length(int N, F&& f) {
     if (N % 8 == 0) {   // rows start on 16 bytes in both types
@@ -384,6 +478,20 @@ bool by_length(int N, F&& f) {
     }
     return true;
 }
+// Rows at a time: up to 32 values a thread forward, 16 (of x and of dy) backward.
+constexpr int unroll_fwd(int values) { return values >= 32 ? 1 : values >= 16 ? 2 : 4; }
+constexpr int unroll_bwd(int values) { return values >= 16 ? 1 : 2; }
+
+unsigned capped(size_t want, int per_sm) {
+    const size_t cap = (size_t)kNumSMs * per_sm;
+    return (unsigned)(want < cap ? want : cap);
+}
+
+#ifdef LA_TUNE
+int norm_tune(const char* n, int d) { const char* e = getenv(n); return e ? atoi(e) : d; }
+#else
+constexpr int norm_tune(const char*, int d) { return d; }
+#endif
 
 template <class X, class Y>
 struct Fwd {
@@ -391,8 +499,9 @@ struct Fwd {
     cudaStream_t s;
     template <int VEC, int LPR, int CH>
     void operator()() {
-        const size_t rows = (size_t)p.B * p.H * p.T, want = (rows + kThreads / LPR - 1) / (kThreads / LPR);
-        m2rnn_norm_fwd_kernel<X, Y, VEC, LPR, CH><<<capped(want, 64), kThreads, 0, s>>>(p);
+        constexpr int U = unroll_fwd(VEC * CH), kRows = kThreads / LPR * U;
+        const size_t items = (size_t)p.B * p.H * ((p.T + kRows - 1) / kRows);
+        m2rnn_norm_fwd_kernel<X, Y, VEC, LPR, CH, U><<<capped(items, norm_tune("LN_F", 2)), kThreads, 0, s>>>(p);
     }
 };
 template <class X, class Y, class DX>
@@ -401,14 +510,14 @@ struct Bwd {
     cudaStream_t s;
     template <int VEC, int LPR, int CH>
     void operator()() {
-        m2rnn_norm_bwd_kernel<X, Y, DX, VEC, LPR, CH><<<p.B * p.H * p.chunks, kThreads, 0, s>>>(p);
+        m2rnn_norm_bwd_kernel<X, Y, DX, VEC, LPR, CH, unroll_bwd(VEC * CH)><<<p.B * p.H * p.chunks, kThreads, 0, s>>>(p);
     }
 };
 
 template <class X, class Y>
 cudaError_t fwd(const NormParams& p, cudaStream_t s) {
     if (!by_length(p.N, Fwd<X, Y>{p, s}))
-        m2rnn_norm_fwd_long_kernel<X, Y><<<capped((size_t)p.B * p.H * p.T, 8), kThreads, 0, s>>>(p);
+        m2rnn_norm_fwd_long_kernel<X, Y><<<p.B * p.H * p.chunks, kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 template <class X, class Y, class DX>
@@ -423,22 +532,28 @@ cudaError_t bwd_x(const NormParams& p, cudaStream_t s) {
     return p.dx_fp32 ? bwd<float, Y, float>(p, s) : bwd<float, Y, __nv_bfloat16>(p, s);
 }
 
+// Row blocks of each (b, h): at most `ctas` CTAs in all where there are fewer
+// pairs (one wave), each with at least
+// `least` times the rows that it takes at a time.
+int chunks_for(int B, int H, int T, int N, int ctas, int least) {
+    const int lanes = N % 8 ? (N <= 256 ? 32 : 256) : N <= 256 ? (N + 7) / 8 : N <= 1024 ? 32 : 256;
+    const int at_once = kThreads / lanes;
+    const long long pairs = (long long)B * H;
+    long long chunks = ctas / pairs, most = T / ((long long)least * at_once);
+    if (chunks > most) chunks = most;
+    return (int)(chunks < 1 ? 1 : chunks);
+}
+
 }  // namespace
 
-cudaError_t launch_norm_fwd(const NormParams& p, cudaStream_t s) {
+cudaError_t launch_norm_fwd(const NormParams& q, cudaStream_t s) {
+    NormParams p = q;
+    p.chunks = chunks_for(p.B, p.H, p.T, p.N, 8 * kNumSMs, 1)   /* rows too long for registers */;
     if (p.x_fp32) return p.y_fp32 ? fwd<float, float>(p, s) : fwd<float, __nv_bfloat16>(p, s);
     return p.y_fp32 ? fwd<__nv_bfloat16, float>(p, s) : fwd<__nv_bfloat16, __nv_bfloat16>(p, s);
 }
 
-int norm_bwd_chunks(int B, int H, int T, int N) {
-    // about four CTAs for each SM, and at least 8 of its row groups for a CTA
-    const int lanes = N <= 256 ? (N + 7) / 8 : N <= 1024 ? 32 : 256;
-    const int rows_at_once = kThreads / (lanes < 1 ? 1 : lanes);
-    const long long pairs = (long long)B * H;
-    long long chunks = (4LL * kNumSMs + pairs - 1) / pairs, most = T / (8LL * (rows_at_once < 1 ? 1 : rows_at_once));
-    if (chunks > most) chunks = most;
-    return (int)(chunks < 1 ? 1 : chunks);
-}
+int norm_bwd_chunks(int B, int H, int T, int N) { return chunks_for(B, H, T, N, norm_tune("LN_B", 2) * kNumSMs, 4); }
 
 cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s) {
     cudaError_t e = p.y_fp32 ? bwd_x<float>(p, s) : bwd_x<__nv_bfloat16>(p, s);
