@@ -240,49 +240,98 @@ def decay_logit_bias(H: int, tau_min: float = 2.0, tau_max: float = 256.0) -> to
 
 # ------------------------------------------------------------------ linear attention
 
-def _la_dims(k, v, q, f, f_is_logit) -> "_lib.LaDims":
-    """Checks k, v, q and f of a call and gives its dims."""
-    if k.dim() != 4 or v.dim() != 4:
-        raise ValueError("k and v must have 4 dimensions (batch, heads, tokens, width), got %d and %d" % (k.dim(), v.dim()))
-    B, G, T, K = k.shape
-    H, V = v.shape[1], v.shape[3]
-    if G != H and (G < 1 or H % G != 0):
-        raise ValueError("k has %d heads: it must have H = %d heads or a divisor of H" % (G, H))
-    dev, lp = k.device, k.dtype
-    mode = _mode(k)
-    _check("k", k, (B, G, T, K), lp, dev)
-    _check("v", v, (B, H, T, V), lp, dev)
-    _check("q", q, (B, G, T, K), lp, dev)
-    per_head = f.dim() == 1
-    _check("f", f, (H,) if per_head else (B, H, T), torch.float32, dev)
-    return _lib.LaDims(B, H, T, K, V, mode, G if G != H else 0, int(bool(f_is_logit)), int(per_head))
+# What a call needs besides its tensors, by its shape and flags: the C dims and
+# the bytes of workspace forward and backward.  (A decode step takes a few
+# microseconds on the GPU; asking again each time costs as much on the host.)
+_la_plans: Dict[tuple, tuple] = {}
 
 
-def _scratch(need: int, device, what: str) -> Optional[torch.Tensor]:
-    """Workspace of one call, from torch's allocator: calls on different
-    streams, and captured graphs, never share one."""
-    if need == _lib.REFUSED:
-        raise M2RNNError(_lib.ERR_UNSUPPORTED_SHAPE, what)
-    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+def _la_plan(B, H, G, T, K, V, mode, f_is_logit, per_head):
+    key = (B, H, G, T, K, V, mode, f_is_logit, per_head)
+    plan = _la_plans.get(key)
+    if plan is None:
+        if G != H and (G < 1 or H % G != 0):
+            raise ValueError("k has %d heads: it must have H = %d heads or a divisor of H" % (G, H))
+        d = _lib.LaDims(B, H, T, K, V, mode, G if G != H else 0, int(f_is_logit), int(per_head))
+        L = _lib.lib()
+        plan = (d, L.m2rnn_linear_attention_workspace(d, 0), L.m2rnn_linear_attention_workspace(d, 1))
+        if plan[1] == _lib.REFUSED:
+            raise M2RNNError(_lib.ERR_UNSUPPORTED_SHAPE, "m2rnn_linear_attention (K = %d, V = %d)" % (K, V))
+        if len(_la_plans) >= 4096:
+            _la_plans.clear()
+        _la_plans[key] = plan
+    return plan
 
 
-def _output(out: dict, name: str, shape, dtype, device) -> torch.Tensor:
-    t = out.get(name)
+def _same(name, t, shape, dtype, device):
+    """_check, in one expression where nothing is wrong."""
+    if not (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous() and t.is_cuda):
+        _check(name, t, shape, dtype, device)
+
+
+def _out(out, name, like, shape, dtype):
+    """The buffer out[name], checked, or a new one on like's device."""
+    t = None if out is None else out.get(name)
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check(name, t, shape, dtype, device)
+        return like.new_empty(shape, dtype=dtype)
+    _same(name, t, shape, dtype, like.device)
     return t
+
+
+def _scratch(need: int, like) -> Tuple[Optional[torch.Tensor], int]:
+    """Workspace of one call and its address, from torch's allocator: calls on
+    different streams, and captured graphs, never share one."""
+    if not need:
+        return None, 0
+    t = like.new_empty(need, dtype=torch.uint8)
+    return t, t.data_ptr()
+
+
+# The current stream's handle and the current device by the calls beneath
+# torch.cuda.current_stream and current_device, whose Python objects cost 3 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(what: str, device, fn, *args) -> None:
     """Calls the library on the device of the tensors, on its current stream."""
-    if device.index is not None and device.index != torch.cuda.current_device():
+    index = device.index
+    if index != _raw_device():
         with torch.cuda.device(device):
-            st = fn(*args, _stream(device))
+            st = fn(*args, _raw_stream(index))
     else:
-        st = fn(*args, _stream(device))
+        st = fn(*args, _raw_stream(index))
     if st != _lib.OK:
         raise M2RNNError(st, what)
+
+
+def _la_inputs(k, v, q, f, S, f_is_logit, tokens):
+    """Checks the inputs of a call (tokens: 4-dimensional k, q, v; else one
+    token's, 3-dimensional) and gives its plan."""
+    dims = 4 if tokens else 3
+    if k.dim() != dims or v.dim() != dims:
+        raise ValueError("k and v must have %d dimensions (batch, heads, %swidth), got %d and %d"
+                         % (dims, "tokens, " if tokens else "", k.dim(), v.dim()))
+    if tokens:
+        B, G, T, K = k.shape
+        _, H, _, V = v.shape
+        vs, fs = (B, H, T, V), (B, H, T)
+    else:
+        B, G, K = k.shape
+        _, H, V = v.shape
+        T, vs, fs = 1, (B, H, V), (B, H)
+    dev, lp = k.device, k.dtype
+    mode = _mode(k)
+    per_head = f.dim() == 1
+    plan = _la_plan(B, H, G, T, K, V, mode, bool(f_is_logit), per_head)
+    _same("k", k, k.shape, lp, dev)
+    _same("v", v, vs, lp, dev)
+    _same("q", q, k.shape, lp, dev)
+    _same("f", f, (H,) if per_head else fs, torch.float32, dev)
+    if S is not None:
+        _same("S0", S, (B, H, K, V), torch.float32, dev)
+    return plan, B, H, T, K, V
 
 
 def linear_attention(k, v, q, f, S0=None, *, want_ST: bool = True, want_ckpt: bool = False,
@@ -295,20 +344,15 @@ def linear_attention(k, v, q, f, S0=None, *, want_ST: bool = True, want_ckpt: bo
     constant for each head; S0 [B, H, K, V] fp32 (None: zeros).  y has the
     inputs' type, ST [B, H, K, V] is fp32.  ckpt [B, H, ceil(T/128), V/4, K, 4]
     holds the states that linear_attention_backward starts from (element (i, j)
-    of a state at [j // 4, i, j % 4]).  `out` may
-    hold buffers for y, ST and ckpt; ST may be S0's."""
-    d = _la_dims(k, v, q, f, f_is_logit)
-    dev, lp = k.device, k.dtype
-    B, H, T, K, V = d.B, d.H, d.T, d.K, d.V
-    _check("S0", S0, (B, H, K, V), torch.float32, dev)
-    out = out or {}
-    y = _output(out, "y", (B, H, T, V), lp, dev)
-    ST = _output(out, "ST", (B, H, K, V), torch.float32, dev) if want_ST else None
-    ckpt = _output(out, "ckpt", (B, H, num_checkpoints(T, LA_CHUNK), V // 4, K, 4), torch.float32, dev) if want_ckpt else None
-    L = _lib.lib()
-    ws = _scratch(L.m2rnn_linear_attention_workspace(d, 0), dev, "m2rnn_linear_attention_forward")
-    _call("m2rnn_linear_attention_forward", dev, L.m2rnn_linear_attention_forward, d, _ptr(k), _ptr(v), _ptr(q),
-          _ptr(f), _ptr(S0), _ptr(y), _ptr(ST), _ptr(ckpt), _ptr(ws), ws.numel() if ws is not None else 0)
+    of a state at [j // 4, i, j % 4]).  `out` may hold buffers for y, ST and
+    ckpt; ST may be S0's."""
+    (d, need, _), B, H, T, K, V = _la_inputs(k, v, q, f, S0, f_is_logit, True)
+    y = _out(out, "y", k, (B, H, T, V), k.dtype)
+    ST = _out(out, "ST", k, (B, H, K, V), torch.float32) if want_ST else None
+    ckpt = _out(out, "ckpt", k, (B, H, num_checkpoints(T, LA_CHUNK), V // 4, K, 4), torch.float32) if want_ckpt else None
+    ws, wp = _scratch(need, k)
+    _call("m2rnn_linear_attention_forward", k.device, _lib.lib().m2rnn_linear_attention_forward, d, k.data_ptr(),
+          v.data_ptr(), q.data_ptr(), f.data_ptr(), _ptr(S0), y.data_ptr(), _ptr(ST), _ptr(ckpt), wp, need)
     return y, ST, ckpt
 
 
@@ -319,12 +363,19 @@ def linear_attention_step(k, v, q, f, S, *, ST: Optional[torch.Tensor] = None, y
     where that is given.  Returns y [B, H, V]."""
     if S is None:
         raise ValueError("linear_attention_step needs the state buffer S")
-    if k.dim() != 3 or v.dim() != 3:
-        raise ValueError("k and v of a step must have 3 dimensions (batch, heads, width), got %d and %d" % (k.dim(), v.dim()))
-    yb = None if y is None else y.unsqueeze(2)
-    o = linear_attention(k.unsqueeze(2), v.unsqueeze(2), q.unsqueeze(2), f if f.dim() == 1 else f.unsqueeze(2), S,
-                         f_is_logit=f_is_logit, out={"y": yb, "ST": S if ST is None else ST})[0]
-    return o.squeeze(2) if y is None else y
+    (d, need, _), B, H, _, K, V = _la_inputs(k, v, q, f, S, f_is_logit, False)
+    if ST is None:
+        ST = S
+    else:
+        _same("ST", ST, (B, H, K, V), torch.float32, k.device)
+    if y is None:
+        y = k.new_empty((B, H, V))
+    else:
+        _same("y", y, (B, H, V), k.dtype, k.device)
+    ws, wp = _scratch(need, k)
+    _call("m2rnn_linear_attention_forward", k.device, _lib.lib().m2rnn_linear_attention_forward, d, k.data_ptr(),
+          v.data_ptr(), q.data_ptr(), f.data_ptr(), S.data_ptr(), y.data_ptr(), ST.data_ptr(), None, wp, need)
+    return y
 
 
 def linear_attention_backward(k, v, q, f, ckpt, dy, dST=None, *, f_is_logit: bool = False,
@@ -332,25 +383,23 @@ def linear_attention_backward(k, v, q, f, ckpt, dy, dST=None, *, f_is_logit: boo
     """Gradients of linear_attention from the checkpoints of its forward.
     Returns dict dk, dv, dq (the inputs' type), df (fp32, f's shape), dS0 (fp32).
     dk and dq of shared k and q are the sums over each group's heads."""
-    d = _la_dims(k, v, q, f, f_is_logit)
+    (d, _, need), B, H, T, K, V = _la_inputs(k, v, q, f, None, f_is_logit, True)
     dev, lp = k.device, k.dtype
-    B, H, T, K, V = d.B, d.H, d.T, d.K, d.V
-    G = d.qk_heads or H
-    _check("dy", dy, (B, H, T, V), lp, dev)
-    _check("dST", dST, (B, H, K, V), torch.float32, dev)
+    _same("dy", dy, (B, H, T, V), lp, dev)
+    if dST is not None:
+        _same("dST", dST, (B, H, K, V), torch.float32, dev)
     if ckpt is None:
         raise ValueError("linear_attention_backward needs the checkpoints of linear_attention(..., want_ckpt=True)")
-    _check("ckpt", ckpt, (B, H, num_checkpoints(T, LA_CHUNK), V // 4, K, 4), torch.float32, dev)
-    out = dict(out or {})
-    for n, shape, t in (("dk", (B, G, T, K), lp), ("dv", (B, H, T, V), lp), ("dq", (B, G, T, K), lp),
-                        ("df", tuple(f.shape), torch.float32), ("dS0", (B, H, K, V), torch.float32)):
-        out[n] = _output(out, n, shape, t, dev)
-    L = _lib.lib()
-    ws = _scratch(L.m2rnn_linear_attention_workspace(d, 1), dev, "m2rnn_linear_attention_backward")
-    _call("m2rnn_linear_attention_backward", dev, L.m2rnn_linear_attention_backward, d, _ptr(k), _ptr(v), _ptr(q),
-          _ptr(f), _ptr(ckpt), _ptr(dy), _ptr(dST), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dq"]),
-          _ptr(out["df"]), _ptr(out["dS0"]), _ptr(ws), ws.numel() if ws is not None else 0)
-    return out
+    _same("ckpt", ckpt, (B, H, num_checkpoints(T, LA_CHUNK), V // 4, K, 4), torch.float32, dev)
+    g = dict(out or {})
+    for n, shape, t in (("dk", k.shape, lp), ("dv", v.shape, lp), ("dq", k.shape, lp), ("df", f.shape, torch.float32),
+                        ("dS0", (B, H, K, V), torch.float32)):
+        g[n] = _out(g, n, k, shape, t)
+    ws, wp = _scratch(need, k)
+    _call("m2rnn_linear_attention_backward", dev, _lib.lib().m2rnn_linear_attention_backward, d, k.data_ptr(),
+          v.data_ptr(), q.data_ptr(), f.data_ptr(), ckpt.data_ptr(), dy.data_ptr(), _ptr(dST), g["dk"].data_ptr(),
+          g["dv"].data_ptr(), g["dq"].data_ptr(), g["df"].data_ptr(), g["dS0"].data_ptr(), wp, need)
+    return g
 
 
 # ------------------------------------------------------------------ layer norm
@@ -360,8 +409,8 @@ _NORM_TYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 def _norm_shape(x, weight, bias):
     """(B, H, T, N) of a call, and whether x is a head-first readout."""
-    params = [t for t in (weight, bias) if t is not None]
-    heads = bool(params) and params[0].dim() == 2
+    first = weight if weight is not None else bias
+    heads = first is not None and first.dim() == 2
     if x.dtype not in _NORM_TYPES:
         raise TypeError("x must be bfloat16 or float32, got %s" % x.dtype)
     if heads:
@@ -375,9 +424,15 @@ def _norm_shape(x, weight, bias):
         B, H, T = 1, 1, x.numel() // N if N else 0
     if N < 1:
         raise ValueError("the last dimension of x is empty")
-    _check("x", x, x.shape, x.dtype, x.device)
-    for n, t in (("weight", weight), ("bias", bias)):
-        _check(n, t, (H, N) if heads else (N,), torch.float32, x.device)
+    if T >= 1 << 31:
+        raise ValueError("x has %d rows: at most 2^31 - 1 in one call" % T)
+    dev = x.device
+    _same("x", x, x.shape, x.dtype, dev)
+    ps = (H, N) if heads else (N,)
+    if weight is not None:
+        _same("weight", weight, ps, torch.float32, dev)
+    if bias is not None:
+        _same("bias", bias, ps, torch.float32, dev)
     return B, H, T, N, heads
 
 
@@ -393,18 +448,16 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = Fals
     (x's by default).  mean and rstd (fp32, x's leading shape) feed
     layer_norm_backward.  `out` may hold buffers for y, mean and rstd."""
     B, H, T, N, heads = _norm_shape(x, weight, bias)
-    dev = x.device
     yt = x.dtype if out_dtype is None else out_dtype
     if yt not in _NORM_TYPES:
         raise TypeError("out_dtype must be bfloat16 or float32, got %s" % yt)
-    out = out or {}
-    lead = tuple(x.shape[:-1])
-    y = _output(out, "y", (B, T, H, N) if heads else tuple(x.shape), yt, dev)
-    rstd = _output(out, "rstd", lead, torch.float32, dev)
-    mean = None if rms else _output(out, "mean", lead, torch.float32, dev)
-    d = _lib.NormDims(B, H, T, N, _NORM_TYPES[x.dtype], _NORM_TYPES[yt], 0, int(bool(rms)), eps)
-    _call("m2rnn_layer_norm_forward", dev, _lib.lib().m2rnn_layer_norm_forward, d, _ptr(x), _ptr(weight), _ptr(bias),
-          _ptr(y), _ptr(mean), _ptr(rstd))
+    lead = x.shape[:-1]
+    y = _out(out, "y", x, (B, T, H, N) if heads else x.shape, yt)
+    rstd = _out(out, "rstd", x, lead, torch.float32)
+    mean = None if rms else _out(out, "mean", x, lead, torch.float32)
+    d = _lib.NormDims(B, H, T, N, _NORM_TYPES[x.dtype], _NORM_TYPES[yt], 0, 1 if rms else 0, eps)
+    _call("m2rnn_layer_norm_forward", x.device, _lib.lib().m2rnn_layer_norm_forward, d, x.data_ptr(), _ptr(weight),
+          _ptr(bias), y.data_ptr(), _ptr(mean), rstd.data_ptr())
     return y, mean, rstd
 
 
@@ -423,20 +476,24 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, rms: bool = False, heads: 
     dt = x.dtype if dx_dtype is None else dx_dtype
     if dy.dtype not in _NORM_TYPES or dt not in _NORM_TYPES or (dt == torch.float32 and x.dtype != torch.float32):
         raise TypeError("dy must be bfloat16 or float32 and dx bfloat16 or x's type, got %s and %s" % (dy.dtype, dt))
-    _check("dy", dy, (B, T, H, N) if per_head else tuple(x.shape), dy.dtype, dev)
-    lead = tuple(x.shape[:-1])
+    _same("dy", dy, (B, T, H, N) if per_head else x.shape, dy.dtype, dev)
+    lead = x.shape[:-1]
     if rstd is None or (mean is None and not rms):
         raise ValueError("layer_norm_backward needs the forward's rstd, and its mean unless rms=True")
-    _check("rstd", rstd, lead, torch.float32, dev)
-    _check("mean", None if rms else mean, lead, torch.float32, dev)
-    out = dict(out or {})
+    _same("rstd", rstd, lead, torch.float32, dev)
+    if not rms:
+        _same("mean", mean, lead, torch.float32, dev)
+    g = dict(out or {})
     shape = (H, N) if per_head else (N,)
-    for n, sh, t in (("dx", tuple(x.shape), dt), ("dweight", shape, torch.float32), ("dbias", shape, torch.float32)):
-        out[n] = _output(out, n, sh, t, dev)
-    d = _lib.NormDims(B, H, T, N, _NORM_TYPES[x.dtype], _NORM_TYPES[dy.dtype], _NORM_TYPES[dt], int(bool(rms)), 0.0)
+    for n, sh, t in (("dx", x.shape, dt), ("dweight", shape, torch.float32), ("dbias", shape, torch.float32)):
+        g[n] = _out(g, n, x, sh, t)
+    d = _lib.NormDims(B, H, T, N, _NORM_TYPES[x.dtype], _NORM_TYPES[dy.dtype], _NORM_TYPES[dt], 1 if rms else 0, 0.0)
     L = _lib.lib()
-    ws = _scratch(L.m2rnn_layer_norm_workspace(d), dev, "m2rnn_layer_norm_backward")
-    _call("m2rnn_layer_norm_backward", dev, L.m2rnn_layer_norm_backward, d, _ptr(dy), _ptr(x), _ptr(weight),
-          None if rms else _ptr(mean), _ptr(rstd), _ptr(out["dx"]), _ptr(out["dweight"]), _ptr(out["dbias"]),
-          _ptr(ws), ws.numel() if ws is not None else 0)
-    return out
+    need = L.m2rnn_layer_norm_workspace(d)
+    if need == _lib.REFUSED:
+        raise M2RNNError(_lib.ERR_UNSUPPORTED_SHAPE, "m2rnn_layer_norm_backward")
+    ws, wp = _scratch(need, x)
+    _call("m2rnn_layer_norm_backward", dev, L.m2rnn_layer_norm_backward, d, dy.data_ptr(), x.data_ptr(), _ptr(weight),
+          None if rms else mean.data_ptr(), rstd.data_ptr(), g["dx"].data_ptr(), g["dweight"].data_ptr(),
+          g["dbias"].data_ptr(), wp, need)
+    return g

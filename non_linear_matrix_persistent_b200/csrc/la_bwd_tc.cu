@@ -112,9 +112,9 @@ __device__ __forceinline__ float column_sums(float (&r)[N]) {
 // tensor memory and, dP'ᵀ, to its place `dp(column)` in shared memory; returns
 // the source's sum of paths into the block, and leaves in cut[] by gate u the
 // sums over the warp's sources before u of the paths to sinks u.. of the block.
-// DIAG: the source's own block (sinks t >= s, an exponential each); otherwise
-// the decay is r·c[t].  ZERO: the chunk has gates at the floor, paths through
-// which count for df alone.
+// The decay is r·c[t].  DIAG: the source's own block, sinks t >= s.  ZERO: the
+// chunk has gates at the floor, paths through which count for df alone, or
+// blocks too steep for the product: the diagonal takes an exponential each.
 template <bool DIAG, bool ZERO, int NSUM, class Place>
 __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const LaTablesZ* tab, int t0, float Fs, float Is,
                                              float Zs, float r, float* cut, Place dp) {
@@ -129,7 +129,7 @@ __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const La
         float d[16], z[ZERO ? 16 : 1];
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
-            if constexpr (DIAG) {
+            if constexpr (DIAG && ZERO) {
                 const float4 f = *reinterpret_cast<const float4*>(&tab->F[t0 + h + e]);
                 const float4 w = *reinterpret_cast<const float4*>(&tab->I[t0 + h + e]);
                 d[e] = ex2_approx((f.x - Fs) + (w.x - Is)); d[e + 1] = ex2_approx((f.y - Fs) + (w.y - Is));
@@ -139,6 +139,9 @@ __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const La
             } else {
                 const float4 c = *reinterpret_cast<const float4*>(&tab->c[t0 + h + e]);
                 d[e] = r * c.x; d[e + 1] = r * c.y; d[e + 2] = r * c.z; d[e + 3] = r * c.w;
+                if constexpr (DIAG)
+#pragma unroll
+                    for (int o = 0; o < 4; ++o) d[e + o] = h + e + o >= lane ? d[e + o] : 0.f;
             }
             if constexpr (ZERO) {
                 const float4 zs = *reinterpret_cast<const float4*>(&tab->Z[t0 + h + e]);
@@ -705,9 +708,11 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 float* cut = sc->cut[quarter];
                 auto place = [&](int col) { return dp + tile_at(col); };
                 const bool diag = wg == quarter;
-                const float r = diag ? 1.f : ex2_approx((tab->F[wg * 32 - 1] - Ft) + (tab->I[wg * 32 - 1] - It));
+                // the decay from the source to the block before the sinks' (for its own block, a reciprocal)
+                const float Fp = wg ? tab->F[wg * 32 - 1] : 0.f, Ip = wg ? tab->I[wg * 32 - 1] : 0.f;
+                const float r = ex2_approx((Fp - Ft) + (Ip - It));
                 constexpr int N = C::NS <= 16 ? 32 : 16;   // registers
-                if (Ze != 0.f)
+                if (Ze != 0.f || tab->steep != 0.f)
                     run = diag ? score_block<true, true, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, cut, place)
                                : score_block<false, true, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, cut, place);
                 else

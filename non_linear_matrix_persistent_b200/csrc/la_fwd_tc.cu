@@ -20,9 +20,11 @@
 // keeps fp32 accuracy over any number of chunks.
 //
 // Decays without an exponential per score: for a row t and a block of 32
-// columns left of its own, D_ts = 2^(L_t - L_e)·2^(L_e - L_s) with e the
-// block's last token; both factors are at most 1 and the second is shared by
-// all rows.  Only the diagonal blocks take one exponential per score.
+// columns, D_ts = 2^(L_t - L_e)·2^(L_e - L_s) with e the block's last token.
+// The second factor is shared by all rows.  Left of the diagonal both are at
+// most 1; in the diagonal block the first is the reciprocal of a decay, within
+// fp32's range unless the block decays by more than 2^-90: such chunks take one
+// exponential per score there.
 #include <cstdlib>
 #include <mutex>
 
@@ -357,15 +359,18 @@ __global__ void __launch_bounds__(Cfg<KP, VP, NW>::kThreads, Cfg<KP, VP, NW>::kC
                         tmem_ld_32x32b<32>(tmem + lanes + j * 32, sc);
                         tc_wait_ld();
                         reg_fence(sc);
-                        if (j < quarter) {
+                        if (j < quarter || tab->steep == 0.f) {
                             const float r = ex2_approx((Ft - tab->F[j * 32 + 31]) + (It - tab->I[j * 32 + 31]));
+                            const int last = j < quarter ? 31 : lane;   // the row's last column of the block
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
                                 const float4 cs = *reinterpret_cast<const float4*>(&tab->c[j * 32 + e]);
-                                pk[e / 2] = pack_bf16(__uint_as_float(sc[e]) * (r * cs.x),
-                                                      __uint_as_float(sc[e + 1]) * (r * cs.y));
-                                pk[e / 2 + 1] = pack_bf16(__uint_as_float(sc[e + 2]) * (r * cs.z),
-                                                          __uint_as_float(sc[e + 3]) * (r * cs.w));
+                                const float2 lo2 = __fmul2_rn(__fmul2_rn(make_float2(r, r), make_float2(cs.x, cs.y)),
+                                                              make_float2(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1]))),
+                                             hi2 = __fmul2_rn(__fmul2_rn(make_float2(r, r), make_float2(cs.z, cs.w)),
+                                                              make_float2(__uint_as_float(sc[e + 2]), __uint_as_float(sc[e + 3])));
+                                pk[e / 2] = pack_bf16(e <= last ? lo2.x : 0.f, e + 1 <= last ? lo2.y : 0.f);
+                                pk[e / 2 + 1] = pack_bf16(e + 2 <= last ? hi2.x : 0.f, e + 3 <= last ? hi2.y : 0.f);
                             }
                         } else {
 #pragma unroll

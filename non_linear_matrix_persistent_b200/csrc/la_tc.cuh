@@ -44,8 +44,13 @@ __device__ __forceinline__ void la_log2(const LaParams& p, float x, float floor_
 // through the token, by one warp (4 tokens a lane): F + I in shared memory,
 // and c[t] = the decay from t to the last token of its block of 32 or, with
 // FROM_PREV, from the last token of the block before through t.
+// steep: some block of 32 decays by more than 2^-90.  Elsewhere the decay
+// between two tokens of one block is the product of a decay to the block's end
+// and the reciprocal of another, both far inside fp32's range: c[] serves the
+// diagonal blocks too.
 struct LaTables {
     float F[128], I[128], c[128];
+    float steep, pad[3];
 };
 struct LaTablesZ : LaTables {
     float Z[128];   // gates at the floor, from the chunk's start through the token
@@ -86,6 +91,12 @@ __device__ __forceinline__ void la_tables(Tab* tab, const LaParams& p, const flo
     // the block's last token, or the one before the block
     float fe = __shfl_sync(~0u, F[3], FROM_PREV ? (lane & ~7) - 1 : lane | 7),
           we = __shfl_sync(~0u, I[3], FROM_PREV ? (lane & ~7) - 1 : lane | 7);
+    {
+        const float pe = __shfl_sync(~0u, F[3] + I[3], lane < 8 ? 0 : (lane & ~7) - 1),
+                    ee = __shfl_sync(~0u, F[3] + I[3], lane | 7);
+        const bool any = __any_sync(~0u, !(ee - (lane < 8 ? 0.f : pe) > -90.f));
+        if (lane == 0) tab->steep = any ? 1.f : 0.f;
+    }
     float sign = 1.f;
     if (FROM_PREV) {
         if (lane < 8) { fe = 0.f; we = 0.f; }
