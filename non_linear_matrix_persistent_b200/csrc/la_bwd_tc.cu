@@ -50,8 +50,10 @@ static_assert(sizeof(DfScratch) <= kTileBytes, "scratch");
 // Two schedules.  Up to 64 x 128 and 128 x 64 (kRoomy) the terms of S, of G
 // and of a q have shared memory of their own: both states' products run while
 // the scores are worked on, and the sum for G while the outputs' products do.
-// For 128 x 128 the terms of S, then those of G, share two buffers and the
-// place of dP', and those of a q take tiles that are no longer read.
+// For 128 x 128 the terms of S, then those of G, then those of a q share two
+// buffers and the place of dP'; dq, dk and dv go to global memory from
+// registers, so that the next tiles are fetched as soon as a q has been formed
+// and nothing waits for staged outputs to leave.
 template <int KP, int VP>
 struct BCfg {
     static constexpr int NW = 16, kThreads = (NW + 3) * 32;
@@ -70,9 +72,8 @@ struct BCfg {
     static constexpr int kBars = 19;
     static constexpr int kSmem = kOffBar + kBars * 8 + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory");
-    static_assert(kX >= (kRoomy ? 3 : 1) * kQ && kOp <= 2 * kTileBytes, "terms of a q; third terms");
-    // where the terms of S, G and a q go, from kOffX; for the tight schedule
-    // the third terms of S and G at kOffP and a q's first two over q and k
+    static_assert(kX >= (kRoomy ? 3 : 2) * kQ && kOp <= 2 * kTileBytes, "terms of a q; third terms");
+    // where the terms of G go, from kOffX; without room the third terms are at kOffP
     static constexpr int kG0 = kRoomy ? 3 * kOp : 0;
     // Tensor memory: the two score matrices, dq, dk, dv and the sum for G.
     // Where the last two do not fit beside the others they go over dY·Vᵀ once
@@ -213,6 +214,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 18; ++i) mbar_init(bar(i), 1);
         for (uint32_t b : {r_s, r_g, r_p, r_dv, r_aq, r_out}) mbar_init(b, NW);   // one arrival a warp
+        if (!C::kRoomy) mbar_init(b_full, 2);   // dy comes later than the other tiles
         *abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 if (lane == 0) {
 #pragma unroll
                     for (int x = 0; x < 3; ++x) {       // the terms of a q
-                        const uint32_t op = C::kRoomy ? X + x * (C::kQ >> 4) : x == 0 ? q : x == 1 ? k : X;
+                        const uint32_t op = x < 2 || C::kRoomy ? X + x * (C::kQ >> 4) : XP;
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
                             tc_mma_f16_ss(tmem + C::kDG, d_mn + op + ks * 128, d_mn + dy + ks * 128, id_dg,
@@ -354,16 +356,24 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
         // ------------------------------------------------------ copies
         if (lane == 0) {
             const int qk = la_qk_pair(p, bh);
-            int loaded = 0;
-            auto load = [&](int i) {
+            int loaded = 0, started = 0;   // chunks whose every load, whose first load has been issued
+            auto load = [&](int i, bool rest, bool dys) {   // the q, k and v tiles, the dy tile
                 if (p.fault == 1 && i > 0) return;   // injected: the copies stop after the first chunk
-                loaded = i + 1;
+                if (rest) started = i + 1;
+                if (dys) loaded = i + 1;
                 const int t = chunk_of(i) * kLaChunk;
                 const uint32_t base = sbase + stage_of(i) * C::kStage, full = b_full + stage_of(i) * 8;
-                mbar_arrive_expect_tx(full, C::kStage);
+                if (C::kRoomy) {
+                    mbar_arrive_expect_tx(full, C::kStage);
+                } else {
+                    if (rest) mbar_arrive_expect_tx(full, C::kStage - C::kV);
+                    if (dys) mbar_arrive_expect_tx(full, C::kV);
+                }
+                if (dys)
 #pragma unroll
-                for (int x = 0; x < VP / 64; ++x)
-                    tma_tile(base + 2 * C::kQ + C::kV + x * kTileBytes, &maps.dy, x * 64, t, bh, full);
+                    for (int x = 0; x < VP / 64; ++x)
+                        tma_tile(base + 2 * C::kQ + C::kV + x * kTileBytes, &maps.dy, x * 64, t, bh, full);
+                if (!rest) return;
 #pragma unroll
                 for (int x = 0; x < KP / 64; ++x) {
                     tma_tile(base + x * kTileBytes, &maps.q, x * 64, t, qk, full);
@@ -389,12 +399,19 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
 #pragma unroll
                 for (int x = 0; x < VP / 64; ++x) tma_prefetch_tile(&maps.v, x * 64, t, bh);
             };
-            for (int i = 0; i < C::kStages && i < n; ++i) load(i);
+            for (int i = 0; i < C::kStages && i < n; ++i) load(i, true, true);
             prefetch(1);
             bool ok = true;
             int i = 0;
             for (; i < n; ++i) {
                 prefetch(i + 2);
+                if (!C::kRoomy) {
+                    if (!(ok = la_wait(r_aq, i & 1, abort_flag, limit) && la_wait(r_df, i & 1, abort_flag, limit))) break;
+                    if (i + 1 < n) load(i + 1, true, false);
+                    if (!(ok = la_wait(b_dg, i & 1, abort_flag, limit))) break;
+                    if (i + 1 < n) load(i + 1, false, true);
+                    continue;
+                }
                 const int ph = i & 1, t = chunk_of(i) * kLaChunk;
                 const uint32_t base = sbase + stage_of(i) * C::kStage;
                 if (!(ok = la_wait(r_out, ph, abort_flag, limit))) break;
@@ -412,10 +429,12 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 tma_store_wait_read();
                 mbar_arrive(b_free);
                 if (!(ok = la_wait(r_df, ph, abort_flag, limit))) break;
-                if (i + C::kStages < n) load(i + C::kStages);
+                if (i + C::kStages < n) load(i + C::kStages, true, true);
             }
-            if (!ok)   // leave no copy in flight
+            if (!ok) {   // leave no copy in flight
+                if (!C::kRoomy && loaded < started) load(started - 1, false, true);
                 for (int j = i; j < loaded; ++j) la_drain(b_full + stage_of(j) * 8, stage_phase(j), limit);
+            }
         }
         __syncwarp();
     } else if (warp == NW + 2) {
@@ -586,18 +605,13 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             arrive(r_s);
         };
         load_S(chunk_of(0));
-        if (C::kRoomy) put_S();
+        put_S();
         constexpr bool kLoadEarly = C::NS <= 16;   // registers
         auto tile_at = [&](int col) { return (col >> 6) * kTileBytes + sw128(row, (col & 63) >> 3); };
 
         for (int i = 0; i < n; ++i) {
             const int ph = i & 1, c = chunk_of(i);
             uint8_t* stage = smem + stage_of(i) * C::kStage;
-            if (!C::kRoomy) {
-                // (their place: the last chunk's products of terms are done, since its sum for G is)
-                if (i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
-                put_S();
-            }
             float gamma = gamma_next;
             if (kLoadEarly && i + 1 < n) load_S(chunk_of(i + 1));
             if (!la_wait(b_tab, ph, abort_flag, limit)) break;
@@ -676,6 +690,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             }
             if (!la_wait(b_sc, ph, abort_flag, limit)) break;
             tc_fence_after();
+            uint8_t* dp = smem + C::kOffP;
             // ---- a_t q_t in three terms
             auto put_aq = [&]() {
 #pragma unroll
@@ -688,14 +703,13 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                     split3(at * bf16lo_to_f32(x.z), at * bf16hi_to_f32(x.z), hi.z, mid.z, lo.z);
                     split3(at * bf16lo_to_f32(x.w), at * bf16hi_to_f32(x.w), hi.w, mid.w, lo.w);
                     uint8_t* X = smem + C::kOffX + pos;
-                    *reinterpret_cast<uint4*>(C::kRoomy ? X : stage + pos) = hi;
-                    *reinterpret_cast<uint4*>(C::kRoomy ? X + C::kQ : stage + C::kQ + pos) = mid;
-                    *reinterpret_cast<uint4*>(C::kRoomy ? X + 2 * C::kQ : X) = lo;
+                    *reinterpret_cast<uint4*>(X) = hi;
+                    *reinterpret_cast<uint4*>(X + C::kQ) = mid;
+                    *reinterpret_cast<uint4*>(C::kRoomy ? X + 2 * C::kQ : dp + pos) = lo;
                 }
                 arrive(r_aq);
             };
             // ---- P'ᵀ, dP'ᵀ and df's sums: source s = row, sinks of block wg
-            uint8_t* dp = smem + C::kOffP;
             float run = 0.f;
             if (wg < quarter) {   // sinks before the source
                 const uint32_t z[16] = {};
@@ -739,46 +753,68 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             if (!la_wait(b_out, ph, abort_flag, limit)) break;
             tc_fence_after();
             const int t = c * kLaChunk + row;
-            // ---- dq, over dP' or the v tile
-            auto rows_out = [&](uint32_t col0, void* out, uint32_t (&o)[C::NQ / 2]) {
-#pragma unroll
-                for (int j = 0; j < C::NQ; j += 16) {
-                    const int col = wg * C::NQ + j;
-                    uint32_t x[16];
-                    tmem_ld<16>(mylane + col0 + col, x);
-                    tc_wait_ld();
-                    reg_fence(x);
-                    if (p.dkq_fp32 && t < p.T && col < p.K) {   // per-head parts of a shared q's or k's gradient
-                        uint4* g = reinterpret_cast<uint4*>(static_cast<float*>(out) + ((size_t)bh * p.T + t) * p.K + col);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) g[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        o[j / 2 + e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-                }
-            };
-            {
-                uint32_t o[C::NQ / 2];
-                rows_out(C::kDQ, p.dq, o);
-#pragma unroll
-                for (int j = 0; j < C::NQ; j += 8)
-                    *reinterpret_cast<uint4*>((C::kOwnScratch ? stage + 2 * C::kQ : dp) + tile_at(wg * C::NQ + j)) =
-                        make_uint4(o[j / 2], o[j / 2 + 1], o[j / 2 + 2], o[j / 2 + 3]);
-            }
-            if (!C::kRoomy) put_aq();  // over q, over k, over the states' terms
-            // ---- dk and dv, kept until their tiles are free
-            uint32_t ok_[C::NQ / 2], ov[C::NV / 2];
-            rows_out(C::kDK, p.dk, ok_);
-#pragma unroll
-            for (int j = 0; j < C::NV; j += 16) {
-                uint32_t x[16];
-                tmem_ld<16>(mylane + C::kDV + wg * C::NV + j, x);
+            // 16 columns of dq, dk or dv: the per-head parts of a shared q's or k's gradient, or packed
+            auto take = [&](uint32_t col, uint32_t (&x)[16]) {
+                tmem_ld<16>(mylane + col, x);
                 tc_wait_ld();
                 reg_fence(x);
+            };
+            auto part_out = [&](void* out, int col, const uint32_t (&x)[16]) {
+                if (t >= p.T || col >= p.K) return;
+                uint4* g = reinterpret_cast<uint4*>(static_cast<float*>(out) + ((size_t)bh * p.T + t) * p.K + col);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            };
+            auto pack16 = [&](const uint32_t (&x)[16], uint32_t* o) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    ov[j / 2 + e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                    o[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+            };
+            auto stage_out = [&](uint8_t* tile, int col, const uint32_t* o) {
+                *reinterpret_cast<uint4*>(tile + tile_at(col)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(tile + tile_at(col + 8)) = make_uint4(o[4], o[5], o[6], o[7]);
+            };
+            // straight to the output, [pair][T][width] bf16
+            auto rows_out = [&](void* out, int width, int col, const uint32_t* o) {
+                if (t >= p.T || col >= width) return;
+                __nv_bfloat16* g = static_cast<__nv_bfloat16*>(out) + ((size_t)bh * p.T + t) * width + col;
+                if (p.out32) {
+                    st_global_v8(g, o);
+                } else {
+                    *reinterpret_cast<uint4*>(g) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(g + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+            };
+            uint32_t okk[C::kRoomy ? C::NQ / 2 : 8], ov[C::kRoomy ? C::NV / 2 : 8];
+            // ---- dq, by way of dP' or the v tile
+#pragma unroll
+            for (int j = 0; j < C::NQ; j += 16) {
+                const int col = wg * C::NQ + j;
+                uint32_t x[16], o[8];
+                take(C::kDQ + col, x);
+                if (p.dkq_fp32) part_out(p.dq, col, x);
+                pack16(x, o);
+                if (C::kRoomy) stage_out(C::kOwnScratch ? stage + 2 * C::kQ : dp, col, o);
+                else if (!p.dkq_fp32) rows_out(p.dq, p.K, col, o);
+            }
+            if (!C::kRoomy) put_aq();
+            // ---- dk and dv, kept until their tiles are free
+#pragma unroll
+            for (int j = 0; j < C::NQ; j += 16) {
+                const int col = wg * C::NQ + j;
+                uint32_t x[16];
+                take(C::kDK + col, x);
+                if (p.dkq_fp32) part_out(p.dk, col, x);
+                pack16(x, okk + (C::kRoomy ? j / 2 : 0));
+                if (!C::kRoomy && !p.dkq_fp32) rows_out(p.dk, p.K, col, okk);
+            }
+#pragma unroll
+            for (int j = 0; j < C::NV; j += 16) {
+                const int col = wg * C::NV + j;
+                uint32_t x[16];
+                take(C::kDV + col, x);
+                pack16(x, ov + (C::kRoomy ? j / 2 : 0));
+                if (!C::kRoomy) rows_out(p.dv, p.V, col, ov);
             }
             // ---- G = A G + the chunk's sum
             if (!la_wait(b_dg, ph, abort_flag, limit)) break;
@@ -795,18 +831,14 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < C::NL; ++e) G[j + e] = fmaf(A, G[j + e], __uint_as_float(d[e]));
             }
-            if (C::kRoomy && i + 1 < n) put_S();   // every read of this chunk's sums is done
-            if (!p.dkq_fp32) {
+            if (i + 1 < n) put_S();   // every read of this chunk's sums is done, and every product of terms
+            if (C::kRoomy) {
 #pragma unroll
-                for (int j = 0; j < C::NQ; j += 8)
-                    *reinterpret_cast<uint4*>(stage + tile_at(wg * C::NQ + j)) =
-                        make_uint4(ok_[j / 2], ok_[j / 2 + 1], ok_[j / 2 + 2], ok_[j / 2 + 3]);
+                for (int j = 0; j < C::NQ; j += 16) stage_out(stage, wg * C::NQ + j, okk + j / 2);
+#pragma unroll
+                for (int j = 0; j < C::NV; j += 16) stage_out(stage + 2 * C::kQ + C::kV, wg * C::NV + j, ov + j / 2);
+                arrive(r_out);
             }
-#pragma unroll
-            for (int j = 0; j < C::NV; j += 8)
-                *reinterpret_cast<uint4*>(stage + 2 * C::kQ + C::kV + tile_at(wg * C::NV + j)) =
-                    make_uint4(ov[j / 2], ov[j / 2 + 1], ov[j / 2 + 2], ov[j / 2 + 3]);
-            arrive(r_out);
         }
         if (c0 == 0 && mine) {
 #pragma unroll
@@ -850,7 +882,10 @@ LaPlan la_bwd_plan(int B, int H, int T, int, int) {
     return {(chunks + per - 1) / per, per};
 }
 
-cudaError_t launch_la_bwd_tc(const LaParams& p, cudaStream_t s) {
+cudaError_t launch_la_bwd_tc(const LaParams& q, cudaStream_t s) {
+    LaParams p = q;
+    p.out32 = !((reinterpret_cast<uintptr_t>(p.dq) | reinterpret_cast<uintptr_t>(p.dk) |
+                 reinterpret_cast<uintptr_t>(p.dv)) & 31u);
     const size_t qk = (size_t)p.B * p.G, vy = (size_t)p.B * p.H;
     BwdMaps m;
     if (!la_tensor_map(&m.q, p.q, p.K, p.T, qk) || !la_tensor_map(&m.k, p.k, p.K, p.T, qk) ||
