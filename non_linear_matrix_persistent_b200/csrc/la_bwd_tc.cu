@@ -113,12 +113,14 @@ __device__ __forceinline__ float column_sums(float (&r)[N]) {
 // tensor memory and, dP'ᵀ, to its place `dp(column)` in shared memory; returns
 // the source's sum of paths into the block, and leaves in cut[] by gate u the
 // sums over the warp's sources before u of the paths to sinks u.. of the block.
-// The decay is r·c[t].  DIAG: the source's own block, sinks t >= s.  ZERO: the
-// chunk has gates at the floor, paths through which count for df alone, or
-// blocks too steep for the product: the diagonal takes an exponential each.
-template <bool DIAG, bool ZERO, int NSUM, class Place>
+// The decay is r·c[t].  `first`: the lane in the source's own block (sinks t >=
+// s), else -1.  ZERO: the chunk has gates at the floor, paths through which
+// count for df alone, or blocks too steep for the product: the diagonal takes
+// an exponential each.  (One body for diagonal and other blocks: the two would
+// not fit the instruction cache together.)
+template <bool ZERO, int NSUM, class Place>
 __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const LaTablesZ* tab, int t0, float Fs, float Is,
-                                             float Zs, float r, float* cut, Place dp) {
+                                             float Zs, float r, int first, float* cut, Place dp) {
     const int lane = threadIdx.x & 31;
     float run = 0.f;
     float R[NSUM];
@@ -130,20 +132,16 @@ __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const La
         float d[16], z[ZERO ? 16 : 1];
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
-            if constexpr (DIAG && ZERO) {
+            const float4 c = *reinterpret_cast<const float4*>(&tab->c[t0 + h + e]);
+            d[e] = r * c.x; d[e + 1] = r * c.y; d[e + 2] = r * c.z; d[e + 3] = r * c.w;
+            if (ZERO && first >= 0) {
                 const float4 f = *reinterpret_cast<const float4*>(&tab->F[t0 + h + e]);
-                const float4 w = *reinterpret_cast<const float4*>(&tab->I[t0 + h + e]);
+                const float4 w = la_whole(tab, t0 + h + e);
                 d[e] = ex2_approx((f.x - Fs) + (w.x - Is)); d[e + 1] = ex2_approx((f.y - Fs) + (w.y - Is));
                 d[e + 2] = ex2_approx((f.z - Fs) + (w.z - Is)); d[e + 3] = ex2_approx((f.w - Fs) + (w.w - Is));
-#pragma unroll
-                for (int o = 0; o < 4; ++o) d[e + o] = h + e + o >= lane ? d[e + o] : 0.f;
-            } else {
-                const float4 c = *reinterpret_cast<const float4*>(&tab->c[t0 + h + e]);
-                d[e] = r * c.x; d[e + 1] = r * c.y; d[e + 2] = r * c.z; d[e + 3] = r * c.w;
-                if constexpr (DIAG)
-#pragma unroll
-                    for (int o = 0; o < 4; ++o) d[e + o] = h + e + o >= lane ? d[e + o] : 0.f;
             }
+#pragma unroll
+            for (int o = 0; o < 4; ++o) d[e + o] = h + e + o >= first ? d[e + o] : 0.f;
             if constexpr (ZERO) {
                 const float4 zs = *reinterpret_cast<const float4*>(&tab->Z[t0 + h + e]);
                 z[e] = zs.x != Zs ? 0.f : d[e]; z[e + 1] = zs.y != Zs ? 0.f : d[e + 1];
@@ -170,9 +168,9 @@ __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const La
             pd[e / 2] = pack_bf16(QD.x, QD.y);
             const int at = NSUM == 32 ? h + e : e;
             run += W.y;
-            R[at + 1] = !DIAG || h + e + 1 > lane ? run : 0.f;   // sources strictly before the gate
+            R[at + 1] = h + e + 1 > first ? run : 0.f;   // sources strictly before the gate
             run += W.x;
-            R[at] = !DIAG || h + e > lane ? run : 0.f;
+            R[at] = h + e > first ? run : 0.f;
         }
         tmem_st_32x32b<8>(tp + h, pp);       // inside the half that has been read
         tmem_st_32x32b<8>(tp + h + 8, pd);
@@ -721,17 +719,15 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 const uint32_t tp = mylane + C::kP + wg * 32, tdp = mylane + C::kDP + wg * 32;
                 float* cut = sc->cut[quarter];
                 auto place = [&](int col) { return dp + tile_at(col); };
-                const bool diag = wg == quarter;
+                const int first = wg == quarter ? lane : -1;
                 // the decay from the source to the block before the sinks' (for its own block, a reciprocal)
                 const float Fp = wg ? tab->F[wg * 32 - 1] : 0.f, Ip = wg ? tab->I[wg * 32 - 1] : 0.f;
                 const float r = ex2_approx((Fp - Ft) + (Ip - It));
                 constexpr int N = C::NS <= 16 ? 32 : 16;   // registers
                 if (Ze != 0.f || tab->steep != 0.f)
-                    run = diag ? score_block<true, true, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, cut, place)
-                               : score_block<false, true, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, cut, place);
+                    run = score_block<true, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place);
                 else
-                    run = diag ? score_block<true, false, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, cut, place)
-                               : score_block<false, false, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, cut, place);
+                    run = score_block<false, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place);
             }
             sc->total[wg][row] = run;
             if (C::kAqFirst) {   // over the states' terms: the sum for G runs while the rows are scaled
@@ -876,7 +872,7 @@ LaPlan la_bwd_plan(int B, int H, int T, int, int) {
 #ifdef LA_TUNE
     if (const char* e = getenv("LA_BSEGS")) segs = atoi(e);
 #endif
-    if (segs > chunks / 2) segs = chunks / 2;
+    if (segs > chunks) segs = chunks;
     if (segs < 1) segs = 1;
     const int per = (int)((chunks + segs - 1) / segs);
     return {(chunks + per - 1) / per, per};

@@ -7,12 +7,12 @@
 // Four matrix products, every accumulator in tensor memory; the state's fp32
 // master stays in registers over the whole walk.
 //
-// A CTA walks the chunks of one (b, h), or of one of its time segments.  8 or
-// 16 warps compute: thread = token row (or state row) = tensor-memory lane, the
-// warpgroups sharing the columns.  One more warp issues the products, another
-// fetches tiles two chunks ahead, stores y and computes the next chunk's
-// decays.  A chunk is a chain of waits (product -> elementwise -> product):
-// two CTAs of 8 warps share an SM where they fit, else a CTA has 16.
+// A CTA walks the chunks of one (b, h), or of one of its time segments.  16
+// warps compute: thread = token row (or state row) = tensor-memory lane, the
+// four warpgroups sharing the columns.  One more warp issues the products, one
+// moves tiles, one computes decays a chunk ahead.  Only S -> Q S -> y and the
+// state's sum -> S form a chain over the chunks; P of the next chunk is formed
+// while the sum of this one is computed.
 //
 // Rounding: the masked scores and the copy of S that multiplies Q are bf16
 // operands (each term of y passes through exactly one of them, and y is
@@ -62,69 +62,167 @@ struct Maps {
     CUtensorMap q, k, v, y;
 };
 
-// FWD: the forward.  SUM: only the segment's own contribution to its final
-// state (from a zero start).  RSUM: the same backwards in time, with decays
-// from the segment's start: Σ_t a_t k_t v_tᵀ.
-enum Kind { FWD, SUM, RSUM };
+constexpr int kNW = 16, kFwdThreads = (kNW + 3) * 32;   // compute warps; one each for products, copies, decays
 
-// NW compute warps: 8 (two CTAs share an SM where they fit) or 16 (one CTA
-// that has an SM to itself).
-template <int KP, int VP, int NW>
-struct Cfg {
-    static constexpr int kThreads = (NW + 2) * 32, WG = NW / 4;
-    static constexpr int kQ = KP / 64 * kTileBytes, kV = VP / 64 * kTileBytes, kStage = 2 * kQ + kV;
-    static constexpr int kOffS = 2 * kStage;                    // bf16 state operand [KP][VP]
-    static constexpr int kOffTab = kOffS + KP * VP * 2;
-    static constexpr int kOffBar = kOffTab + (int)sizeof(LaTables);
-    static constexpr int kBars = 13;
-    static constexpr int kSmem = kOffBar + kBars * 8 + 16;
-    static constexpr int kCtas = NW == 8 && kSmem <= 113 * 1024 ? 2 : 1;
-    // tensor memory: scores (P in bf16 over them), P·V, Q·S, the state's sum.
-    // With two CTAs an SM, P·V takes the second half of the scores, which P leaves free.
-    static constexpr bool kPacked = kCtas == 2;
-    static constexpr int kTmem = kPacked ? 256 : 512;
-    static constexpr int kPV = kPacked ? 64 : 128, kQS = kPV + VP, kDS = kQS + VP;
-    static_assert(kDS + VP <= kTmem, "tensor memory");
-    static constexpr int NS = VP / WG / (KP == 128 ? 1 : 2);    // state columns per thread
-    static constexpr int NL = NS < 16 ? NS : 16;                // per tensor-memory load
-    static constexpr int NY = VP / WG;                          // columns of y per thread
-    // Tensor-memory column of the 16 columns of P that hold score block j (of
-    // 32 columns; warpgroup j % WG computes it): inside that warpgroup's own
-    // score columns, so that no warp writes over scores that another reads.
-    static constexpr __device__ int p_col(int j) { return kPacked ? (j & 1) * 32 + (j >> 1) * 16 : j * 32; }
+// Three bf16 terms of eight scaled values of a tile's row, to three places.
+__device__ __forceinline__ void put_scaled(const uint8_t* src, uint8_t* d0, uint8_t* d1, uint8_t* d2, float w) {
+    const uint4 x = *reinterpret_cast<const uint4*>(src);
+    uint4 hi, mid, lo;
+    split3(w * bf16lo_to_f32(x.x), w * bf16hi_to_f32(x.x), hi.x, mid.x, lo.x);
+    split3(w * bf16lo_to_f32(x.y), w * bf16hi_to_f32(x.y), hi.y, mid.y, lo.y);
+    split3(w * bf16lo_to_f32(x.z), w * bf16hi_to_f32(x.z), hi.z, mid.z, lo.z);
+    split3(w * bf16lo_to_f32(x.w), w * bf16hi_to_f32(x.w), hi.w, mid.w, lo.w);
+    *reinterpret_cast<uint4*>(d0) = hi;
+    *reinterpret_cast<uint4*>(d1) = mid;
+    *reinterpret_cast<uint4*>(d2) = lo;
+}
+
+// A warp's writes are done (shared memory for the products, tensor memory):
+// one arrival a warp.
+__device__ __forceinline__ void warp_arrive(uint32_t b) {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(b);
+}
+
+// Σ_s k_s ⊗ v_s over a chunk with one side in three scaled terms: accumulates
+// into D[KP][VP].  a, b: the sides' first tiles (units of 16 bytes from the
+// descriptor's start); astep, bstep: from one term to the next, 0 for the side
+// that is not scaled.
+template <int KP, int VP>
+__device__ __forceinline__ void outer_sum(uint32_t d, uint64_t mn, uint32_t a, uint32_t astep, uint32_t b, uint32_t bstep,
+                                          bool first) {
+    constexpr uint32_t id = idesc_bf16_f32(KP, VP, 1, 1);
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+            tc_mma_f16_ss(d, mn + a + x * astep + ks * 128, mn + b + x * bstep + ks * 128, id, !(first && x == 0 && ks == 0));
+}
+
+// The thread's part of a [KP][VP] accumulator or state: row kap, NS columns
+// from v0.  128 rows have a tensor-memory lane each; 64 rows have 16 lanes in
+// every quarter, which two half warps read.
+template <int KP, int VP>
+struct Part {
+    static constexpr int NS = KP * VP / (kNW * 32), NL = NS < 16 ? NS : 16;
+    int kap, v0;
+    uint32_t col;   // tensor-memory column of the warp's load
+    __device__ __forceinline__ Part() {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2, quarter = warp & 3;
+        kap = KP == 128 ? quarter * 32 + lane : quarter * 16 + (lane & 15);
+        v0 = KP == 128 ? wg * NS : (wg * 2 + (lane >> 4)) * NS;
+        col = KP == 128 ? wg * NS : wg * 2 * NS;
+    }
+    // S = A S + the accumulator
+    __device__ __forceinline__ void add(uint32_t acc, float A, float (&S)[NS]) const {
+#pragma unroll
+        for (int j = 0; j < NS; j += NL) {
+            uint32_t d[NL];
+            if constexpr (KP == 128) tmem_ld<NL>(acc + col + j, d);
+            else tmem_ld_16x32bx2<NL, NS>(acc + col + j, d);   // threads 16..31: the same lanes, NS columns on
+            tc_wait_ld();
+            reg_fence(d);
+#pragma unroll
+            for (int e = 0; e < NL; ++e) S[j + e] = fmaf(A, S[j + e], __uint_as_float(d[e]));
+        }
+    }
+    __device__ __forceinline__ void load(const float* src, int K, int V, float (&S)[NS]) const {
+#pragma unroll
+        for (int j = 0; j < NS; j += 4) {
+            const float4 x = src && kap < K && v0 + j < V ? *reinterpret_cast<const float4*>(src + (size_t)kap * V + v0 + j)
+                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+        }
+    }
+    __device__ __forceinline__ void store(float* dst, int K, int V, const float (&S)[NS]) const {
+#pragma unroll
+        for (int j = 0; j < NS; j += 4)
+            if (kap < K && v0 + j < V)
+                *reinterpret_cast<float4*>(dst + (size_t)kap * V + v0 + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+    }
 };
 
-template <int KP, int VP, int NW, Kind KIND>
-__global__ void __launch_bounds__(Cfg<KP, VP, NW>::kThreads, Cfg<KP, VP, NW>::kCtas)
-    m2rnn_la_fwd_tc_kernel(const LaParams p, const __grid_constant__ Maps maps, float* seg_decay) {
-    using C = Cfg<KP, VP, NW>;
+// The decay warp: tables of the walk's chunks into two buffers in turn, a chunk
+// ahead of their use.  b_tab, t_free: two barriers each, one per buffer.
+template <class ChunkOf>
+__device__ __forceinline__ void decay_warp(const LaParams& p, int bh, int n, ChunkOf chunk_of, LaTables* tab, uint32_t b_tab,
+                                           uint32_t t_free, volatile int* abort_flag) {
+    float fx[4], fnext[4];
+    la_load_f(p, bh, chunk_of(0), fx);
+    for (int i = 0; i < n; ++i) {
+        if (i + 1 < n) la_load_f(p, bh, chunk_of(i + 1), fnext);
+        if (i >= 2 && !la_wait(t_free + (i & 1) * 8, ((i - 2) >> 1) & 1, abort_flag, p.wait_limit_ns)) break;
+        la_tables(tab + (i & 1), p, fx, p.T - chunk_of(i) * kLaChunk, kLogFloorFwd);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(b_tab + (i & 1) * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) fx[e] = fnext[e];
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------------------------ forward
+
+template <int KP, int VP>
+struct Cfg {
+    static constexpr int kQ = KP / 64 * kTileBytes, kV = VP / 64 * kTileBytes, kStage = 2 * kQ + kV;
+    static constexpr int kStages = KP == 64 && VP == 64 ? 3 : 2;
+    static constexpr bool kScaleV = VP < KP;                    // the narrower side carries the decays
+    static constexpr int kTerm = kScaleV ? kV : kQ;
+    // 128 x 128 has no room for the scaled side's three terms: they go over the
+    // k tile, the q tile and the state operand, once Q S is done
+    static constexpr bool kInPlace = KP * VP == 128 * 128;
+    static constexpr bool kStageY = !kInPlace && VP <= KP;      // y by TMA, over the q tile; else from registers
+    static constexpr int kOffS = kStages * kStage;              // bf16 state operand [KP][VP]
+    static constexpr int kOffX = kOffS + KP * VP * 2;           // the terms
+    static constexpr int kOffTab = kOffX + (kInPlace ? 0 : 3 * kTerm);
+    static constexpr int kOffBar = kOffTab + 2 * (int)sizeof(LaTables);
+    static constexpr int kBars = 22;
+    static constexpr int kSmem = kOffBar + kBars * 8 + 16;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    // tensor memory: scores (two of them where they fit: the next chunk's are
+    // computed early), P·V, Q·S, the state's sum
+    static constexpr int kScores = VP == 64 ? 2 : 1;
+    static constexpr int kPV = kScores * 128, kQS = kPV + VP, kDS = kQS + VP;
+    static_assert(kDS + VP <= 512, "tensor memory");
+    static constexpr int NY = VP / 4;                           // columns of y per thread
+};
+
+template <int KP, int VP>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    m2rnn_la_fwd_tc_kernel(const LaParams p, const __grid_constant__ Maps maps) {
+    using C = Cfg<KP, VP>;
+    using Pt = Part<KP, VP>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bh = blockIdx.x / p.segs, seg = blockIdx.x % p.segs;
     const int nchunks = (p.T + kLaChunk - 1) / kLaChunk;
     const int c0 = seg * p.seg_chunks, n = min(nchunks - c0, p.seg_chunks);
-    if ((KIND == SUM && seg == p.segs - 1) || (KIND == RSUM && seg == 0)) return;   // no segment starts from this sum
-    auto chunk_of = [&](int i) { return KIND == RSUM ? c0 + n - 1 - i : c0 + i; };
+    auto chunk_of = [&](int i) { return c0 + i; };
+    auto stage_of = [&](int i) { return i % C::kStages; };
+    auto stage_phase = [&](int i) { return (uint32_t)(i / C::kStages) & 1u; };
 
     LaTables* tab = reinterpret_cast<LaTables*>(smem + C::kOffTab);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
-    const uint32_t b_full = bar(0), b_sc = bar(2), r_k = bar(3), b_ds1 = bar(4), r_p = bar(5), b_pv = bar(6),
-                   r_lo = bar(7), b_ds2 = bar(8), r_s = bar(9), b_tab = bar(10), b_drain = bar(11), r_y = bar(12);
+    // b_qk, b_v: one per stage; pairs of barriers serve chunks in turn, where one side may be a chunk ahead
+    const uint32_t b_qk = bar(0), b_v = bar(3), b_sc = bar(6), b_tab = bar(8), t_free = bar(10), r_y = bar(12),
+                   r_p = bar(14), r_s = bar(15), r_k = bar(16), b_pv = bar(17), b_ds = bar(18), b_qs = bar(19),
+                   b_drain = bar(20);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint64_t limit = p.wait_limit_ns;
 
     if (threadIdx.x == 0) {
-        mbar_init(bar(0), 1);
-        mbar_init(bar(1), 1);
-        for (uint32_t b : {b_sc, b_ds1, b_pv, b_ds2, b_tab, b_drain}) mbar_init(b, 1);
-        for (uint32_t b : {r_k, r_p, r_lo, r_s, r_y}) mbar_init(b, NW);   // one arrival a warp
+        for (int i = 0; i < 21; ++i) mbar_init(bar(i), 1);
+        for (uint32_t b : {t_free, t_free + 8, r_y, r_y + 8, r_p, r_s, r_k}) mbar_init(b, kNW);
         *abort_flag = 0;
         fence_mbarrier_init();
     }
-    if (warp == NW) {
-        tmem_alloc(smem_u32(tmem_slot), C::kTmem);
+    if (warp == kNW) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -133,64 +231,90 @@ __global__ void __launch_bounds__(Cfg<KP, VP, NW>::kThreads, Cfg<KP, VP, NW>::kC
     const uint32_t tmem = *tmem_slot;
     const uint32_t sbase = smem_u32(smem);
 
-    if (warp == NW) {
+    if (warp == kNW) {
         // ------------------------------------------------------ products
-        constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, 0, 0), id_qs = idesc_bf16_f32(128, VP, 0, 1),
-                           id_pv = idesc_bf16_f32(128, VP, 0, 1), id_ds = idesc_bf16_f32(KP, VP, 1, 1);
+        constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, 0, 0), id_v = idesc_bf16_f32(128, VP, 0, 1);
         const uint64_t d_tile = sw128_desc(sbase, 16), d_mn = sw128_desc(sbase, kTileBytes),
                        d_s = sw128_desc(sbase + C::kOffS, KP * 128);
-        bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            const int s = i & 1, ph = i & 1;
-            // operand positions in units of 16 bytes
-            const uint32_t q = s * (C::kStage >> 4), k = q + (C::kQ >> 4), v = k + (C::kQ >> 4);
-            // the state's product: A = a scaled k tile, its rows (tokens) along the contraction
-            auto state_product = [&](uint32_t a, bool first) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    tc_mma_f16_ss(tmem + C::kDS, d_mn + a + ks * 128, d_mn + v + ks * 128, id_ds, !(first && ks == 0));
-            };
-            if (!(ok = la_wait(b_full + s * 8, (i >> 1) & 1, abort_flag, limit))) break;
-            if (KIND == FWD) {
-                if (!(ok = la_wait(r_s, ph, abort_flag, limit))) break;
-                tc_fence_after();
-                if (lane == 0) {
-#pragma unroll
-                    for (int ks = 0; ks < KP / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * (kTileBytes >> 4) + (ks & 3) * 2;
-                        tc_mma_f16_ss(tmem, d_tile + q + off, d_tile + k + off, id_sc, ks > 0);
-                    }
-#pragma unroll
-                    for (int ks = 0; ks < KP / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * (kTileBytes >> 4) + (ks & 3) * 2;
-                        tc_mma_f16_ss(tmem + C::kQS, d_tile + q + off, d_s + ks * 128, id_qs, ks > 0);
-                    }
-                    tc_commit(b_sc);
-                }
-            }
-            if (!(ok = la_wait(r_k, ph, abort_flag, limit))) break;
+        constexpr uint32_t X = C::kOffX >> 4, XS = C::kTerm >> 4;
+        auto tile = [](int ks) { return (uint32_t)((ks >> 2) * (kTileBytes >> 4) + (ks & 3) * 2); };
+        auto scores = [&](int i) {   // Q Kᵀ
+            const uint32_t q = stage_of(i) * (C::kStage >> 4), k = q + (C::kQ >> 4);
             tc_fence_after();
             if (lane == 0) {
-                state_product(k, true);
-                state_product(q, false);
-                tc_commit(b_ds1);
-            }
-            if (KIND == FWD) {
-                if (!(ok = la_wait(r_p, ph, abort_flag, limit))) break;
-                tc_fence_after();
-                if (lane == 0) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        tc_mma_f16_ts(tmem + C::kPV, tmem + C::p_col(ks >> 1) + (ks & 1) * 8, d_mn + v + ks * 128, id_pv,
-                                      ks > 0);
-                    tc_commit(b_pv);
-                }
+                for (int ks = 0; ks < KP / 16; ++ks)
+                    tc_mma_f16_ss(tmem + (i % C::kScores) * 128, d_tile + q + tile(ks), d_tile + k + tile(ks), id_sc, ks > 0);
+                tc_commit(b_sc + (i & 1) * 8);
             }
-            if (!(ok = la_wait(r_lo, ph, abort_flag, limit))) break;
-            tc_fence_after();
-            if (lane == 0) {
-                state_product(k, false);
-                tc_commit(b_ds2);
+        };
+        if (la_wait(b_qk, 0, abort_flag, limit)) {
+            scores(0);
+            for (int i = 0; i < n; ++i) {
+                // Q S, P V and the state's sum in this order, the next chunk's
+                // scores as soon as its tiles are there and their place is free
+                const int ph = i & 1, s = stage_of(i), s1 = stage_of(i + 1);
+                const uint32_t q = s * (C::kStage >> 4), k = q + (C::kQ >> 4), v = k + (C::kQ >> 4);
+                int step = 0;
+                bool next = i + 1 == n;
+                const uint64_t t0 = globaltimer_ns();
+                while (step < 3 || !next) {
+                    if (step == 0 && mbar_test_wait(r_s, ph)) {
+                        tc_fence_after();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int ks = 0; ks < KP / 16; ++ks)
+                                tc_mma_f16_ss(tmem + C::kQS, d_tile + q + tile(ks), d_s + ks * 128, id_v, ks > 0);
+                            if (C::kInPlace) tc_commit(b_qs);
+                        }
+                        step = 1;
+                    } else if (step == 1 && mbar_test_wait(r_p, ph) && mbar_test_wait(b_v + s * 8, stage_phase(i))) {
+                        tc_fence_after();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks)   // P: 16 columns of bf16 pairs at the start of each block's 32
+                                tc_mma_f16_ts(tmem + C::kPV, tmem + (i % C::kScores) * 128 + (ks >> 1) * 32 + (ks & 1) * 8,
+                                              d_mn + v + ks * 128, id_v, ks > 0);
+                            tc_commit(b_pv);
+                        }
+                        step = 2;
+                    } else if (step == 2 && mbar_test_wait(r_k, ph)) {
+                        tc_fence_after();
+                        if (lane == 0) {
+                            if (C::kInPlace) {
+                                constexpr uint32_t id = idesc_bf16_f32(KP, VP, 1, 1);
+#pragma unroll
+                                for (int x = 0; x < 3; ++x) {
+                                    const uint32_t a = x == 0 ? k : x == 1 ? q : C::kOffS >> 4;
+#pragma unroll
+                                    for (int ks = 0; ks < 8; ++ks)
+                                        tc_mma_f16_ss(tmem + C::kDS, d_mn + a + ks * 128, d_mn + v + ks * 128, id,
+                                                      x > 0 || ks > 0);
+                                }
+                            } else if (C::kScaleV) {
+                                outer_sum<KP, VP>(tmem + C::kDS, d_mn, k, 0, X, XS, true);
+                            } else {
+                                outer_sum<KP, VP>(tmem + C::kDS, d_mn, X, XS, v, 0, true);
+                            }
+                            tc_commit(b_ds);
+                        }
+                        step = 3;
+                    }
+                    // (with two score matrices the place was free when r_s came: y of the chunk before had been read)
+                    if (!next && (C::kScores == 2 ? step > 0 : step > 1 && mbar_test_wait(b_pv, ph)) &&
+                        mbar_test_wait(b_qk + s1 * 8, stage_phase(i + 1))) {
+                        scores(i + 1);
+                        next = true;
+                    }
+                    if (*abort_flag) break;
+                    if (globaltimer_ns() - t0 > limit) {
+                        *abort_flag = 1;
+                        atomicOr(&g_la_status, 1u);
+                        break;
+                    }
+                }
+                if (*abort_flag) break;
+                __syncwarp();
             }
         }
         if (lane == 0) {   // nothing is in flight when the CTA ends
@@ -198,271 +322,369 @@ __global__ void __launch_bounds__(Cfg<KP, VP, NW>::kThreads, Cfg<KP, VP, NW>::kC
             la_drain(b_drain, 0, limit);
         }
         __syncwarp();
-    } else if (warp == NW + 1) {
-        // ------------------------------------------------------ copies and decays
-        const int qk = la_qk_pair(p, bh);
-        int loaded = 0;
-        auto load = [&](int i) {   // lane 0: the tiles of the walk's i-th chunk
-            if (p.fault == 1 && i > 0) return;   // injected: the copies stop after the first chunk
-            loaded = i + 1;
-            const int s = i & 1, t = chunk_of(i) * kLaChunk;
-            const uint32_t base = sbase + s * C::kStage, full = b_full + s * 8;
-            mbar_arrive_expect_tx(full, KIND == FWD ? C::kStage : C::kQ + C::kV);
-#pragma unroll
-            for (int x = 0; x < KP / 64; ++x) {
-                if (KIND == FWD) tma_tile(base + x * kTileBytes, &maps.q, x * 64, t, qk, full);
-                tma_tile(base + C::kQ + x * kTileBytes, &maps.k, x * 64, t, qk, full);
-            }
-#pragma unroll
-            for (int x = 0; x < VP / 64; ++x) tma_tile(base + 2 * C::kQ + x * kTileBytes, &maps.v, x * 64, t, bh, full);
-        };
+    } else if (warp == kNW + 1) {
+        // ------------------------------------------------------ copies
         if (lane == 0) {
-            load(0);
-            if (n > 1) load(1);
-        }
-        float fx[4], fnext[4];
-        la_load_f(p, bh, chunk_of(0), fx);
-        la_load_f(p, bh, n > 1 ? chunk_of(1) : chunk_of(0), fnext);
-        la_tables(tab, p, fx, p.T - chunk_of(0) * kLaChunk, kLogFloorFwd);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b_tab);
-        bool ok = true;
-        int i = 0;
-        for (; i < n; ++i) {
-            const int ph = i & 1;
-            if (i + 1 < n) {   // the next chunk's decays, once this one's are no longer read
+            const int qk = la_qk_pair(p, bh);
+            int nqk = 0, nv = 0;   // chunks whose tiles have been asked for
+            auto load_qk = [&](int i) {
+                if (p.fault == 1 && i > 0) return;   // injected: the copies stop after the first chunk
+                nqk = i + 1;
+                const int s = stage_of(i), t = chunk_of(i) * kLaChunk;
+                const uint32_t base = sbase + s * C::kStage, full = b_qk + s * 8;
+                mbar_arrive_expect_tx(full, 2 * C::kQ);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) fx[e] = fnext[e];
-                if (i + 2 < n) la_load_f(p, bh, chunk_of(i + 2), fnext);
-                if (!(ok = la_wait(KIND == FWD ? r_p : r_k, ph, abort_flag, limit))) break;
-                la_tables(tab, p, fx, p.T - chunk_of(i + 1) * kLaChunk, kLogFloorFwd);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_tab);
+                for (int x = 0; x < KP / 64; ++x) {
+                    tma_tile(base + x * kTileBytes, &maps.q, x * 64, t, qk, full);
+                    tma_tile(base + C::kQ + x * kTileBytes, &maps.k, x * 64, t, qk, full);
+                }
+            };
+            auto load_v = [&](int i) {
+                if (p.fault == 1 && i > 0) return;
+                nv = i + 1;
+                const int s = stage_of(i), t = chunk_of(i) * kLaChunk;
+                const uint32_t base = sbase + s * C::kStage + 2 * C::kQ, full = b_v + s * 8;
+                mbar_arrive_expect_tx(full, C::kV);
+#pragma unroll
+                for (int x = 0; x < VP / 64; ++x) tma_tile(base + x * kTileBytes, &maps.v, x * 64, t, bh, full);
+            };
+            for (int i = 0; i < C::kStages && i < n; ++i) {
+                load_qk(i);
+                load_v(i);
             }
-            // the stage is free when its products are done and y, staged over its q (and k) tile, has left
-            if (!(ok = la_wait(KIND == FWD ? r_y : b_ds2, ph, abort_flag, limit))) break;
-            if (lane == 0) {
-                if (KIND == FWD) {
+            bool ok = true;
+            for (int i = 0; i < n; ++i) {
+                // the stage is free: its products are done, y has been staged
+                if (!(ok = la_wait(r_y + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
+                if (C::kStageY) {
 #pragma unroll
                     for (int x = 0; x < VP / 64; ++x)
                         if (x * 64 < p.V)
-                            tma_store_tile(&maps.y, sbase + (i & 1) * C::kStage + x * kTileBytes, x * 64,
+                            tma_store_tile(&maps.y, sbase + stage_of(i) * C::kStage + x * kTileBytes, x * 64,
                                            chunk_of(i) * kLaChunk, bh);
                     tma_store_commit();
                     tma_store_wait_read();
                 }
-                if (i + 2 < n) load(i + 2);
+                if (i + C::kStages < n) {
+                    load_qk(i + C::kStages);
+                    load_v(i + C::kStages);
+                }
+            }
+            if (!ok) {   // leave no copy in flight
+                for (int j = max(0, nqk - C::kStages); j < nqk; ++j) la_drain(b_qk + stage_of(j) * 8, stage_phase(j), limit);
+                for (int j = max(0, nv - C::kStages); j < nv; ++j) la_drain(b_v + stage_of(j) * 8, stage_phase(j), limit);
             }
         }
-        if (!ok && lane == 0)   // leave no copy in flight
-            for (int j = i; j < loaded; ++j) la_drain(b_full + (j & 1) * 8, (j >> 1) & 1, limit);
         __syncwarp();
+    } else if (warp == kNW + 2) {
+        decay_warp(p, bh, n, chunk_of, tab, b_tab, t_free, abort_flag);
     } else {
         // ------------------------------------------------------ elementwise work
         const int wg = warp >> 2, quarter = warp & 3;
-        const int row = quarter * 32 + lane;                     // token of the chunk
-        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;   // tensor-memory lane base
-        // This thread's part of the state: row kap, columns [v0, v0 + NS).  The
-        // sum of 128 state rows has a lane for each; that of 64 rows has 16
-        // lanes in every quarter, which two half warps read.
-        const int kap = KP == 128 ? row : quarter * 16 + (lane & 15);
-        const int v0 = KP == 128 ? wg * C::NS : (wg * 2 + (lane >> 4)) * C::NS;
-        const bool mine = kap < p.K;
-        float S[C::NS];
-        {
-            const float* src = KIND != FWD ? nullptr
-                               : p.segs > 1 ? p.seg_state + ((size_t)bh * p.segs + seg) * p.K * p.V
-                               : p.S0       ? p.S0 + (size_t)bh * p.K * p.V
-                                            : nullptr;
+        const int row = quarter * 32 + lane;                          // token of the chunk
+        const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16);   // tensor-memory lane base
+        const Pt part;
+        float S[Pt::NS];
+        part.load(p.segs > 1 ? p.seg_state + ((size_t)bh * p.segs + seg) * p.K * p.V
+                  : p.S0     ? p.S0 + (size_t)bh * p.K * p.V
+                             : nullptr,
+                  p.K, p.V, S);
+        auto put_operand = [&](int c) {   // S before chunk c: its bf16 copy for Q·S, the checkpoint
+            uint8_t* op = smem + C::kOffS + (part.v0 >> 6) * (KP * 128);
 #pragma unroll
-            for (int j = 0; j < C::NS; j += 4) {
-                const float4 x = src && mine && v0 + j < p.V
-                                     ? *reinterpret_cast<const float4*>(src + (size_t)kap * p.V + v0 + j)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-                S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
-            }
-        }
-        auto arrive = [&](uint32_t b) {   // this warp's writes are done: shared memory for the products, tensor memory
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b);
-        };
-        auto store_state = [&](float* dst) {
-            if (!mine) return;
-#pragma unroll
-            for (int j = 0; j < C::NS; j += 4)
-                if (v0 + j < p.V)
-                    *reinterpret_cast<float4*>(dst + (size_t)kap * p.V + v0 + j) =
-                        make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
-        };
-        auto write_operand = [&]() {   // bf16 copy of S for Q·S
-            uint8_t* op = smem + C::kOffS + (v0 >> 6) * (KP * 128);
-#pragma unroll
-            for (int j = 0; j < C::NS; j += 8)
-                *reinterpret_cast<uint4*>(op + sw128(kap, ((v0 & 63) + j) >> 3)) =
+            for (int j = 0; j < Pt::NS; j += 8)
+                *reinterpret_cast<uint4*>(op + sw128(part.kap, ((part.v0 & 63) + j) >> 3)) =
                     make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]), pack_bf16(S[j + 4], S[j + 5]),
                                pack_bf16(S[j + 6], S[j + 7]));
-        };
-        if (KIND == FWD) {
-            write_operand();
-            arrive(r_s);
-        }
-        float decay = 1.f;
-
-        for (int i = 0; i < n; ++i) {
-            const int s = i & 1, ph = i & 1, c = chunk_of(i);
-            uint8_t* stage = smem + s * C::kStage;
-            if (KIND == FWD && p.ckpt && mine) {   // [V/4][K][4]: a warp's rows are adjacent
+            warp_arrive(r_s);
+            if (p.ckpt && part.kap < p.K) {   // [V/4][K][4]: a warp's rows are adjacent
                 float* ck = p.ckpt + ((size_t)bh * nchunks + c) * p.K * p.V;
 #pragma unroll
-                for (int j = 0; j < C::NS; j += 4)
-                    if (v0 + j < p.V)
-                        *reinterpret_cast<float4*>(ck + ((size_t)((v0 + j) >> 2) * p.K + kap) * 4) =
+                for (int j = 0; j < Pt::NS; j += 4)
+                    if (part.v0 + j < p.V)
+                        *reinterpret_cast<float4*>(ck + ((size_t)((part.v0 + j) >> 2) * p.K + part.kap) * 4) =
                             make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
             }
-            if (!la_wait(b_tab, ph, abort_flag, limit)) break;
-            const float Ft = tab->F[row], It = tab->I[row], Fe = tab->F[127], Ie = tab->I[127];
-            const float at = ex2_approx(Ft + It), A = ex2_approx(Fe + Ie);
-            const float w = KIND == RSUM ? at : ex2_approx((Fe - Ft) + (Ie - It));
-            if (!la_wait(b_full + s * 8, (i >> 1) & 1, abort_flag, limit)) break;
-            if (KIND == FWD && !la_wait(b_sc, ph, abort_flag, limit)) break;
+        };
+        float at = 0.f, w = 0.f, A = 0.f;        // of the chunk whose P has been formed last
+        // P = masked, decayed scores in bf16, over the scores: row `row`, block wg of 32 columns
+        auto put_P = [&](int i) -> bool {
+            if (!la_wait(b_tab + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) return false;
+            const LaTables* tb = tab + (i & 1);
+            const float Ft = tb->F[row], It = tb->I[row], Fe = tb->F[127], Ie = tb->I[127];
+            at = ex2_approx(Ft + It);
+            A = ex2_approx(Fe + Ie);
+            w = ex2_approx((Fe - Ft) + (Ie - It));
+            if (!la_wait(b_sc + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) return false;
             tc_fence_after();
-            // ---- w k in three bf16 terms: over the k tile, over the q tile, and kept
-            constexpr int kCh = KP / 8 / C::WG;                 // 16-byte chunks of the row for this thread
-            uint32_t lo[kCh][4];
+            const uint32_t at_ = mine + (i % C::kScores) * 128 + wg * 32;
+            uint32_t pk[16];
+            if (wg > quarter) {
 #pragma unroll
-            for (int j = 0; j < kCh; ++j) {
-                const int ch = wg * kCh + j;
-                const uint32_t at_ = (ch >> 3) * kTileBytes + sw128(row, ch & 7);
-                uint4* kp = reinterpret_cast<uint4*>(stage + C::kQ + at_);
-                const uint4 x = *kp;
-                uint4 hi, mid;
-                split3(w * bf16lo_to_f32(x.x), w * bf16hi_to_f32(x.x), hi.x, mid.x, lo[j][0]);
-                split3(w * bf16lo_to_f32(x.y), w * bf16hi_to_f32(x.y), hi.y, mid.y, lo[j][1]);
-                split3(w * bf16lo_to_f32(x.z), w * bf16hi_to_f32(x.z), hi.z, mid.z, lo[j][2]);
-                split3(w * bf16lo_to_f32(x.w), w * bf16hi_to_f32(x.w), hi.w, mid.w, lo[j][3]);
-                *kp = hi;
-                *reinterpret_cast<uint4*>(stage + at_) = mid;
-            }
-            arrive(r_k);
-            if (KIND == FWD) {
-                // ---- P = masked, decayed scores in bf16, back to tensor memory
-#pragma unroll
-                for (int j = wg; j < 4; j += C::WG) {          // block of 32 columns
-                    uint32_t pk[16];
-                    if (j > quarter) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = 0;
-                    } else {
-                        uint32_t sc[32];
-                        tmem_ld_32x32b<32>(tmem + lanes + j * 32, sc);
-                        tc_wait_ld();
-                        reg_fence(sc);
-                        if (j < quarter || tab->steep == 0.f) {
-                            const float r = ex2_approx((Ft - tab->F[j * 32 + 31]) + (It - tab->I[j * 32 + 31]));
-                            const int last = j < quarter ? 31 : lane;   // the row's last column of the block
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 cs = *reinterpret_cast<const float4*>(&tab->c[j * 32 + e]);
-                                const float2 lo2 = __fmul2_rn(__fmul2_rn(make_float2(r, r), make_float2(cs.x, cs.y)),
-                                                              make_float2(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1]))),
-                                             hi2 = __fmul2_rn(__fmul2_rn(make_float2(r, r), make_float2(cs.z, cs.w)),
-                                                              make_float2(__uint_as_float(sc[e + 2]), __uint_as_float(sc[e + 3])));
-                                pk[e / 2] = pack_bf16(e <= last ? lo2.x : 0.f, e + 1 <= last ? lo2.y : 0.f);
-                                pk[e / 2 + 1] = pack_bf16(e + 2 <= last ? hi2.x : 0.f, e + 3 <= last ? hi2.y : 0.f);
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 fs = *reinterpret_cast<const float4*>(&tab->F[j * 32 + e]);
-                                const float4 is = *reinterpret_cast<const float4*>(&tab->I[j * 32 + e]);
-                                auto d = [&](int o, float f, float w_) {
-                                    return e + o <= lane ? __uint_as_float(sc[e + o]) * ex2_approx((Ft - f) + (It - w_))
-                                                         : 0.f;
-                                };
-                                pk[e / 2] = pack_bf16(d(0, fs.x, is.x), d(1, fs.y, is.y));
-                                pk[e / 2 + 1] = pack_bf16(d(2, fs.z, is.z), d(3, fs.w, is.w));
-                            }
-                        }
-                    }
-                    tmem_st16(tmem + lanes + C::p_col(j), pk);
-                }
-                tc_wait_st();
-                arrive(r_p);
-            }
-            // ---- the state's third term, once the first two are multiplied
-            if (!la_wait(b_ds1, ph, abort_flag, limit)) break;
-#pragma unroll
-            for (int j = 0; j < kCh; ++j) {
-                const int ch = wg * kCh + j;
-                *reinterpret_cast<uint4*>(stage + C::kQ + (ch >> 3) * kTileBytes + sw128(row, ch & 7)) =
-                    make_uint4(lo[j][0], lo[j][1], lo[j][2], lo[j][3]);
-            }
-            arrive(r_lo);
-            // ---- y = a (Q S) + P V, kept until the stage is free
-            uint32_t o[C::NY / 2];
-            if (KIND == FWD) {
-                if (!la_wait(b_pv, ph, abort_flag, limit)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int j = 0; j < C::NY; j += 16) {
-                    uint32_t pv[16], qs[16];
-                    tmem_ld<16>(tmem + lanes + C::kPV + wg * C::NY + j, pv);
-                    tmem_ld<16>(tmem + lanes + C::kQS + wg * C::NY + j, qs);
-                    tc_wait_ld();
-                    reg_fence(pv);
-                    reg_fence(qs);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        o[j / 2 + e] = pack_bf16(fmaf(at, __uint_as_float(qs[2 * e]), __uint_as_float(pv[2 * e])),
-                                                 fmaf(at, __uint_as_float(qs[2 * e + 1]), __uint_as_float(pv[2 * e + 1])));
-                }
-            }
-            // ---- S = A S + the chunk's sum
-            if (!la_wait(b_ds2, ph, abort_flag, limit)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int j = 0; j < C::NS; j += C::NL) {
-                uint32_t d[C::NL];
-                if constexpr (KP == 128)
-                    tmem_ld<C::NL>(tmem + lanes + C::kDS + wg * C::NS + j, d);
-                else   // threads 16..31: the same lanes, NS columns on
-                    tmem_ld_16x32bx2<C::NL, C::NS>(tmem + lanes + C::kDS + wg * 2 * C::NS + j, d);
-                tc_wait_ld();
-                reg_fence(d);
-#pragma unroll
-                for (int e = 0; e < C::NL; ++e) S[j + e] = fmaf(A, S[j + e], __uint_as_float(d[e]));
-            }
-            decay *= A;
-            if (KIND == FWD) {
-                if (i + 1 < n) {
-                    write_operand();
-                    arrive(r_s);
-                }
-#pragma unroll
-                for (int j = 0; j < C::NY; j += 8) {
-                    const int col = wg * C::NY + j;
-                    *reinterpret_cast<uint4*>(stage + (col >> 6) * kTileBytes + sw128(row, (col & 63) >> 3)) =
-                        make_uint4(o[j / 2], o[j / 2 + 1], o[j / 2 + 2], o[j / 2 + 3]);
-                }
-                arrive(r_y);
+                for (int e = 0; e < 16; ++e) pk[e] = 0;
             } else {
-                tc_fence_before();   // ordered before the next chunk's r_k arrival
+                uint32_t sc[32];
+                tmem_ld<32>(at_, sc);
+                const float r = ex2_approx((Ft - tb->F[wg * 32 + 31]) + (It - tb->I[wg * 32 + 31]));
+                const int last = wg < quarter ? 31 : lane;   // the row's last column of the block
+                tc_wait_ld();
+                reg_fence(sc);
+                if (wg < quarter || tb->steep == 0.f) {
+                    const float2 r2 = make_float2(r, r);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 cs = *reinterpret_cast<const float4*>(&tb->c[wg * 32 + e]);
+                        const float2 x = __fmul2_rn(__fmul2_rn(r2, make_float2(cs.x, cs.y)),
+                                                    make_float2(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1]))),
+                                     y = __fmul2_rn(__fmul2_rn(r2, make_float2(cs.z, cs.w)),
+                                                    make_float2(__uint_as_float(sc[e + 2]), __uint_as_float(sc[e + 3])));
+                        pk[e / 2] = pack_bf16(e <= last ? x.x : 0.f, e + 1 <= last ? x.y : 0.f);
+                        pk[e / 2 + 1] = pack_bf16(e + 2 <= last ? y.x : 0.f, e + 3 <= last ? y.y : 0.f);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 fs = *reinterpret_cast<const float4*>(&tb->F[wg * 32 + e]);
+                        const float4 is = la_whole(tb, wg * 32 + e);
+                        auto d = [&](int o, float f, float w_) {
+                            return e + o <= lane ? __uint_as_float(sc[e + o]) * ex2_approx((Ft - f) + (It - w_)) : 0.f;
+                        };
+                        pk[e / 2] = pack_bf16(d(0, fs.x, is.x), d(1, fs.y, is.y));
+                        pk[e / 2 + 1] = pack_bf16(d(2, fs.z, is.z), d(3, fs.w, is.w));
+                    }
+                }
+            }
+            tmem_st16(at_, pk);
+            tc_wait_st();
+            warp_arrive(r_p);
+            return true;
+        };
+        // the scaled side's terms of chunk i (their buffer is free: the last sum is done)
+        auto put_terms = [&](int i) -> bool {
+            const uint32_t full = C::kScaleV ? b_v : b_qk;
+            if (!la_wait(full + stage_of(i) * 8, stage_phase(i), abort_flag, limit)) return false;
+            if (C::kInPlace && !la_wait(b_qs, i & 1, abort_flag, limit)) return false;
+            uint8_t* stage = smem + stage_of(i) * C::kStage;
+            constexpr int kCh = C::kTerm / 128 / 16 / 4;         // 16-byte chunks of the row for this thread
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) {
+                const int ch = wg * kCh + j;
+                const uint32_t pos = (ch >> 3) * kTileBytes + sw128(row, ch & 7);
+                uint8_t* src = stage + (C::kScaleV ? 2 * C::kQ : C::kQ) + pos;
+                uint8_t* X = smem + C::kOffX + pos;
+                if (C::kInPlace) put_scaled(src, src, stage + pos, smem + C::kOffS + pos, w);
+                else put_scaled(src, X, X + C::kTerm, X + 2 * C::kTerm, w);
+            }
+            warp_arrive(r_k);
+            if (lane == 0) mbar_arrive(t_free + (i & 1) * 8);    // this chunk's tables are no longer read
+            return true;
+        };
+        bool ok = true;
+        put_operand(c0);
+        ok = put_P(0) && put_terms(0);
+        for (int i = 0; ok && i < n; ++i) {
+            const int ph = i & 1;
+            const float at_i = at, A_i = A;
+            // ---- y = a (Q S) + P V
+            if (!la_wait(b_pv, ph, abort_flag, limit)) break;
+            tc_fence_after();
+            const int t = chunk_of(i) * kLaChunk + row;
+#pragma unroll
+            for (int j = 0; j < C::NY; j += 16) {
+                const int col = wg * C::NY + j;
+                uint32_t pv[16], qs[16], o[8];
+                tmem_ld<16>(mine + C::kPV + col, pv);
+                tmem_ld<16>(mine + C::kQS + col, qs);
+                tc_wait_ld();
+                reg_fence(pv);
+                reg_fence(qs);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    o[e] = pack_bf16(fmaf(at_i, __uint_as_float(qs[2 * e]), __uint_as_float(pv[2 * e])),
+                                     fmaf(at_i, __uint_as_float(qs[2 * e + 1]), __uint_as_float(pv[2 * e + 1])));
+                if (C::kStageY) {
+                    uint8_t* dst = smem + stage_of(i) * C::kStage + (col >> 6) * kTileBytes;
+                    *reinterpret_cast<uint4*>(dst + sw128(row, (col & 63) >> 3)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(dst + sw128(row, ((col & 63) >> 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                } else if (t < p.T && col < p.V) {
+                    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + ((size_t)bh * p.T + t) * p.V + col;
+                    if (p.out32) {
+                        st_global_v8(y, o);
+                    } else {
+                        *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(y + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+            }
+            // ---- the next chunk's P while the state's sum is computed
+            if (i + 1 < n && !(ok = put_P(i + 1))) break;
+            // ---- S = A S + the chunk's sum
+            if (!la_wait(b_ds, ph, abort_flag, limit)) break;
+            tc_fence_after();
+            part.add(mine + C::kDS, A_i, S);
+            warp_arrive(r_y + (i & 1) * 8);
+            if (i + 1 < n) {
+                put_operand(chunk_of(i + 1));
+                ok = put_terms(i + 1);
             }
         }
-        if (KIND != FWD) {
-            store_state(p.seg_state + ((size_t)bh * p.segs + seg) * p.K * p.V);
-            if (threadIdx.x == 0) seg_decay[(size_t)bh * p.segs + seg] = decay;
-        } else if (p.ST && c0 + n == nchunks) {
-            store_state(p.ST + (size_t)bh * p.K * p.V);
+        if (p.ST && c0 + n == nchunks) part.store(p.ST + (size_t)bh * p.K * p.V, p.K, p.V, S);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kNW) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ segment sums
+
+// What a segment's tokens add to the state at its end, from a zero start
+// (REV: to the state's gradient at its start): Σ w_s k_s v_sᵀ (Σ w_t q_t dy_tᵀ)
+// with w the decay to the segment's end (from its start through t).  The walk
+// starts at that end, so w is a running product times the chunk's decay and
+// the whole segment is one sum in tensor memory: a chunk's terms are written
+// while the last one's products run.
+template <int KP, int VP>
+struct SumCfg {
+    static constexpr int kQ = KP / 64 * kTileBytes, kV = VP / 64 * kTileBytes, kStage = kQ + kV;
+    static constexpr bool kScaleV = VP < KP;
+    static constexpr int kTerm = kScaleV ? kV : kQ;
+    static constexpr int kSets = KP * VP < 128 * 128 ? 2 : 1;   // sets of terms
+    static constexpr int kOffX = 2 * kStage;
+    static constexpr int kOffTab = kOffX + kSets * 3 * kTerm;
+    static constexpr int kOffBar = kOffTab + 2 * (int)sizeof(LaTables);
+    static constexpr int kBars = 10;
+    static constexpr int kSmem = kOffBar + kBars * 8 + 16;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+template <int KP, int VP, bool REV>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    m2rnn_la_sum_tc_kernel(const LaParams p, const __grid_constant__ Maps maps, float* seg_decay) {
+    using C = SumCfg<KP, VP>;
+    using Pt = Part<KP, VP>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int bh = blockIdx.x / p.segs, seg = blockIdx.x % p.segs;
+    if (REV ? seg == 0 : seg == p.segs - 1) return;   // no segment starts from this sum
+    const int nchunks = (p.T + kLaChunk - 1) / kLaChunk;
+    const int c0 = seg * p.seg_chunks, n = min(nchunks - c0, p.seg_chunks);
+    auto chunk_of = [&](int i) { return REV ? c0 + i : c0 + n - 1 - i; };
+
+    LaTables* tab = reinterpret_cast<LaTables*>(smem + C::kOffTab);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    const uint32_t b_full = bar(0), b_tab = bar(2), t_free = bar(4), b_ds = bar(6), r_k = bar(8), b_drain = bar(9);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint64_t limit = p.wait_limit_ns;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 10; ++i) mbar_init(bar(i), 1);
+        for (uint32_t b : {t_free, t_free + 8, r_k}) mbar_init(b, kNW);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == kNW) {
+        tmem_alloc(smem_u32(tmem_slot), VP);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t sbase = smem_u32(smem);
+
+    if (warp == kNW) {
+        const uint64_t d_mn = sw128_desc(sbase, kTileBytes);
+        for (int i = 0; i < n; ++i) {
+            if (!la_wait(b_full + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) break;
+            if (!la_wait(r_k, i & 1, abort_flag, limit)) break;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t k = (i & 1) * (C::kStage >> 4), v = k + (C::kQ >> 4),
+                               x = (C::kOffX + (i % C::kSets) * 3 * C::kTerm) >> 4, xs = C::kTerm >> 4;
+                if (C::kScaleV) outer_sum<KP, VP>(tmem, d_mn, k, 0, x, xs, i == 0);
+                else outer_sum<KP, VP>(tmem, d_mn, x, xs, v, 0, i == 0);
+                tc_commit(b_ds + (i & 1) * 8);
+            }
+        }
+        if (lane == 0) {
+            tc_commit(b_drain);
+            la_drain(b_drain, 0, limit);
+        }
+        __syncwarp();
+    } else if (warp == kNW + 1) {
+        if (lane == 0) {
+            const int qk = la_qk_pair(p, bh);
+            int loaded = 0;
+            auto load = [&](int i) {
+                if (p.fault == 1 && i > 0) return;
+                loaded = i + 1;
+                const int t = chunk_of(i) * kLaChunk;
+                const uint32_t base = sbase + (i & 1) * C::kStage, full = b_full + (i & 1) * 8;
+                mbar_arrive_expect_tx(full, C::kStage);
+#pragma unroll
+                for (int x = 0; x < KP / 64; ++x) tma_tile(base + x * kTileBytes, &maps.k, x * 64, t, qk, full);
+#pragma unroll
+                for (int x = 0; x < VP / 64; ++x) tma_tile(base + C::kQ + x * kTileBytes, &maps.v, x * 64, t, bh, full);
+            };
+            load(0);
+            if (n > 1) load(1);
+            bool ok = true;
+            for (int i = 0; i + 2 < n; ++i) {
+                if (!(ok = la_wait(b_ds + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
+                load(i + 2);
+            }
+            if (!ok)
+                for (int j = max(0, loaded - 2); j < loaded; ++j) la_drain(b_full + (j & 1) * 8, (j >> 1) & 1, limit);
+        }
+        __syncwarp();
+    } else if (warp == kNW + 2) {
+        decay_warp(p, bh, n, chunk_of, tab, b_tab, t_free, abort_flag);
+    } else {
+        const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        float carry = 1.f;
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            if (!(ok = la_wait(b_tab + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
+            const LaTables* tb = tab + (i & 1);
+            const float Ft = tb->F[row], It = tb->I[row], Fe = tb->F[127], Ie = tb->I[127];
+            const float w = carry * ex2_approx(REV ? Ft + It : (Fe - Ft) + (Ie - It));
+            carry *= ex2_approx(Fe + Ie);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(t_free + (i & 1) * 8);
+            if (!(ok = la_wait(b_full + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
+            const int j = i - C::kSets;   // whose terms these replace
+            if (j >= 0 && !(ok = la_wait(b_ds + (j & 1) * 8, (j >> 1) & 1, abort_flag, limit))) break;
+            const uint8_t* src = smem + (i & 1) * C::kStage + (C::kScaleV ? C::kQ : 0);
+            uint8_t* dst = smem + C::kOffX + (i % C::kSets) * 3 * C::kTerm;
+            constexpr int kCh = C::kTerm / 128 / 16 / 4;
+#pragma unroll
+            for (int e = 0; e < kCh; ++e) {
+                const int ch = wg * kCh + e;
+                const uint32_t pos = (ch >> 3) * kTileBytes + sw128(row, ch & 7);
+                put_scaled(src + pos, dst + pos, dst + pos + C::kTerm, dst + pos + 2 * C::kTerm, w);
+            }
+            warp_arrive(r_k);
+        }
+        if (ok && la_wait(b_ds + ((n - 1) & 1) * 8, ((n - 1) >> 1) & 1, abort_flag, limit)) {
+            tc_fence_after();
+            const Pt part;
+            float S[Pt::NS];
+#pragma unroll
+            for (int e = 0; e < Pt::NS; ++e) S[e] = 0.f;
+            part.add(tmem + ((uint32_t)(quarter * 32) << 16), 1.f, S);
+            part.store(p.seg_state + ((size_t)bh * p.segs + seg) * p.K * p.V, p.K, p.V, S);
+            if (threadIdx.x == 0) seg_decay[(size_t)bh * p.segs + seg] = carry;
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == NW) {
+    if (warp == kNW) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::kTmem);
+        tmem_dealloc(tmem, VP);
     }
 }
 
@@ -486,27 +708,35 @@ __global__ void m2rnn_la_seg_scan_kernel(const LaParams p, const float* __restri
     }
 }
 
-template <int KP, int VP, int NW, Kind KIND>
-cudaError_t launch_nw(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
-    using C = Cfg<KP, VP, NW>;
-    auto kern = m2rnn_la_fwd_tc_kernel<KP, VP, NW, KIND>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    kern<<<p.B * p.H * p.segs, C::kThreads, C::kSmem, s>>>(p, m, seg_decay);
-    return cudaGetLastError();
-}
-template <int KP, int VP, Kind KIND>
-cudaError_t launch(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
-    if constexpr (Cfg<KP, VP, 8>::kCtas == 2) {
-        if ((long long)p.B * p.H * p.segs > kNumSMs) return launch_nw<KP, VP, 8, KIND>(p, m, seg_decay, s);
+template <int KP, int VP>
+struct FwdKernel {
+    static cudaError_t launch(const LaParams& p, const Maps& m, float*, cudaStream_t s) {
+        auto kern = m2rnn_la_fwd_tc_kernel<KP, VP>;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<KP, VP>::kSmem);
+        if (e != cudaSuccess) return e;
+        kern<<<p.B * p.H * p.segs, kFwdThreads, Cfg<KP, VP>::kSmem, s>>>(p, m);
+        return cudaGetLastError();
     }
-    return launch_nw<KP, VP, 16, KIND>(p, m, seg_decay, s);
-}
-template <Kind KIND>
+};
+template <bool REV>
+struct Sum {
+    template <int KP, int VP>
+    struct Kernel {
+        static cudaError_t launch(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
+            auto kern = m2rnn_la_sum_tc_kernel<KP, VP, REV>;
+            const cudaError_t e =
+                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SumCfg<KP, VP>::kSmem);
+            if (e != cudaSuccess) return e;
+            kern<<<p.B * p.H * p.segs, kFwdThreads, SumCfg<KP, VP>::kSmem, s>>>(p, m, seg_decay);
+            return cudaGetLastError();
+        }
+    };
+};
+template <template <int, int> class Kernel>
 cudaError_t launch_shape(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
     if (p.K <= 64)
-        return p.V <= 64 ? launch<64, 64, KIND>(p, m, seg_decay, s) : launch<64, 128, KIND>(p, m, seg_decay, s);
-    return p.V <= 64 ? launch<128, 64, KIND>(p, m, seg_decay, s) : launch<128, 128, KIND>(p, m, seg_decay, s);
+        return p.V <= 64 ? Kernel<64, 64>::launch(p, m, seg_decay, s) : Kernel<64, 128>::launch(p, m, seg_decay, s);
+    return p.V <= 64 ? Kernel<128, 64>::launch(p, m, seg_decay, s) : Kernel<128, 128>::launch(p, m, seg_decay, s);
 }
 
 float* decays_of(const LaParams& p) {   // behind the segment states in the workspace
@@ -516,14 +746,14 @@ float* decays_of(const LaParams& p) {   // behind the segment states in the work
 }  // namespace
 
 LaPlan la_fwd_plan(int B, int H, int T, int K, int V) {
-    const int chunks = (T + kLaChunk - 1) / kLaChunk, per_sm = K <= 64 && V <= 64 ? 2 : 1;
+    const int chunks = (T + kLaChunk - 1) / kLaChunk, per_sm = 1;
     const long long pairs = (long long)B * H, slots = (long long)kNumSMs * per_sm;
     long long segs = 1;
     if (pairs * 2 <= kNumSMs && chunks >= 4) segs = slots / pairs;
 #ifdef LA_TUNE
     if (const char* e = getenv("LA_SEGS")) segs = atoi(e);
 #endif
-    if (segs > chunks / 2) segs = chunks / 2;
+    if (segs > chunks) segs = chunks;
     if (segs < 1) segs = 1;
     const int per = (int)((chunks + segs - 1) / segs);
     return {(chunks + per - 1) / per, per};
@@ -533,20 +763,22 @@ size_t la_seg_bytes(const LaPlan& plan, int B, int H, int K, int V) {
     return plan.segs <= 1 ? 0 : sizeof(float) * (size_t)B * H * plan.segs * ((size_t)K * V + 1);
 }
 
-cudaError_t launch_la_fwd_tc(const LaParams& p, cudaStream_t s) {
+cudaError_t launch_la_fwd_tc(const LaParams& q, cudaStream_t s) {
+    LaParams p = q;
+    p.out32 = !(reinterpret_cast<uintptr_t>(p.y) & 31u);
     Maps m;
     if (!la_tensor_map(&m.q, p.q, p.K, p.T, (size_t)p.B * p.G) || !la_tensor_map(&m.k, p.k, p.K, p.T, (size_t)p.B * p.G) ||
         !la_tensor_map(&m.v, p.v, p.V, p.T, (size_t)p.B * p.H) || !la_tensor_map(&m.y, p.y, p.V, p.T, (size_t)p.B * p.H))
         return cudaErrorNotSupported;
     if (p.segs > 1) {
-        cudaError_t e = launch_shape<SUM>(p, m, decays_of(p), s);
+        cudaError_t e = launch_shape<Sum<false>::Kernel>(p, m, decays_of(p), s);
         if (e != cudaSuccess) return e;
         const size_t n = (size_t)p.B * p.H * p.K * p.V / 4;
         m2rnn_la_seg_scan_kernel<<<(unsigned)((n + 127) / 128), 128, 0, s>>>(p, decays_of(p), p.S0, 0);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    return launch_shape<FWD>(p, m, nullptr, s);
+    return launch_shape<FwdKernel>(p, m, nullptr, s);
 }
 
 // The same sums for the gradient: what a segment's tokens add to dL/dS at its
@@ -557,7 +789,7 @@ cudaError_t launch_la_seg_grads(const LaParams& p, cudaStream_t s) {
         return cudaErrorNotSupported;
     m.q = m.k;
     m.y = m.v;
-    cudaError_t e = launch_shape<RSUM>(p, m, decays_of(p), s);
+    cudaError_t e = launch_shape<Sum<true>::Kernel>(p, m, decays_of(p), s);
     if (e != cudaSuccess) return e;
     const size_t n = (size_t)p.B * p.H * p.K * p.V / 4;
     m2rnn_la_seg_scan_kernel<<<(unsigned)((n + 127) / 128), 128, 0, s>>>(p, decays_of(p), p.dST, 1);

@@ -41,7 +41,8 @@ __device__ __forceinline__ void la_log2(const LaParams& p, float x, float floor_
 }
 
 // Cumulative log-decays of a chunk's 128 tokens, from the chunk's start
-// through the token, by one warp (4 tokens a lane): F + I in shared memory,
+// through the token, by one warp (4 tokens a lane): F + I in shared memory
+// (128 whole parts of -256 at most: 16 bits),
 // and c[t] = the decay from t to the last token of its block of 32 or, with
 // FROM_PREV, from the last token of the block before through t.
 // steep: some block of 32 decays by more than 2^-90.  Elsewhere the decay
@@ -49,9 +50,14 @@ __device__ __forceinline__ void la_log2(const LaParams& p, float x, float floor_
 // and the reciprocal of another, both far inside fp32's range: c[] serves the
 // diagonal blocks too.
 struct LaTables {
-    float F[128], I[128], c[128];
+    float F[128], c[128];
+    short I[128];
     float steep, pad[3];
 };
+__device__ __forceinline__ float4 la_whole(const LaTables* tab, int t) {   // I[t..t+3]
+    const short4 w = *reinterpret_cast<const short4*>(&tab->I[t]);
+    return make_float4(w.x, w.y, w.z, w.w);
+}
 struct LaTablesZ : LaTables {
     float Z[128];   // gates at the floor, from the chunk's start through the token
 };
@@ -103,7 +109,7 @@ __device__ __forceinline__ void la_tables(Tab* tab, const LaParams& p, const flo
         sign = -1.f;
     }
     *reinterpret_cast<float4*>(&tab->F[lane * 4]) = make_float4(F[0], F[1], F[2], F[3]);
-    *reinterpret_cast<float4*>(&tab->I[lane * 4]) = make_float4(I[0], I[1], I[2], I[3]);
+    *reinterpret_cast<short4*>(&tab->I[lane * 4]) = make_short4((short)I[0], (short)I[1], (short)I[2], (short)I[3]);
     *reinterpret_cast<float4*>(&tab->c[lane * 4]) =
         make_float4(ex2_approx(sign * ((fe - F[0]) + (we - I[0]))), ex2_approx(sign * ((fe - F[1]) + (we - I[1]))),
                     ex2_approx(sign * ((fe - F[2]) + (we - I[2]))), ex2_approx(sign * ((fe - F[3]) + (we - I[3]))));

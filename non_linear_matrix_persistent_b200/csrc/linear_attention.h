@@ -34,7 +34,7 @@ struct LaParams {
     void* dv;
     float* df;              // [B*H][T]: the output, or (f_per_head) per-token values in the workspace
     float* dS0;             // may alias dST
-    int out32;              // dq, dk and dv start on 32 bytes
+    int out32;              // y, or dq, dk and dv, start on 32 bytes
     int dkq_fp32;           // dk and dq are fp32 whatever the inputs' type (per-head partials)
     // tensor-core kernels: time segments
     int segs;               // CTAs along T for each (b, h)
