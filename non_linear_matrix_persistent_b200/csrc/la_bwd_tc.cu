@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t tmem = 0;   // the CTA has all 512 columns
     const uint32_t sbase = smem_u32(smem);
 
     if (warp == NW) {
@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             id_dg = idesc_bf16_f32(KP, VP, 1, 1);                      // (a Q)ᵀ dY
         const uint64_t d_tile = sw128_desc(sbase, 16), d_mn = sw128_desc(sbase, kTileBytes),
                        d_op = sw128_desc(sbase, KP * 128);
+        const uint32_t one = lane == 0;
         constexpr uint32_t X = C::kOffX >> 4, OP = C::kOp >> 4, XP = C::kOffP >> 4;
         auto kmajor = [](int ks, int rows) { return (uint32_t)((ks >> 2) * (rows * 128 >> 4) + (ks & 3) * 2); };
         // rows (128 tokens) times a state in three terms, the first two at x
@@ -245,8 +246,8 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 const uint32_t op = e < 2 || C::kRoomy ? x + e * OP : XP;
 #pragma unroll
                 for (int ks = 0; ks < VP / 16; ++ks)
-                    tc_mma_f16_ss(tmem + d, d_tile + rows + kmajor(ks, 128), d_op + op + kmajor(ks, KP), id_ki,
-                                  e > 0 || ks > 0);
+                    mma_ss(d, d_tile + rows + kmajor(ks, 128), d_op + op + kmajor(ks, KP), id_ki,
+                                  e > 0 || ks > 0, one);
             }
         };
         auto tiles = [&](int i, uint32_t& q, uint32_t& k, uint32_t& v, uint32_t& dy) {
@@ -260,11 +261,11 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             tiles(i, q, k, v, dy);
 #pragma unroll
             for (int ks = 0; ks < KP / 16; ++ks)
-                tc_mma_f16_ss(tmem + C::kP, d_tile + k + kmajor(ks, 128), d_tile + q + kmajor(ks, 128), id_sc, ks > 0);
+                mma_ss(C::kP, d_tile + k + kmajor(ks, 128), d_tile + q + kmajor(ks, 128), id_sc, ks > 0, one);
 #pragma unroll
             for (int ks = 0; ks < VP / 16; ++ks)
-                tc_mma_f16_ss(tmem + C::kDP, d_tile + v + kmajor(ks, 128), d_tile + dy + kmajor(ks, 128), id_sc, ks > 0);
-            tc_commit(b_sc);
+                mma_ss(C::kDP, d_tile + v + kmajor(ks, 128), d_tile + dy + kmajor(ks, 128), id_sc, ks > 0, one);
+            mma_commit(b_sc, one);
         };
         bool ok = true;
         for (int i = 0; i < n; ++i) {
@@ -274,81 +275,69 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             auto inter_dv = [&]() {
 #pragma unroll
                 for (int ks = 0; ks < KP / 16; ++ks)
-                    tc_mma_f16_ss(tmem + C::kDV, d_tile + k + kmajor(ks, 128), d_op + X + (C::kG0 >> 4) + ks * 128, id_vi,
-                                  ks > 0);
+                    mma_ss(C::kDV, d_tile + k + kmajor(ks, 128), d_op + X + (C::kG0 >> 4) + ks * 128, id_vi,
+                                  ks > 0, one);
             };
             if (!(ok = la_wait(b_full + stage_of(i) * 8, stage_phase(i), abort_flag, limit))) break;
             if (C::kEarly) {
                 if (i > 0 && !(ok = la_wait(b_out, ph ^ 1, abort_flag, limit))) break;
-                if (lane == 0) scores(i);
+                scores(i);
             }
             if (!(ok = la_wait(r_s, ph, abort_flag, limit))) break;
             tc_fence_after();
-            if (lane == 0) {
-                if (!C::kEarly && C::kRoomy) scores(i);
-                times_state(C::kDQ, dy, X);                     // dY Sᵀ
-                if (C::kRoomy) {
-                    times_state(C::kDK, v, X + (C::kG0 >> 4));  // V Gᵀ
-                    if (C::kOwnDv) inter_dv();
-                }
-                tc_commit(b_in);
-                if (!C::kRoomy) scores(i);
+            if (!C::kEarly && C::kRoomy) scores(i);
+            times_state(C::kDQ, dy, X);                     // dY Sᵀ
+            if (C::kRoomy) {
+                times_state(C::kDK, v, X + (C::kG0 >> 4));  // V Gᵀ
+                if (C::kOwnDv) inter_dv();
             }
+            mma_commit(b_in, one);
+            if (!C::kRoomy) scores(i);
             if (!C::kRoomy) {
                 if (!(ok = la_wait(r_g, ph, abort_flag, limit))) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    times_state(C::kDK, v, X);
-                    tc_commit(b_g);
-                }
+                times_state(C::kDK, v, X);
+                mma_commit(b_g, one);
             }
             auto sum_for_G = [&]() -> bool {
                 if (!la_wait(r_aq, ph, abort_flag, limit)) return false;
                 tc_fence_after();
-                if (lane == 0) {
 #pragma unroll
-                    for (int x = 0; x < 3; ++x) {       // the terms of a q
-                        const uint32_t op = x < 2 || C::kRoomy ? X + x * (C::kQ >> 4) : XP;
+                for (int x = 0; x < 3; ++x) {       // the terms of a q
+                    const uint32_t op = x < 2 || C::kRoomy ? X + x * (C::kQ >> 4) : XP;
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            tc_mma_f16_ss(tmem + C::kDG, d_mn + op + ks * 128, d_mn + dy + ks * 128, id_dg,
-                                          x > 0 || ks > 0);
-                    }
-                    tc_commit(b_dg);
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ss(C::kDG, d_mn + op + ks * 128, d_mn + dy + ks * 128, id_dg,
+                                      x > 0 || ks > 0, one);
                 }
+                mma_commit(b_dg, one);
                 return true;
             };
             if (C::kAqFirst && !(ok = sum_for_G())) break;
             if (!(ok = la_wait(r_p, ph, abort_flag, limit))) break;
             tc_fence_after();
-            if (lane == 0) {
-                if (!C::kOwnDv) {
-                    inter_dv();
-                    tc_commit(b_dv);
-                }
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)      // contraction over s, the rows of the dP'ᵀ and k tiles
-                    tc_mma_f16_ss(tmem + C::kDQ, d_mn + XP + ks * 128, d_mn + k + ks * 128, id_dq, 1);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)      // over t: P'ᵀ and dP'ᵀ of 16 sinks over their 16 score columns
-                    tc_mma_f16_ts(tmem + C::kDK, tmem + C::kP + ks * 16 + 8, d_mn + q + ks * 128, id_dk, 1);
+            if (!C::kOwnDv) {
+                inter_dv();
+                mma_commit(b_dv, one);
             }
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)      // contraction over s, the rows of the dP'ᵀ and k tiles
+                mma_ss(C::kDQ, d_mn + XP + ks * 128, d_mn + k + ks * 128, id_dq, 1, one);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)      // over t: P'ᵀ and dP'ᵀ of 16 sinks over their 16 score columns
+                mma_ts(C::kDK, C::kP + ks * 16 + 8, d_mn + q + ks * 128, id_dk, 1, one);
             if (!C::kOwnDv) {
                 if (!(ok = la_wait(r_dv, ph, abort_flag, limit))) break;
                 tc_fence_after();
             }
-            if (lane == 0) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    tc_mma_f16_ts(tmem + C::kDV, tmem + C::kP + ks * 16, d_mn + dy + ks * 128, id_vi, 1);
-                tc_commit(b_out);
-            }
+            for (int ks = 0; ks < 8; ++ks)
+                mma_ts(C::kDV, C::kP + ks * 16, d_mn + dy + ks * 128, id_vi, 1, one);
+            mma_commit(b_out, one);
             if (!C::kAqFirst && !(ok = sum_for_G())) break;
         }
-        if (lane == 0) {   // nothing is in flight when the CTA ends
-            tc_commit(b_drain);
-            la_drain(b_drain, 0, limit);
-        }
+        mma_commit(b_drain, one);   // nothing is in flight when the CTA ends
+        if (lane == 0) la_drain(b_drain, 0, limit);
         __syncwarp();
     } else if (warp == NW + 1) {
         // ------------------------------------------------------ copies

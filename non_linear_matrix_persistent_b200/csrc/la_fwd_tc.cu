@@ -92,13 +92,13 @@ __device__ __forceinline__ void warp_arrive(uint32_t b) {
 // that is not scaled.
 template <int KP, int VP>
 __device__ __forceinline__ void outer_sum(uint32_t d, uint64_t mn, uint32_t a, uint32_t astep, uint32_t b, uint32_t bstep,
-                                          bool first) {
+                                          bool first, uint32_t one) {
     constexpr uint32_t id = idesc_bf16_f32(KP, VP, 1, 1);
 #pragma unroll
     for (int x = 0; x < 3; ++x)
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-            tc_mma_f16_ss(d, mn + a + x * astep + ks * 128, mn + b + x * bstep + ks * 128, id, !(first && x == 0 && ks == 0));
+            mma_ss(d, mn + a + x * astep + ks * 128, mn + b + x * bstep + ks * 128, id, !(first && x == 0 && ks == 0), one);
 }
 
 // The thread's part of a [KP][VP] accumulator or state: row kap, NS columns
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t tmem = 0;   // the CTA has all 512 columns
     const uint32_t sbase = smem_u32(smem);
 
     if (warp == kNW) {
@@ -238,15 +238,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                        d_s = sw128_desc(sbase + C::kOffS, KP * 128);
         constexpr uint32_t X = C::kOffX >> 4, XS = C::kTerm >> 4;
         auto tile = [](int ks) { return (uint32_t)((ks >> 2) * (kTileBytes >> 4) + (ks & 3) * 2); };
+        const uint32_t one = lane == 0;
         auto scores = [&](int i) {   // Q Kᵀ
             const uint32_t q = stage_of(i) * (C::kStage >> 4), k = q + (C::kQ >> 4);
             tc_fence_after();
-            if (lane == 0) {
 #pragma unroll
-                for (int ks = 0; ks < KP / 16; ++ks)
-                    tc_mma_f16_ss(tmem + (i % C::kScores) * 128, d_tile + q + tile(ks), d_tile + k + tile(ks), id_sc, ks > 0);
-                tc_commit(b_sc + (i & 1) * 8);
-            }
+            for (int ks = 0; ks < KP / 16; ++ks)
+                mma_ss((i % C::kScores) * 128, d_tile + q + tile(ks), d_tile + k + tile(ks), id_sc, ks > 0, one);
+            mma_commit(b_sc + (i & 1) * 8, one);
         };
         if (la_wait(b_qk, 0, abort_flag, limit)) {
             scores(0);
@@ -259,68 +258,63 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 bool next = i + 1 == n;
                 const uint64_t t0 = globaltimer_ns();
                 while (step < 3 || !next) {
-                    if (step == 0 && mbar_test_wait(r_s, ph)) {
+                    if (step == 0 && __all_sync(~0u, mbar_test_wait(r_s, ph))) {
                         tc_fence_after();
-                        if (lane == 0) {
 #pragma unroll
-                            for (int ks = 0; ks < KP / 16; ++ks)
-                                tc_mma_f16_ss(tmem + C::kQS, d_tile + q + tile(ks), d_s + ks * 128, id_v, ks > 0);
-                            if (C::kInPlace) tc_commit(b_qs);
-                        }
+                        for (int ks = 0; ks < KP / 16; ++ks)
+                            mma_ss(C::kQS, d_tile + q + tile(ks), d_s + ks * 128, id_v, ks > 0, one);
+                        if (C::kInPlace) mma_commit(b_qs, one);
                         step = 1;
-                    } else if (step == 1 && mbar_test_wait(r_p, ph) && mbar_test_wait(b_v + s * 8, stage_phase(i))) {
+                    } else if (step == 1 &&
+                               __all_sync(~0u, mbar_test_wait(r_p, ph) && mbar_test_wait(b_v + s * 8, stage_phase(i)))) {
                         tc_fence_after();
-                        if (lane == 0) {
 #pragma unroll
-                            for (int ks = 0; ks < 8; ++ks)   // P: 16 columns of bf16 pairs at the start of each block's 32
-                                tc_mma_f16_ts(tmem + C::kPV, tmem + (i % C::kScores) * 128 + (ks >> 1) * 32 + (ks & 1) * 8,
-                                              d_mn + v + ks * 128, id_v, ks > 0);
-                            tc_commit(b_pv);
-                        }
+                        for (int ks = 0; ks < 8; ++ks)   // P: 16 columns of bf16 pairs at the start of each block's 32
+                            mma_ts(C::kPV, (i % C::kScores) * 128 + (ks >> 1) * 32 + (ks & 1) * 8, d_mn + v + ks * 128, id_v,
+                                   ks > 0, one);
+                        mma_commit(b_pv, one);
                         step = 2;
-                    } else if (step == 2 && mbar_test_wait(r_k, ph)) {
+                    } else if (step == 2 && __all_sync(~0u, mbar_test_wait(r_k, ph))) {
                         tc_fence_after();
-                        if (lane == 0) {
-                            if (C::kInPlace) {
-                                constexpr uint32_t id = idesc_bf16_f32(KP, VP, 1, 1);
+                        if (C::kInPlace) {
+                            constexpr uint32_t id = idesc_bf16_f32(KP, VP, 1, 1);
 #pragma unroll
-                                for (int x = 0; x < 3; ++x) {
-                                    const uint32_t a = x == 0 ? k : x == 1 ? q : C::kOffS >> 4;
+                            for (int x = 0; x < 3; ++x) {
+                                const uint32_t a = x == 0 ? k : x == 1 ? q : C::kOffS >> 4;
 #pragma unroll
-                                    for (int ks = 0; ks < 8; ++ks)
-                                        tc_mma_f16_ss(tmem + C::kDS, d_mn + a + ks * 128, d_mn + v + ks * 128, id,
-                                                      x > 0 || ks > 0);
-                                }
-                            } else if (C::kScaleV) {
-                                outer_sum<KP, VP>(tmem + C::kDS, d_mn, k, 0, X, XS, true);
-                            } else {
-                                outer_sum<KP, VP>(tmem + C::kDS, d_mn, X, XS, v, 0, true);
+                                for (int ks = 0; ks < 8; ++ks)
+                                    mma_ss(C::kDS, d_mn + a + ks * 128, d_mn + v + ks * 128, id, x > 0 || ks > 0, one);
                             }
-                            tc_commit(b_ds);
+                        } else if (C::kScaleV) {
+                            outer_sum<KP, VP>(C::kDS, d_mn, k, 0, X, XS, true, one);
+                        } else {
+                            outer_sum<KP, VP>(C::kDS, d_mn, X, XS, v, 0, true, one);
                         }
+                        mma_commit(b_ds, one);
                         step = 3;
                     }
                     // (with two score matrices the place was free when r_s came: y of the chunk before had been read)
-                    if (!next && (C::kScores == 2 ? step > 0 : step > 1 && mbar_test_wait(b_pv, ph)) &&
-                        mbar_test_wait(b_qk + s1 * 8, stage_phase(i + 1))) {
+                    if (!next && (C::kScores == 2 ? step > 0 : step > 1) &&
+                        __all_sync(~0u, (C::kScores == 2 || mbar_test_wait(b_pv, ph)) &&
+                                            mbar_test_wait(b_qk + s1 * 8, stage_phase(i + 1)))) {
                         scores(i + 1);
                         next = true;
                     }
-                    if (*abort_flag) break;
-                    if (globaltimer_ns() - t0 > limit) {
-                        *abort_flag = 1;
-                        atomicOr(&g_la_status, 1u);
+                    const bool late = globaltimer_ns() - t0 > limit;
+                    if (__any_sync(~0u, late || *abort_flag)) {
+                        if (late) {
+                            *abort_flag = 1;
+                            atomicOr(&g_la_status, 1u);
+                        }
+                        i = n;
                         break;
                     }
                 }
-                if (*abort_flag) break;
                 __syncwarp();
             }
         }
-        if (lane == 0) {   // nothing is in flight when the CTA ends
-            tc_commit(b_drain);
-            la_drain(b_drain, 0, limit);
-        }
+        mma_commit(b_drain, one);   // nothing is in flight when the CTA ends
+        if (lane == 0) la_drain(b_drain, 0, limit);
         __syncwarp();
     } else if (warp == kNW + 1) {
         // ------------------------------------------------------ copies
@@ -587,33 +581,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         fence_mbarrier_init();
     }
     if (warp == kNW) {
-        tmem_alloc(smem_u32(tmem_slot), VP);
+        tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t tmem = 0;   // the CTA has all 512 columns
     const uint32_t sbase = smem_u32(smem);
 
     if (warp == kNW) {
         const uint64_t d_mn = sw128_desc(sbase, kTileBytes);
+        const uint32_t one = lane == 0;
         for (int i = 0; i < n; ++i) {
             if (!la_wait(b_full + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) break;
             if (!la_wait(r_k, i & 1, abort_flag, limit)) break;
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t k = (i & 1) * (C::kStage >> 4), v = k + (C::kQ >> 4),
-                               x = (C::kOffX + (i % C::kSets) * 3 * C::kTerm) >> 4, xs = C::kTerm >> 4;
-                if (C::kScaleV) outer_sum<KP, VP>(tmem, d_mn, k, 0, x, xs, i == 0);
-                else outer_sum<KP, VP>(tmem, d_mn, x, xs, v, 0, i == 0);
-                tc_commit(b_ds + (i & 1) * 8);
-            }
+            const uint32_t k = (i & 1) * (C::kStage >> 4), v = k + (C::kQ >> 4),
+                           x = (C::kOffX + (i % C::kSets) * 3 * C::kTerm) >> 4, xs = C::kTerm >> 4;
+            if (C::kScaleV) outer_sum<KP, VP>(0, d_mn, k, 0, x, xs, i == 0, one);
+            else outer_sum<KP, VP>(0, d_mn, x, xs, v, 0, i == 0, one);
+            mma_commit(b_ds + (i & 1) * 8, one);
         }
-        if (lane == 0) {
-            tc_commit(b_drain);
-            la_drain(b_drain, 0, limit);
-        }
+        mma_commit(b_drain, one);
+        if (lane == 0) la_drain(b_drain, 0, limit);
         __syncwarp();
     } else if (warp == kNW + 1) {
         if (lane == 0) {
@@ -684,7 +675,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     __syncthreads();
     if (warp == kNW) {
         tc_fence_after();
-        tmem_dealloc(tmem, VP);
+        tmem_dealloc(tmem, 512);
     }
 }
 
