@@ -90,7 +90,7 @@ struct BCfg {
     static constexpr int NQ = KP / 4, NV = VP / 4;              // columns of dq, dk and of dv per thread
 };
 
-// Column sums over the 32 lanes of N = 16 or 32 values a lane: lane l gets
+// Column sums over the 32 lanes of N = 8 or 16 values a lane: lane l gets
 // column l·N/32's.
 template <int N>
 __device__ __forceinline__ float column_sums(float (&r)[N]) {
@@ -105,7 +105,9 @@ __device__ __forceinline__ float column_sums(float (&r)[N]) {
             r[e] = keep + __shfl_xor_sync(~0u, send, d);
         }
     }
-    return N == 32 ? r[0] : r[0] + __shfl_xor_sync(~0u, r[0], 1);
+#pragma unroll
+    for (int d = 16 / N; d; d >>= 1) r[0] += __shfl_xor_sync(~0u, r[0], d);
+    return r[0];
 }
 
 // One source's block of 32 sinks: from the raw scores (lane = source s, 32
@@ -118,70 +120,72 @@ __device__ __forceinline__ float column_sums(float (&r)[N]) {
 // count for df alone, or blocks too steep for the product: the diagonal takes
 // an exponential each.  (One body for diagonal and other blocks: the two would
 // not fit the instruction cache together.)
-template <bool ZERO, int NSUM, class Place>
+// PW: columns at a time, 16 or, where registers are short, 8.
+template <bool ZERO, int PW, class Place>
 __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const LaTablesZ* tab, int t0, float Fs, float Is,
                                              float Zs, float r, int first, float* cut, Place dp) {
     const int lane = threadIdx.x & 31;
     float run = 0.f;
-    float R[NSUM];
 #pragma unroll
     for (int h = 16; h >= 0; h -= 16) {
-        uint32_t x[16], y[16];
-        tmem_ld<16>(tp + h, x);
-        tmem_ld<16>(tdp + h, y);
-        float d[16], z[ZERO ? 16 : 1];
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-            const float4 c = *reinterpret_cast<const float4*>(&tab->c[t0 + h + e]);
-            d[e] = r * c.x; d[e + 1] = r * c.y; d[e + 2] = r * c.z; d[e + 3] = r * c.w;
-            if (ZERO && first >= 0) {
-                const float4 f = *reinterpret_cast<const float4*>(&tab->F[t0 + h + e]);
-                const float4 w = la_whole(tab, t0 + h + e);
-                d[e] = ex2_approx((f.x - Fs) + (w.x - Is)); d[e + 1] = ex2_approx((f.y - Fs) + (w.y - Is));
-                d[e + 2] = ex2_approx((f.z - Fs) + (w.z - Is)); d[e + 3] = ex2_approx((f.w - Fs) + (w.w - Is));
-            }
-#pragma unroll
-            for (int o = 0; o < 4; ++o) d[e + o] = h + e + o >= first ? d[e + o] : 0.f;
-            if constexpr (ZERO) {
-                const float4 zs = *reinterpret_cast<const float4*>(&tab->Z[t0 + h + e]);
-                z[e] = zs.x != Zs ? 0.f : d[e]; z[e + 1] = zs.y != Zs ? 0.f : d[e + 1];
-                z[e + 2] = zs.z != Zs ? 0.f : d[e + 2]; z[e + 3] = zs.w != Zs ? 0.f : d[e + 3];
-            }
-        }
-        tc_wait_ld();
-        reg_fence(x);
-        reg_fence(y);
         uint32_t pp[8], pd[8];
 #pragma unroll
-        for (int e = 14; e >= 0; e -= 2) {
-            const float2 P = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                         Q = make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), D = make_float2(d[e], d[e + 1]);
-            float2 PD = __fmul2_rn(P, D);
-            const float2 W = __fmul2_rn(PD, Q);
-            float2 QD = __fmul2_rn(Q, D);
-            if constexpr (ZERO) {
-                const float2 Zd = make_float2(z[e], z[e + 1]);
-                PD = __fmul2_rn(P, Zd);
-                QD = __fmul2_rn(Q, Zd);
+        for (int g = 16 - PW; g >= 0; g -= PW) {
+            uint32_t x[PW], y[PW];
+            tmem_ld<PW>(tp + h + g, x);
+            tmem_ld<PW>(tdp + h + g, y);
+            float d[PW], z[ZERO ? PW : 1];
+#pragma unroll
+            for (int e = 0; e < PW; e += 4) {
+                const int at = h + g + e;
+                const float4 c = *reinterpret_cast<const float4*>(&tab->c[t0 + at]);
+                d[e] = r * c.x; d[e + 1] = r * c.y; d[e + 2] = r * c.z; d[e + 3] = r * c.w;
+                if (ZERO && first >= 0) {
+                    const float4 f = *reinterpret_cast<const float4*>(&tab->F[t0 + at]);
+                    const float4 w = la_whole(tab, t0 + at);
+                    d[e] = ex2_approx((f.x - Fs) + (w.x - Is)); d[e + 1] = ex2_approx((f.y - Fs) + (w.y - Is));
+                    d[e + 2] = ex2_approx((f.z - Fs) + (w.z - Is)); d[e + 3] = ex2_approx((f.w - Fs) + (w.w - Is));
+                }
+#pragma unroll
+                for (int o = 0; o < 4; ++o) d[e + o] = at + o >= first ? d[e + o] : 0.f;
+                if constexpr (ZERO) {
+                    const float4 zs = *reinterpret_cast<const float4*>(&tab->Z[t0 + at]);
+                    z[e] = zs.x != Zs ? 0.f : d[e]; z[e + 1] = zs.y != Zs ? 0.f : d[e + 1];
+                    z[e + 2] = zs.z != Zs ? 0.f : d[e + 2]; z[e + 3] = zs.w != Zs ? 0.f : d[e + 3];
+                }
             }
-            pp[e / 2] = pack_bf16(PD.x, PD.y);
-            pd[e / 2] = pack_bf16(QD.x, QD.y);
-            const int at = NSUM == 32 ? h + e : e;
-            run += W.y;
-            R[at + 1] = h + e + 1 > first ? run : 0.f;   // sources strictly before the gate
-            run += W.x;
-            R[at] = h + e > first ? run : 0.f;
+            tc_wait_ld();
+            reg_fence(x);
+            reg_fence(y);
+            float R[PW];
+#pragma unroll
+            for (int e = PW - 2; e >= 0; e -= 2) {
+                const float2 P = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                             Q = make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])),
+                             D = make_float2(d[e], d[e + 1]);
+                float2 PD = __fmul2_rn(P, D);
+                const float2 W = __fmul2_rn(PD, Q);
+                float2 QD = __fmul2_rn(Q, D);
+                if constexpr (ZERO) {
+                    const float2 Zd = make_float2(z[e], z[e + 1]);
+                    PD = __fmul2_rn(P, Zd);
+                    QD = __fmul2_rn(Q, Zd);
+                }
+                pp[(g + e) / 2] = pack_bf16(PD.x, PD.y);
+                pd[(g + e) / 2] = pack_bf16(QD.x, QD.y);
+                run += W.y;
+                R[e + 1] = h + g + e + 1 > first ? run : 0.f;   // sources strictly before the gate
+                run += W.x;
+                R[e] = h + g + e > first ? run : 0.f;
+            }
+            const float c = column_sums(R);
+            if (!(lane & (32 / PW - 1))) cut[t0 + h + g + lane / (32 / PW)] = c;
         }
         tmem_st_32x32b<8>(tp + h, pp);       // inside the half that has been read
         tmem_st_32x32b<8>(tp + h + 8, pd);
         *reinterpret_cast<uint4*>(dp(t0 + h)) = make_uint4(pd[0], pd[1], pd[2], pd[3]);
         *reinterpret_cast<uint4*>(dp(t0 + h + 8)) = make_uint4(pd[4], pd[5], pd[6], pd[7]);
-        if constexpr (NSUM == 16) {
-            const float c = column_sums(R);
-            if (!(lane & 1)) cut[t0 + h + (lane >> 1)] = c;
-        }
     }
-    if constexpr (NSUM == 32) cut[t0 + lane] = column_sums(R);
     return run;
 }
 
@@ -712,7 +716,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 // the decay from the source to the block before the sinks' (for its own block, a reciprocal)
                 const float Fp = wg ? tab->F[wg * 32 - 1] : 0.f, Ip = wg ? tab->I[wg * 32 - 1] : 0.f;
                 const float r = ex2_approx((Fp - Ft) + (Ip - It));
-                constexpr int N = C::NS <= 16 ? 32 : 16;   // registers
+                constexpr int N = C::NS <= 16 ? 16 : 8;
                 if (Ze != 0.f || tab->steep != 0.f)
                     run = score_block<true, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place);
                 else

@@ -247,70 +247,62 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 mma_ss((i % C::kScores) * 128, d_tile + q + tile(ks), d_tile + k + tile(ks), id_sc, ks > 0, one);
             mma_commit(b_sc + (i & 1) * 8, one);
         };
+        // Q S, P V and the state's sum of a chunk in this order, the next
+        // chunk's scores as soon as its tiles are there and their place is free
         if (la_wait(b_qk, 0, abort_flag, limit)) {
             scores(0);
             for (int i = 0; i < n; ++i) {
-                // Q S, P V and the state's sum in this order, the next chunk's
-                // scores as soon as its tiles are there and their place is free
                 const int ph = i & 1, s = stage_of(i), s1 = stage_of(i + 1);
                 const uint32_t q = s * (C::kStage >> 4), k = q + (C::kQ >> 4), v = k + (C::kQ >> 4);
-                int step = 0;
                 bool next = i + 1 == n;
-                const uint64_t t0 = globaltimer_ns();
-                while (step < 3 || !next) {
-                    if (step == 0 && __all_sync(~0u, mbar_test_wait(r_s, ph))) {
-                        tc_fence_after();
-#pragma unroll
-                        for (int ks = 0; ks < KP / 16; ++ks)
-                            mma_ss(C::kQS, d_tile + q + tile(ks), d_s + ks * 128, id_v, ks > 0, one);
-                        if (C::kInPlace) mma_commit(b_qs, one);
-                        step = 1;
-                    } else if (step == 1 &&
-                               __all_sync(~0u, mbar_test_wait(r_p, ph) && mbar_test_wait(b_v + s * 8, stage_phase(i)))) {
-                        tc_fence_after();
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)   // P: 16 columns of bf16 pairs at the start of each block's 32
-                            mma_ts(C::kPV, (i % C::kScores) * 128 + (ks >> 1) * 32 + (ks & 1) * 8, d_mn + v + ks * 128, id_v,
-                                   ks > 0, one);
-                        mma_commit(b_pv, one);
-                        step = 2;
-                    } else if (step == 2 && __all_sync(~0u, mbar_test_wait(r_k, ph))) {
-                        tc_fence_after();
-                        if (C::kInPlace) {
-                            constexpr uint32_t id = idesc_bf16_f32(KP, VP, 1, 1);
-#pragma unroll
-                            for (int x = 0; x < 3; ++x) {
-                                const uint32_t a = x == 0 ? k : x == 1 ? q : C::kOffS >> 4;
-#pragma unroll
-                                for (int ks = 0; ks < 8; ++ks)
-                                    mma_ss(C::kDS, d_mn + a + ks * 128, d_mn + v + ks * 128, id, x > 0 || ks > 0, one);
-                            }
-                        } else if (C::kScaleV) {
-                            outer_sum<KP, VP>(C::kDS, d_mn, k, 0, X, XS, true, one);
-                        } else {
-                            outer_sum<KP, VP>(C::kDS, d_mn, X, XS, v, 0, true, one);
-                        }
-                        mma_commit(b_ds, one);
-                        step = 3;
+                auto next_scores = [&](bool wait) -> bool {
+                    if (next) return true;
+                    if (wait) {
+                        if (C::kScores == 1 && !la_wait(b_pv, ph, abort_flag, limit)) return false;
+                        if (!la_wait(b_qk + s1 * 8, stage_phase(i + 1), abort_flag, limit)) return false;
+                    } else if (!__all_sync(~0u, (C::kScores == 2 || mbar_test_wait(b_pv, ph)) &&
+                                                    mbar_test_wait(b_qk + s1 * 8, stage_phase(i + 1)))) {
+                        return true;
                     }
-                    // (with two score matrices the place was free when r_s came: y of the chunk before had been read)
-                    if (!next && (C::kScores == 2 ? step > 0 : step > 1) &&
-                        __all_sync(~0u, (C::kScores == 2 || mbar_test_wait(b_pv, ph)) &&
-                                            mbar_test_wait(b_qk + s1 * 8, stage_phase(i + 1)))) {
-                        scores(i + 1);
-                        next = true;
+                    scores(i + 1);
+                    next = true;
+                    return true;
+                };
+                if (!la_wait(r_s, ph, abort_flag, limit)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < KP / 16; ++ks)
+                    mma_ss(C::kQS, d_tile + q + tile(ks), d_s + ks * 128, id_v, ks > 0, one);
+                if (C::kInPlace) mma_commit(b_qs, one);
+                if (!la_wait(b_v + s * 8, stage_phase(i), abort_flag, limit)) break;
+                if (!la_wait(r_p, ph, abort_flag, limit)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)   // P: 16 columns of bf16 pairs at the start of each block's 32
+                    mma_ts(C::kPV, (i % C::kScores) * 128 + (ks >> 1) * 32 + (ks & 1) * 8, d_mn + v + ks * 128, id_v, ks > 0,
+                           one);
+                mma_commit(b_pv, one);
+                // (of two score matrices the other is free since r_s: y of the chunk before had been read)
+                if (C::kScores == 2) next_scores(false);
+                if (!la_wait(r_k, ph, abort_flag, limit)) break;
+                tc_fence_after();
+                if (C::kScores == 1) next_scores(false);
+                if (C::kInPlace) {
+                    constexpr uint32_t id = idesc_bf16_f32(KP, VP, 1, 1);
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) {
+                        const uint32_t a = x == 0 ? k : x == 1 ? q : C::kOffS >> 4;
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_ss(C::kDS, d_mn + a + ks * 128, d_mn + v + ks * 128, id, x > 0 || ks > 0, one);
                     }
-                    const bool late = globaltimer_ns() - t0 > limit;
-                    if (__any_sync(~0u, late || *abort_flag)) {
-                        if (late) {
-                            *abort_flag = 1;
-                            atomicOr(&g_la_status, 1u);
-                        }
-                        i = n;
-                        break;
-                    }
+                } else if (C::kScaleV) {
+                    outer_sum<KP, VP>(C::kDS, d_mn, k, 0, X, XS, true, one);
+                } else {
+                    outer_sum<KP, VP>(C::kDS, d_mn, X, XS, v, 0, true, one);
                 }
-                __syncwarp();
+                mma_commit(b_ds, one);
+                if (!next_scores(true)) break;
             }
         }
         mma_commit(b_drain, one);   // nothing is in flight when the CTA ends

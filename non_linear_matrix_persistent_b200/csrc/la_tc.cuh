@@ -233,18 +233,35 @@ __device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk
 __device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 // ---------------------------------------------------------------- waits
+// One attempt, suspended by the hardware until the phase completes or about 0.1
+// ms have passed: warps that poll instead take issue slots from those at work
+// and from the one that feeds the tensor core.
+__device__ __forceinline__ bool la_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(100000u)
+        : "memory");
+    return ok != 0;
+}
 // Bounded mbarrier wait: false when it runs longer than the limit or another
 // thread of the CTA has given up.
 __device__ __forceinline__ bool la_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
+    uint64_t t0 = 0;
+    for (int k = 1;; ++k) {
         if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > limit_ns) {
-            *abort_flag = 1;
-            atomicOr(&g_la_status, 1u);
-            return false;
+        if ((k & 63) == 0) {
+            if (*abort_flag) return false;
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > limit_ns) {
+                *abort_flag = 1;
+                atomicOr(&g_la_status, 1u);
+                return false;
+            }
         }
     }
 }
