@@ -374,28 +374,17 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 for (int x = 0; x < VP / 64; ++x)
                     tma_tile(base + 2 * C::kQ + x * kTileBytes, &maps.v, x * 64, t, bh, full);
             };
-            // into L2 a chunk before its load: the tiles and the checkpoint
+            // the next chunk's checkpoint into L2 (its tiles too, or two chunks
+            // ahead, was slower: 7B-MoE shape 515 against 475 us)
             auto prefetch = [&](int i) {
-                if (i >= n || p.fault) return;
-                const int c = chunk_of(i), t = c * kLaChunk;
-                bulk_prefetch(p.ckpt + ((size_t)bh * nchunks + c) * p.K * p.V, p.K * p.V * 4);
-                if (i < C::kStages) return;
-#pragma unroll
-                for (int x = 0; x < VP / 64; ++x) tma_prefetch_tile(&maps.dy, x * 64, t, bh);
-#pragma unroll
-                for (int x = 0; x < KP / 64; ++x) {
-                    tma_prefetch_tile(&maps.q, x * 64, t, qk);
-                    tma_prefetch_tile(&maps.k, x * 64, t, qk);
-                }
-#pragma unroll
-                for (int x = 0; x < VP / 64; ++x) tma_prefetch_tile(&maps.v, x * 64, t, bh);
+                if (i < n && !p.fault)
+                    bulk_prefetch(p.ckpt + ((size_t)bh * nchunks + chunk_of(i)) * p.K * p.V, p.K * p.V * 4);
             };
             for (int i = 0; i < C::kStages && i < n; ++i) load(i, true, true);
-            prefetch(1);
             bool ok = true;
             int i = 0;
             for (; i < n; ++i) {
-                prefetch(i + 2);
+                prefetch(i + 1);
                 if (!C::kRoomy) {
                     if (!(ok = la_wait(r_aq, i & 1, abort_flag, limit) && la_wait(r_df, i & 1, abort_flag, limit))) break;
                     if (i + 1 < n) load(i + 1, true, false);

@@ -213,11 +213,6 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
-// The same box into L2 only, ahead of its load.
-__device__ __forceinline__ void tma_prefetch_tile(const CUtensorMap* map, int x, int t, int z) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(t), "r"(z)
-                 : "memory");
-}
 // `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
 __device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
