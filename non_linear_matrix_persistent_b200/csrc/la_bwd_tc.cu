@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             id_dq = idesc_bf16_f32(128, KP, 1, 1),                     // dP' K
             id_dk = idesc_bf16_f32(128, KP, 0, 1),                     // dP'ᵀ Q
             id_dg = idesc_bf16_f32(KP, VP, 1, 1);                      // (a Q)ᵀ dY
-        const uint64_t d_tile = sw128_desc(sbase, 16), d_mn = sw128_desc(sbase, kTileBytes),
+        const Desc d_tile = sw128_desc(sbase, 16), d_mn = sw128_desc(sbase, kTileBytes),
                        d_op = sw128_desc(sbase, KP * 128);
         const uint32_t one = lane == 0;
         constexpr uint32_t X = C::kOffX >> 4, OP = C::kOp >> 4, XP = C::kOffP >> 4;
@@ -282,12 +282,12 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                     mma_ss(C::kDV, d_tile + k + kmajor(ks, 128), d_op + X + (C::kG0 >> 4) + ks * 128, id_vi,
                                   ks > 0, one);
             };
-            if (!(ok = la_wait(b_full + stage_of(i) * 8, stage_phase(i), abort_flag, limit))) break;
+            if (!(ok = la_wait_warp(b_full + stage_of(i) * 8, stage_phase(i), abort_flag, limit))) break;
             if (C::kEarly) {
-                if (i > 0 && !(ok = la_wait(b_out, ph ^ 1, abort_flag, limit))) break;
+                if (i > 0 && !(ok = la_wait_warp(b_out, ph ^ 1, abort_flag, limit))) break;
                 scores(i);
             }
-            if (!(ok = la_wait(r_s, ph, abort_flag, limit))) break;
+            if (!(ok = la_wait_warp(r_s, ph, abort_flag, limit))) break;
             tc_fence_after();
             if (!C::kEarly && C::kRoomy) scores(i);
             times_state(C::kDQ, dy, X);                     // dY Sᵀ
@@ -298,13 +298,13 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             mma_commit(b_in, one);
             if (!C::kRoomy) scores(i);
             if (!C::kRoomy) {
-                if (!(ok = la_wait(r_g, ph, abort_flag, limit))) break;
+                if (!(ok = la_wait_warp(r_g, ph, abort_flag, limit))) break;
                 tc_fence_after();
                 times_state(C::kDK, v, X);
                 mma_commit(b_g, one);
             }
             auto sum_for_G = [&]() -> bool {
-                if (!la_wait(r_aq, ph, abort_flag, limit)) return false;
+                if (!la_wait_warp(r_aq, ph, abort_flag, limit)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {       // the terms of a q
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 return true;
             };
             if (C::kAqFirst && !(ok = sum_for_G())) break;
-            if (!(ok = la_wait(r_p, ph, abort_flag, limit))) break;
+            if (!(ok = la_wait_warp(r_p, ph, abort_flag, limit))) break;
             tc_fence_after();
             if (!C::kOwnDv) {
                 inter_dv();
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             for (int ks = 0; ks < 8; ++ks)      // over t: P'ᵀ and dP'ᵀ of 16 sinks over their 16 score columns
                 mma_ts(C::kDK, C::kP + ks * 16 + 8, d_mn + q + ks * 128, id_dk, 1, one);
             if (!C::kOwnDv) {
-                if (!(ok = la_wait(r_dv, ph, abort_flag, limit))) break;
+                if (!(ok = la_wait_warp(r_dv, ph, abort_flag, limit))) break;
                 tc_fence_after();
             }
 #pragma unroll

@@ -91,7 +91,7 @@ __device__ __forceinline__ void warp_arrive(uint32_t b) {
 // descriptor's start); astep, bstep: from one term to the next, 0 for the side
 // that is not scaled.
 template <int KP, int VP>
-__device__ __forceinline__ void outer_sum(uint32_t d, uint64_t mn, uint32_t a, uint32_t astep, uint32_t b, uint32_t bstep,
+__device__ __forceinline__ void outer_sum(uint32_t d, Desc mn, uint32_t a, uint32_t astep, uint32_t b, uint32_t bstep,
                                           bool first, uint32_t one) {
     constexpr uint32_t id = idesc_bf16_f32(KP, VP, 1, 1);
 #pragma unroll
@@ -209,14 +209,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     // b_qk, b_v: one per stage; pairs of barriers serve chunks in turn, where one side may be a chunk ahead
     const uint32_t b_qk = bar(0), b_v = bar(3), b_sc = bar(6), b_tab = bar(8), t_free = bar(10), r_y = bar(12),
-                   r_p = bar(14), r_s = bar(15), r_k = bar(16), b_pv = bar(17), b_ds = bar(18), b_qs = bar(19),
-                   b_drain = bar(20);
+                   r_p = bar(14), r_s = bar(15), r_k = bar(16), b_pv = bar(17), b_ds = bar(18), b_drain = bar(19);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint64_t limit = p.wait_limit_ns;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 21; ++i) mbar_init(bar(i), 1);
+        for (int i = 0; i < 20; ++i) mbar_init(bar(i), 1);
         for (uint32_t b : {t_free, t_free + 8, r_y, r_y + 8, r_p, r_s, r_k}) mbar_init(b, kNW);
         *abort_flag = 0;
         fence_mbarrier_init();
@@ -234,7 +233,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (warp == kNW) {
         // ------------------------------------------------------ products
         constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, 0, 0), id_v = idesc_bf16_f32(128, VP, 0, 1);
-        const uint64_t d_tile = sw128_desc(sbase, 16), d_mn = sw128_desc(sbase, kTileBytes),
+        const Desc d_tile = sw128_desc(sbase, 16), d_mn = sw128_desc(sbase, kTileBytes),
                        d_s = sw128_desc(sbase + C::kOffS, KP * 128);
         constexpr uint32_t X = C::kOffX >> 4, XS = C::kTerm >> 4;
         auto tile = [](int ks) { return (uint32_t)((ks >> 2) * (kTileBytes >> 4) + (ks & 3) * 2); };
@@ -247,9 +246,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 mma_ss((i % C::kScores) * 128, d_tile + q + tile(ks), d_tile + k + tile(ks), id_sc, ks > 0, one);
             mma_commit(b_sc + (i & 1) * 8, one);
         };
-        // Q S, P V and the state's sum of a chunk in this order, the next
-        // chunk's scores as soon as its tiles are there and their place is free
-        if (la_wait(b_qk, 0, abort_flag, limit)) {
+        // P V, Q S (which waits for S) and the state's sum of a chunk in this order,
+        // the next chunk's scores as soon as its tiles are there and their place is free
+        if (la_wait_warp(b_qk, 0, abort_flag, limit)) {
             scores(0);
             for (int i = 0; i < n; ++i) {
                 const int ph = i & 1, s = stage_of(i), s1 = stage_of(i + 1);
@@ -258,8 +257,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 auto next_scores = [&](bool wait) -> bool {
                     if (next) return true;
                     if (wait) {
-                        if (C::kScores == 1 && !la_wait(b_pv, ph, abort_flag, limit)) return false;
-                        if (!la_wait(b_qk + s1 * 8, stage_phase(i + 1), abort_flag, limit)) return false;
+                        if (C::kScores == 1 && !la_wait_warp(b_pv, ph, abort_flag, limit)) return false;
+                        if (!la_wait_warp(b_qk + s1 * 8, stage_phase(i + 1), abort_flag, limit)) return false;
                     } else if (!__all_sync(~0u, (C::kScores == 2 || mbar_test_wait(b_pv, ph)) &&
                                                     mbar_test_wait(b_qk + s1 * 8, stage_phase(i + 1)))) {
                         return true;
@@ -268,23 +267,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     next = true;
                     return true;
                 };
-                if (!la_wait(r_s, ph, abort_flag, limit)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < KP / 16; ++ks)
-                    mma_ss(C::kQS, d_tile + q + tile(ks), d_s + ks * 128, id_v, ks > 0, one);
-                if (C::kInPlace) mma_commit(b_qs, one);
-                if (!la_wait(b_v + s * 8, stage_phase(i), abort_flag, limit)) break;
-                if (!la_wait(r_p, ph, abort_flag, limit)) break;
+                if (!la_wait_warp(b_v + s * 8, stage_phase(i), abort_flag, limit)) break;
+                if (!la_wait_warp(r_p, ph, abort_flag, limit)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)   // P: 16 columns of bf16 pairs at the start of each block's 32
                     mma_ts(C::kPV, (i % C::kScores) * 128 + (ks >> 1) * 32 + (ks & 1) * 8, d_mn + v + ks * 128, id_v, ks > 0,
                            one);
+                if (!la_wait_warp(r_s, ph, abort_flag, limit)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < KP / 16; ++ks)
+                    mma_ss(C::kQS, d_tile + q + tile(ks), d_s + ks * 128, id_v, ks > 0, one);
                 mma_commit(b_pv, one);
                 // (of two score matrices the other is free since r_s: y of the chunk before had been read)
                 if (C::kScores == 2) next_scores(false);
-                if (!la_wait(r_k, ph, abort_flag, limit)) break;
+                if (!la_wait_warp(r_k, ph, abort_flag, limit)) break;
                 tc_fence_after();
                 if (C::kScores == 1) next_scores(false);
                 if (C::kInPlace) {
@@ -449,7 +447,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         auto put_terms = [&](int i) -> bool {
             const uint32_t full = C::kScaleV ? b_v : b_qk;
             if (!la_wait(full + stage_of(i) * 8, stage_phase(i), abort_flag, limit)) return false;
-            if (C::kInPlace && !la_wait(b_qs, i & 1, abort_flag, limit)) return false;
+            if (C::kInPlace && !la_wait(b_pv, i & 1, abort_flag, limit)) return false;   // Q S has read q and S
             uint8_t* stage = smem + stage_of(i) * C::kStage;
             constexpr int kCh = C::kTerm / 128 / 16 / 4;         // 16-byte chunks of the row for this thread
 #pragma unroll
@@ -583,11 +581,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t sbase = smem_u32(smem);
 
     if (warp == kNW) {
-        const uint64_t d_mn = sw128_desc(sbase, kTileBytes);
+        const Desc d_mn = sw128_desc(sbase, kTileBytes);
         const uint32_t one = lane == 0;
         for (int i = 0; i < n; ++i) {
-            if (!la_wait(b_full + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) break;
-            if (!la_wait(r_k, i & 1, abort_flag, limit)) break;
+            if (!la_wait_warp(b_full + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) break;
+            if (!la_wait_warp(r_k, i & 1, abort_flag, limit)) break;
             tc_fence_after();
             const uint32_t k = (i & 1) * (C::kStage >> 4), v = k + (C::kQ >> 4),
                            x = (C::kOffX + (i % C::kSets) * 3 * C::kTerm) >> 4, xs = C::kTerm >> 4;

@@ -125,36 +125,43 @@ __device__ __forceinline__ void la_load_f(const LaParams& p, int bh, int c, floa
 // Byte position of the 16-byte chunk `ch` (of 8) of row `row` in a swizzled tile.
 __device__ __forceinline__ uint32_t sw128(int row, int ch) { return row * 128 + ((ch ^ (row & 7)) << 4); }
 
+// A descriptor as its two words: positions are added to the lower one alone.
+struct Desc {
+    uint32_t lo, hi;
+};
+__device__ __forceinline__ Desc operator+(Desc d, uint32_t at) { return {d.lo + at, d.hi}; }
 // Descriptor of a 128-byte-swizzled operand.  K-major: lbo unused, sbo = 1024
 // (8 rows).  MN-major: lbo = bytes from one 64-column tile to the next, sbo =
 // 1024 (8 contraction rows).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo) {
-    return smem_desc(saddr, lbo, 1024) | (2ull << 61);
+__device__ __forceinline__ Desc sw128_desc(uint32_t saddr, uint32_t lbo) {
+    const uint64_t d = smem_desc(saddr, lbo, 1024) | (2ull << 61);
+    return {(uint32_t)d, (uint32_t)(d >> 32)};
 }
 
 // Products issued by a whole warp, of which the lane with `one` != 0 issues: the
 // operands are the same in every lane, so that they are computed and kept in
-// uniform registers.  (Issued from a branch that only one lane takes, a product
-// cost 97 cycles of moves beside the working warps; the tensor core takes 52.)
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate, uint32_t one) {
+// uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, Desc a, Desc b, uint32_t idesc, uint32_t accumulate, uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(one)
         : "memory");
 }
 // The same with A in tensor memory: 128 lanes, two bf16 per 32-bit column.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate, uint32_t one) {
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, Desc b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(one)
         : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t one) {
@@ -257,6 +264,43 @@ __device__ __forceinline__ bool la_wait(uint32_t bar, uint32_t parity, volatile 
                 atomicOr(&g_la_status, 1u);
                 return false;
             }
+        }
+    }
+}
+// The same for the warp that issues the products, with an outcome that the
+// compiler knows to be the warp's: the attempts are one asm loop and the
+// answers are voted on, so that everything it computes stays in uniform
+// registers, where the products take their operands from.
+__device__ __forceinline__ bool la_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                             uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+            "mov.u32 n, 64;\n\t"
+            "LA_TRY_%=:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "@p bra LA_DONE_%=;\n\t"
+            "sub.u32 n, n, 1;\n\t"
+            "setp.ne.u32 q, n, 0;\n\t"
+            "@q bra LA_TRY_%=;\n\t"
+            "LA_DONE_%=:\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (__all_sync(~0u, ok)) return true;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        const bool late = t - t0 > limit_ns;
+        if (__any_sync(~0u, late || *abort_flag)) {
+            if (late) {
+                *abort_flag = 1;
+                atomicOr(&g_la_status, 1u);
+            }
+            __syncwarp();
+            return false;
         }
     }
 }
