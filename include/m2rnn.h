@@ -213,8 +213,8 @@ m2rnn_status m2rnn_backward_noalloc(const m2rnn_dims* d,
  * M2RNN_MODE_FP32_DEBUG everything is fp32 and runs on the CUDA cores.  The
  * other modes are refused.  States, gates and their gradients are fp32.
  *
- * Gates lie in [0, 1].  A gate of exactly 0 discards the state before it (in
- * the tensor-core backward, one below 2^-100 does too).  A state that
+ * Gates lie in [0, 1].  A gate of 0 (or below 2^-126, which fp32 arithmetic
+ * here flushes to 0) discards the state before it.  A state that
  * holds an infinity or NaN is not discarded by a gate of 0 (0·inf = NaN, as in
  * the formula).
  *
@@ -298,11 +298,14 @@ void m2rnn_set_wait_limit_ns(uint64_t ns);
 
 /* Test hook: host-side fault injection for later launches (not part of the
  * method).  0 = none; 1 = the input producer of the bf16 forward (tensor-core
- * or row kernel) and of the tensor-core backwards stops after its first chunk
- * (16 steps forward, one checkpoint chunk backward), so the kernel's bounded
+ * or row kernel), of the tensor-core backwards and of the tensor-core kernels
+ * of linear attention stops after its first chunk
+ * (16 steps forward, one checkpoint chunk backward, 128 tokens of linear
+ * attention), so the kernel's bounded
  * waits run out: the
  * call returns M2RNN_OK, the kernel exits early with undefined outputs and
- * m2rnn_get_device_status reports M2RNN_ERR_DEVICE_TIMEOUT (after about the
+ * m2rnn_get_device_status (m2rnn_linear_attention_status) reports
+ * M2RNN_ERR_DEVICE_TIMEOUT (after about the
  * wait limit).  Returns M2RNN_OK, or M2RNN_ERR_INVALID_ARG for other values. */
 int m2rnn_debug_set_fault(int fault);
 

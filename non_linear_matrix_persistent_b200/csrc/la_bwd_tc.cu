@@ -18,8 +18,8 @@
 // It is summed as it stands (suffix sums over t in registers, sums over s
 // across lanes), never as a difference of running totals: those cancel, and
 // for a gate near 0 the division by f_u would amplify what is left.  Gates
-// below 2^-100 act as 2^-100 there, which keeps that quotient; in every other
-// gradient a path through such a gate is left out.
+// below 2^-100 act as 2^-100 there, which keeps that quotient; every other
+// gradient has the gate itself.
 //
 // Rounding: P', dP' and the copy of G that gives dv are bf16 operands; S and G
 // enter the products that df also reads, and a_t q_t enters G, as three bf16
@@ -81,8 +81,6 @@ struct BCfg {
     static constexpr bool kOwnDv = KP == 64;
     static constexpr int kP = 0, kDP = 128, kDQ = 256, kDK = kDQ + KP, kDV = kOwnDv ? kDK + KP : kDP,
                          kDG = KP == 128 ? (VP == 64 ? kDP + 64 : kDQ) : VP == 64 ? kDV + VP : kDP;
-    // the sum for G comes before the outputs' products
-    static constexpr bool kAqFirst = false;
     // the scores' columns are free for the next chunk once the products that read them are done
     static constexpr bool kEarly = KP == 64 && VP == 64;
     static constexpr int NS = KP * VP / 512;                    // state elements per thread
@@ -150,8 +148,11 @@ __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const La
                 for (int o = 0; o < 4; ++o) d[e + o] = at + o >= first ? d[e + o] : 0.f;
                 if constexpr (ZERO) {
                     const float4 zs = *reinterpret_cast<const float4*>(&tab->Z[t0 + at]);
-                    z[e] = zs.x != Zs ? 0.f : d[e]; z[e + 1] = zs.y != Zs ? 0.f : d[e + 1];
-                    z[e + 2] = zs.z != Zs ? 0.f : d[e + 2]; z[e + 3] = zs.w != Zs ? 0.f : d[e + 3];
+                    // (Z falls with t: before the source, where d is 0, the difference is positive)
+                    z[e] = d[e] * ex2_approx(fminf(zs.x - Zs, 0.f));
+                    z[e + 1] = d[e + 1] * ex2_approx(fminf(zs.y - Zs, 0.f));
+                    z[e + 2] = d[e + 2] * ex2_approx(fminf(zs.z - Zs, 0.f));
+                    z[e + 3] = d[e + 3] * ex2_approx(fminf(zs.w - Zs, 0.f));
                 }
             }
             tc_wait_ld();
@@ -208,13 +209,14 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const uint32_t b_full = bar(0), r_s = bar(2), b_in = bar(3), r_g = bar(4), b_g = bar(5), r_p = bar(6),
                    b_dv = bar(7), r_dv = bar(8), b_out = bar(9), r_aq = bar(10), b_dg = bar(11), r_out = bar(12),
-                   b_free = bar(13), b_tab = bar(14), r_df = bar(15), b_drain = bar(16), b_sc = bar(17);
+                   b_free = bar(13), b_tab = bar(14), b_drain = bar(15), b_sc = bar(16),
+                   r_df = bar(17);   // two, for chunks in turn: the copies may be a chunk behind df
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint64_t limit = p.wait_limit_ns;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 18; ++i) mbar_init(bar(i), 1);
+        for (int i = 0; i < 19; ++i) mbar_init(bar(i), 1);
         for (uint32_t b : {r_s, r_g, r_p, r_dv, r_aq, r_out}) mbar_init(b, NW);   // one arrival a warp
         if (!C::kRoomy) mbar_init(b_full, 2);   // dy comes later than the other tiles
         *abort_flag = 0;
@@ -317,7 +319,6 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 mma_commit(b_dg, one);
                 return true;
             };
-            if (C::kAqFirst && !(ok = sum_for_G())) break;
             if (!(ok = la_wait_warp(r_p, ph, abort_flag, limit))) break;
             tc_fence_after();
             if (!C::kOwnDv) {
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             for (int ks = 0; ks < 8; ++ks)
                 mma_ts(C::kDV, C::kP + ks * 16, d_mn + dy + ks * 128, id_vi, 1, one);
             mma_commit(b_out, one);
-            if (!C::kAqFirst && !(ok = sum_for_G())) break;
+            if (!(ok = sum_for_G())) break;
         }
         mma_commit(b_drain, one);   // nothing is in flight when the CTA ends
         if (lane == 0) la_drain(b_drain, 0, limit);
@@ -386,7 +387,8 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             for (; i < n; ++i) {
                 prefetch(i + 1);
                 if (!C::kRoomy) {
-                    if (!(ok = la_wait(r_aq, i & 1, abort_flag, limit) && la_wait(r_df, i & 1, abort_flag, limit))) break;
+                    if (!(ok = la_wait(r_aq, i & 1, abort_flag, limit) &&
+                          la_wait(r_df + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
                     if (i + 1 < n) load(i + 1, true, false);
                     if (!(ok = la_wait(b_dg, i & 1, abort_flag, limit))) break;
                     if (i + 1 < n) load(i + 1, false, true);
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 tma_store_commit();
                 tma_store_wait_read();
                 mbar_arrive(b_free);
-                if (!(ok = la_wait(r_df, ph, abort_flag, limit))) break;
+                if (!(ok = la_wait(r_df + ph * 8, (i >> 1) & 1, abort_flag, limit))) break;
                 if (i + C::kStages < n) load(i + C::kStages, true, true);
             }
             if (!ok) {   // leave no copy in flight
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
 #pragma unroll
             for (int w = 0; w < NW; ++w) gamma += sc->gamma[w];
             __syncwarp();
-            if (lane == 0) mbar_arrive(r_df);
+            if (lane == 0) mbar_arrive(r_df + ph * 8);
             // sums over sources before each token of this lane (exclusive)
             auto before = [&](const float (&v)[4], float (&o)[4]) {
                 float s[4] = {v[0], v[0] + v[1], v[0] + v[1] + v[2], v[0] + v[1] + v[2] + v[3]};
@@ -597,9 +599,9 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             if (!la_wait(b_tab, ph, abort_flag, limit)) break;
             const float Ft = tab->F[row], It = tab->I[row], Fe = tab->F[127], Ie = tab->I[127];
             const float Zt = tab->Z[row], Ze = tab->Z[127];
-            // decays for df, and for everything else (paths through gates at the floor left out)
+            // decays for df, and for everything else
             const float at0 = ex2_approx(Ft + It), bt0 = ex2_approx((Fe - Ft) + (Ie - It)), A0 = ex2_approx(Fe + Ie);
-            const float at = Zt != 0.f ? 0.f : at0, bt = Zt != Ze ? 0.f : bt0, A = Ze != 0.f ? 0.f : A0;
+            const float at = at0 * ex2_approx(Zt), bt = bt0 * ex2_approx(Ze - Zt), A = A0 * ex2_approx(Ze);
             gamma *= A0;
 #pragma unroll
             for (int d = 16; d; d >>= 1) gamma += __shfl_xor_sync(~0u, gamma, d);
@@ -665,7 +667,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             } else {
                 // the scratch and dP' may be written: df has been read, or V Gᵀ is done and dq has left
                 if (!C::kOwnScratch && !la_wait(b_in, ph, abort_flag, limit)) break;
-                if (C::kOwnScratch && i > 0 && !la_wait(r_df, ph ^ 1, abort_flag, limit)) break;
+                if (C::kOwnScratch && i > 0 && !la_wait(r_df + (ph ^ 1) * 8, ((i - 1) >> 1) & 1, abort_flag, limit)) break;
                 if (!C::kOwnScratch && i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
             }
             if (!la_wait(b_sc, ph, abort_flag, limit)) break;
@@ -712,10 +714,6 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                     run = score_block<false, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place);
             }
             sc->total[wg][row] = run;
-            if (C::kAqFirst) {   // over the states' terms: the sum for G runs while the rows are scaled
-                if (!la_wait(b_in, ph, abort_flag, limit)) break;
-                put_aq();
-            }
             if (C::kRoomy && !scale_all()) break;
             tc_wait_st();
             arrive(r_p);
@@ -727,7 +725,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 tc_wait_st();
                 arrive(r_dv);
             }
-            if (C::kRoomy && !C::kAqFirst) put_aq();   // over the states' terms, whose products are done
+            if (C::kRoomy) put_aq();   // over the states' terms, whose products are done
             if (!la_wait(b_out, ph, abort_flag, limit)) break;
             tc_fence_after();
             const int t = c * kLaChunk + row;
@@ -851,9 +849,6 @@ LaPlan la_bwd_plan(int B, int H, int T, int, int) {
     const long long pairs = (long long)B * H;
     long long segs = 1;
     if (pairs * 2 <= kNumSMs && chunks >= 4) segs = kNumSMs / pairs;
-#ifdef LA_TUNE
-    if (const char* e = getenv("LA_BSEGS")) segs = atoi(e);
-#endif
     if (segs > chunks) segs = chunks;
     if (segs < 1) segs = 1;
     const int per = (int)((chunks + segs - 1) / segs);

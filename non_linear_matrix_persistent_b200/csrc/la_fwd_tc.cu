@@ -25,7 +25,6 @@
 // most 1; in the diagonal block the first is the reciprocal of a decay, within
 // fp32's range unless the block decays by more than 2^-90: such chunks take one
 // exponential per score there.
-#include <cstdlib>
 #include <mutex>
 
 #include "kernels.h"
@@ -539,7 +538,7 @@ struct SumCfg {
     static constexpr int kOffX = 2 * kStage;
     static constexpr int kOffTab = kOffX + kSets * 3 * kTerm;
     static constexpr int kOffBar = kOffTab + 2 * (int)sizeof(LaTables);
-    static constexpr int kBars = 10;
+    static constexpr int kBars = 11;
     static constexpr int kSmem = kOffBar + kBars * 8 + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -560,13 +559,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     LaTables* tab = reinterpret_cast<LaTables*>(smem + C::kOffTab);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
-    const uint32_t b_full = bar(0), b_tab = bar(2), t_free = bar(4), b_ds = bar(6), r_k = bar(8), b_drain = bar(9);
+    const uint32_t b_full = bar(0), b_tab = bar(2), t_free = bar(4), b_ds = bar(6), r_k = bar(8), b_drain = bar(10);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint64_t limit = p.wait_limit_ns;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 10; ++i) mbar_init(bar(i), 1);
-        for (uint32_t b : {t_free, t_free + 8, r_k}) mbar_init(b, kNW);
+        for (int i = 0; i < 11; ++i) mbar_init(bar(i), 1);
+        for (uint32_t b : {t_free, t_free + 8, r_k, r_k + 8}) mbar_init(b, kNW);
         *abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -585,7 +584,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint32_t one = lane == 0;
         for (int i = 0; i < n; ++i) {
             if (!la_wait_warp(b_full + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) break;
-            if (!la_wait_warp(r_k, i & 1, abort_flag, limit)) break;
+            if (!la_wait_warp(r_k + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) break;
             tc_fence_after();
             const uint32_t k = (i & 1) * (C::kStage >> 4), v = k + (C::kQ >> 4),
                            x = (C::kOffX + (i % C::kSets) * 3 * C::kTerm) >> 4, xs = C::kTerm >> 4;
@@ -648,7 +647,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const uint32_t pos = (ch >> 3) * kTileBytes + sw128(row, ch & 7);
                 put_scaled(src + pos, dst + pos, dst + pos + C::kTerm, dst + pos + 2 * C::kTerm, w);
             }
-            warp_arrive(r_k);
+            warp_arrive(r_k + (i & 1) * 8);
         }
         if (ok && la_wait(b_ds + ((n - 1) & 1) * 8, ((n - 1) >> 1) & 1, abort_flag, limit)) {
             tc_fence_after();
@@ -731,9 +730,6 @@ LaPlan la_fwd_plan(int B, int H, int T, int K, int V) {
     const long long pairs = (long long)B * H, slots = (long long)kNumSMs * per_sm;
     long long segs = 1;
     if (pairs * 2 <= kNumSMs && chunks >= 4) segs = slots / pairs;
-#ifdef LA_TUNE
-    if (const char* e = getenv("LA_SEGS")) segs = atoi(e);
-#endif
     if (segs > chunks) segs = chunks;
     if (segs < 1) segs = 1;
     const int per = (int)((chunks + segs - 1) / segs);

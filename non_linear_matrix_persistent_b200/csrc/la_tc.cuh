@@ -26,15 +26,18 @@ static __device__ unsigned g_la_status;
 // Floor of a gate's base-2 logarithm.  Forward: 2^-256, which every product of
 // decays flushes to 0, so a gate of 0 (or below 2^-126) discards the state.
 // Backward: 2^-100, so that the sums over paths through a gate of 0, divided
-// by the gate again, still give its gradient; the other gradients leave such
-// paths out (LaTables::Z).
+// by the gate again, still give its gradient; in the other gradients the rest
+// of such a gate's exponent is made up for (LaTablesZ::Z).
 constexpr float kLogFloorFwd = -256.f, kLogFloorBwd = -100.f, kGateFloorBwd = 7.888609052210118e-31f;
 
 // log2 of a gate split into an integer and a fraction in [-1/2, 1/2]: sums of
 // the integers are exact, so differences of cumulative sums keep their
 // precision behind a gate close to 0.  A NaN stays a NaN.
-__device__ __forceinline__ void la_log2(const LaParams& p, float x, float floor_, float& whole, float& frac) {
+// `rest`: what the floor took away (a gate of 0 has a logarithm of -300 here).
+__device__ __forceinline__ void la_log2(const LaParams& p, float x, float floor_, float& whole, float& frac,
+                                        float& rest) {
     float l = p.f_is_logit ? -1.4426950408889634f * log1pf(expf(-x)) : log2f(x);
+    rest = l < floor_ ? fmaxf(l, -300.f) - floor_ : 0.f;
     l = l < floor_ ? floor_ : l;
     whole = rintf(l);
     frac = l - whole;
@@ -59,30 +62,44 @@ __device__ __forceinline__ float4 la_whole(const LaTables* tab, int t) {   // I[
     return make_float4(w.x, w.y, w.z, w.w);
 }
 struct LaTablesZ : LaTables {
-    float Z[128];   // gates at the floor, from the chunk's start through the token
+    float Z[128];   // exponents beneath the floor, from the chunk's start through the token: 0 or negative
 };
+// The fraction back into [-1/2, 1/2]: a cumulative sum keeps the precision of
+// its small part, which the decays between neighbours are made of.
+__device__ __forceinline__ void la_carry(float& frac, float& whole) {
+    const float r = rintf(frac);
+    frac -= r;
+    whole += r;
+}
 template <bool FROM_PREV = false, class Tab = LaTables>
 __device__ __forceinline__ void la_tables(Tab* tab, const LaParams& p, const float (&x)[4], int valid, float floor_) {
     const int lane = threadIdx.x & 31;
     float F[4], I[4], Z[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        la_log2(p, x[i], floor_, I[i], F[i]);
-        if (lane * 4 + i >= valid) { F[i] = 0.f; I[i] = 0.f; }   // behind the last token: a gate of 1
-        Z[i] = (I[i] + F[i] <= floor_ ? 1.f : 0.f) + (i > 0 ? Z[i > 0 ? i - 1 : 0] : 0.f);
-        if (i > 0) { F[i] += F[i - 1]; I[i] += I[i - 1]; }
+        float rest;
+        la_log2(p, x[i], floor_, I[i], F[i], rest);
+        if (lane * 4 + i >= valid) { F[i] = 0.f; I[i] = 0.f; rest = 0.f; }   // behind the last token: a gate of 1
+        Z[i] = rest + (i > 0 ? Z[i > 0 ? i - 1 : 0] : 0.f);
+        if (i > 0) {
+            F[i] += F[i - 1];
+            I[i] += I[i - 1];
+            la_carry(F[i], I[i]);
+        }
     }
     float f = F[3], w = I[3];
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
         const float a = __shfl_up_sync(~0u, f, d), b = __shfl_up_sync(~0u, w, d);
         if (lane >= d) { f += a; w += b; }
+        la_carry(f, w);
     }
     const float f0 = __shfl_up_sync(~0u, f, 1), w0 = __shfl_up_sync(~0u, w, 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         F[i] += lane ? f0 : 0.f;
         I[i] += lane ? w0 : 0.f;
+        la_carry(F[i], I[i]);
     }
     if constexpr (FROM_PREV) {
         float z = Z[3];

@@ -22,8 +22,6 @@
 
 #include <cuda_bf16.h>
 
-#include <cstdlib>
-
 namespace m2rnn {
 namespace {
 
@@ -487,12 +485,6 @@ unsigned capped(size_t want, int per_sm) {
     return (unsigned)(want < cap ? want : cap);
 }
 
-#ifdef LA_TUNE
-int norm_tune(const char* n, int d) { const char* e = getenv(n); return e ? atoi(e) : d; }
-#else
-constexpr int norm_tune(const char*, int d) { return d; }
-#endif
-
 template <class X, class Y>
 struct Fwd {
     const NormParams& p;
@@ -501,7 +493,7 @@ struct Fwd {
     void operator()() {
         constexpr int U = unroll_fwd(VEC * CH), kRows = kThreads / LPR * U;
         const size_t items = (size_t)p.B * p.H * ((p.T + kRows - 1) / kRows);
-        m2rnn_norm_fwd_kernel<X, Y, VEC, LPR, CH, U><<<capped(items, norm_tune("LN_F", 2)), kThreads, 0, s>>>(p);
+        m2rnn_norm_fwd_kernel<X, Y, VEC, LPR, CH, U><<<capped(items, 2), kThreads, 0, s>>>(p);
     }
 };
 template <class X, class Y, class DX>
@@ -548,12 +540,12 @@ int chunks_for(int B, int H, int T, int N, int ctas, int least) {
 
 cudaError_t launch_norm_fwd(const NormParams& q, cudaStream_t s) {
     NormParams p = q;
-    p.chunks = chunks_for(p.B, p.H, p.T, p.N, 8 * kNumSMs, 1)   /* rows too long for registers */;
+    p.chunks = chunks_for(p.B, p.H, p.T, p.N, 8 * kNumSMs, 1);   // rows too long for registers
     if (p.x_fp32) return p.y_fp32 ? fwd<float, float>(p, s) : fwd<float, __nv_bfloat16>(p, s);
     return p.y_fp32 ? fwd<__nv_bfloat16, float>(p, s) : fwd<__nv_bfloat16, __nv_bfloat16>(p, s);
 }
 
-int norm_bwd_chunks(int B, int H, int T, int N) { return chunks_for(B, H, T, N, norm_tune("LN_B", 2) * kNumSMs, 4); }
+int norm_bwd_chunks(int B, int H, int T, int N) { return chunks_for(B, H, T, N, 2 * kNumSMs, 4); }
 
 cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s) {
     cudaError_t e = p.y_fp32 ? bwd_x<float>(p, s) : bwd_x<__nv_bfloat16>(p, s);

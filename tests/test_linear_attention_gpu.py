@@ -104,6 +104,84 @@ def test_gates(K, V, gate, T):
     check(*inputs(2, 2, T, K, V, gate=gate, seed=5))
 
 
+@pytest.mark.parametrize("f", [1.0, 0.9, 0.2, 0.15, 0.14, 1e-3, 1e-20, 1e-33, 0.0])
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128)])
+def test_constant_gates(f, K, V):
+    """Decays over a block of 32 tokens on both sides of 2^-90, where the diagonal blocks change their form, and
+    gates beneath every floor."""
+    x, _ = inputs(1, 2, 200, K, V, gate="head", seed=6)
+    x["f"] = torch.full_like(x["f"], f)
+    check(x, False)
+
+
+@pytest.mark.parametrize("K,V", [(64, 128), (128, 64), (128, 128), (32, 64), (64, 64)])
+@pytest.mark.parametrize("G", [1, 4])
+def test_many_chunks(K, V, G):
+    """Several chunks for every schedule, with shared k and q and odd ends, one CTA a pair."""
+    check(*inputs(30, 4, 523, K, V, G=G, gate="logit", seed=8))
+
+
+@pytest.mark.parametrize("K,V", [(64, 128), (128, 64), (128, 128), (64, 64)])
+@pytest.mark.parametrize("gate", ["edges", "head"])
+def test_segments(K, V, gate):
+    """Two pairs over 12 chunks: split along T forward and backward, an odd number of chunks a segment."""
+    check(*inputs(1, 2, 1500, K, V, G=1, gate=gate, seed=10))
+
+
+@pytest.mark.parametrize("K,V", [(64, 128), (128, 128), (64, 64)])
+def test_buffers_on_16_bytes(K, V):
+    """Inputs and outputs that start on 16 bytes and not on 32."""
+    a = api()
+    x, _ = inputs(1, 2, 140, K, V, seed=12)
+
+    def off(t):
+        n = 8 if t.dtype == torch.bfloat16 else 4
+        pad = torch.full((t.numel() + 2 * n,), 3.0, dtype=t.dtype, device=DEV)
+        v = pad[n:n + t.numel()].view(t.shape)
+        v.copy_(t)
+        assert v.data_ptr() % 32 == 16
+        return v
+
+    args = [off(x[n]) for n in ("k", "v", "q", "f")]
+    out = {"y": off(torch.zeros_like(x["v"])), "ST": off(torch.zeros_like(x["S0"]))}
+    y, ST, ck = a.linear_attention(*args, off(x["S0"]), want_ckpt=True, out=out)
+    y2, ST2, ck2 = a.linear_attention(x["k"], x["v"], x["q"], x["f"], x["S0"], want_ckpt=True)
+    assert torch.equal(y, y2) and torch.equal(ST, ST2) and torch.equal(ck, ck2)
+    out = {"dk": off(torch.zeros_like(x["k"])), "dv": off(torch.zeros_like(x["v"])), "dq": off(torch.zeros_like(x["q"])),
+           "df": off(torch.zeros_like(x["f"])), "dS0": off(torch.zeros_like(x["S0"]))}
+    g = a.linear_attention_backward(*args, off(ck), off(x["dy"]), off(x["dST"]), out=out)
+    g2 = a.linear_attention_backward(x["k"], x["v"], x["q"], x["f"], ck2, x["dy"], x["dST"])
+    assert all(torch.equal(g[n], g2[n]) for n in g2)
+
+
+def test_a_nan_reaches_what_it_should():
+    """A NaN in one pair's v: its later readouts and the states are NaN, other pairs and earlier tokens are not."""
+    a = api()
+    x, _ = inputs(1, 2, 300, 64, 64, start=False, seed=14)
+    x["v"][0, 0, 140, 3] = float("nan")
+    y, ST, ck = a.linear_attention(x["k"], x["v"], x["q"], x["f"], want_ckpt=True)
+    assert bool(torch.isfinite(y[0, 1]).all()) and bool(torch.isfinite(ST[0, 1]).all())
+    assert bool(torch.isfinite(y[0, 0, :128]).all()) and bool(torch.isnan(y[0, 0, 140:, 3]).all())
+    assert bool(torch.isnan(ST[0, 0, :, 3]).all())
+    g = a.linear_attention_backward(x["k"], x["v"], x["q"], x["f"], ck, x["dy"])
+    assert all(bool(torch.isfinite(g[n][0, 1]).all()) for n in g)
+
+
+def test_strided_inputs_are_refused():
+    a = api()
+    x, _ = inputs(1, 2, 40, 64, 64, seed=16)
+    with pytest.raises(ValueError, match="contiguous"):
+        a.linear_attention(x["k"].transpose(2, 3).contiguous().transpose(2, 3), x["v"], x["q"], x["f"])
+    with pytest.raises(ValueError, match="shape"):
+        a.linear_attention(x["k"], x["v"], x["q"], x["f"][:, :, :39].contiguous())
+    with pytest.raises(TypeError):
+        a.linear_attention(x["k"], x["v"], x["q"], x["f"].double())
+    with pytest.raises(ValueError, match="ckpt"):
+        a.linear_attention_backward(x["k"], x["v"], x["q"], x["f"], torch.zeros(1, 2, 1, 64, 64, device=DEV), x["dy"])
+    with pytest.raises(RuntimeError, match="UNSUPPORTED"):
+        a.linear_attention(x["k"][..., :48].contiguous(), x["v"], x["q"][..., :48].contiguous(), x["f"])
+
+
 @pytest.mark.parametrize("H,G", [(4, 2), (6, 1), (8, 8)])
 @pytest.mark.parametrize("T", [1, 37, 260])
 @pytest.mark.parametrize("K,V", [(64, 64), (128, 64)])
