@@ -114,8 +114,8 @@ __device__ __forceinline__ float column_sums(float (&r)[N]) {
 // the source's sum of paths into the block, and leaves in cut[] by gate u the
 // sums over the warp's sources before u of the paths to sinks u.. of the block.
 // The decay is r·c[t].  `first`: the lane in the source's own block (sinks t >=
-// s), else -1.  ZERO: the chunk has gates at the floor, paths through which
-// count for df alone, or blocks too steep for the product: the diagonal takes
+// s), else -1.  ZERO: the chunk has gates beneath the floor, paths through which
+// are smaller in everything but df, or blocks too steep for the product: the diagonal takes
 // an exponential each.  (One body for diagonal and other blocks: the two would
 // not fit the instruction cache together.)
 // PW: columns at a time, 16 or, where registers are short, 8.
@@ -245,15 +245,16 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
         const uint32_t one = lane == 0;
         constexpr uint32_t X = C::kOffX >> 4, OP = C::kOp >> 4, XP = C::kOffP >> 4;
         auto kmajor = [](int ks, int rows) { return (uint32_t)((ks >> 2) * (rows * 128 >> 4) + (ks & 3) * 2); };
-        // rows (128 tokens) times a state in three terms, the first two at x
+        // rows (128 tokens) times a state in three terms, the first two at x; the
+        // smallest first: an accumulation rounds at the size that the sum has by then
         auto times_state = [&](uint32_t d, uint32_t rows, uint32_t x) {
 #pragma unroll
-            for (int e = 0; e < 3; ++e) {
+            for (int e = 2; e >= 0; --e) {
                 const uint32_t op = e < 2 || C::kRoomy ? x + e * OP : XP;
 #pragma unroll
                 for (int ks = 0; ks < VP / 16; ++ks)
                     mma_ss(d, d_tile + rows + kmajor(ks, 128), d_op + op + kmajor(ks, KP), id_ki,
-                                  e > 0 || ks > 0, one);
+                                  e < 2 || ks > 0, one);
             }
         };
         auto tiles = [&](int i, uint32_t& q, uint32_t& k, uint32_t& v, uint32_t& dy) {
@@ -309,12 +310,12 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 if (!la_wait_warp(r_aq, ph, abort_flag, limit)) return false;
                 tc_fence_after();
 #pragma unroll
-                for (int x = 0; x < 3; ++x) {       // the terms of a q
+                for (int x = 2; x >= 0; --x) {      // the terms of a q
                     const uint32_t op = x < 2 || C::kRoomy ? X + x * (C::kQ >> 4) : XP;
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         mma_ss(C::kDG, d_mn + op + ks * 128, d_mn + dy + ks * 128, id_dg,
-                                      x > 0 || ks > 0, one);
+                                      x < 2 || ks > 0, one);
                 }
                 mma_commit(b_dg, one);
                 return true;
@@ -843,17 +844,6 @@ cudaError_t launch(const LaParams& p, const BwdMaps& m, cudaStream_t s) {
 }
 
 }  // namespace
-
-LaPlan la_bwd_plan(int B, int H, int T, int, int) {
-    const int chunks = (T + kLaChunk - 1) / kLaChunk;
-    const long long pairs = (long long)B * H;
-    long long segs = 1;
-    if (pairs * 2 <= kNumSMs && chunks >= 4) segs = kNumSMs / pairs;
-    if (segs > chunks) segs = chunks;
-    if (segs < 1) segs = 1;
-    const int per = (int)((chunks + segs - 1) / segs);
-    return {(chunks + per - 1) / per, per};
-}
 
 cudaError_t launch_la_bwd_tc(const LaParams& q, cudaStream_t s) {
     LaParams p = q;

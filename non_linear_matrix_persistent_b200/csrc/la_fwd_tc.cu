@@ -85,19 +85,20 @@ __device__ __forceinline__ void warp_arrive(uint32_t b) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(b);
 }
 
-// Σ_s k_s ⊗ v_s over a chunk with one side in three scaled terms: accumulates
-// into D[KP][VP].  a, b: the sides' first tiles (units of 16 bytes from the
+// Σ_s k_s ⊗ v_s over a chunk with one side in three scaled terms, into
+// D[KP][VP].  a, b: the sides' first tiles (units of 16 bytes from the
 // descriptor's start); astep, bstep: from one term to the next, 0 for the side
-// that is not scaled.
+// that is not scaled.  The smallest terms come first: an accumulation rounds at
+// the size that the sum has by then.
 template <int KP, int VP>
 __device__ __forceinline__ void outer_sum(uint32_t d, Desc mn, uint32_t a, uint32_t astep, uint32_t b, uint32_t bstep,
-                                          bool first, uint32_t one) {
+                                          uint32_t one) {
     constexpr uint32_t id = idesc_bf16_f32(KP, VP, 1, 1);
 #pragma unroll
-    for (int x = 0; x < 3; ++x)
+    for (int x = 2; x >= 0; --x)
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-            mma_ss(d, mn + a + x * astep + ks * 128, mn + b + x * bstep + ks * 128, id, !(first && x == 0 && ks == 0), one);
+            mma_ss(d, mn + a + x * astep + ks * 128, mn + b + x * bstep + ks * 128, id, x < 2 || ks > 0, one);
 }
 
 // The thread's part of a [KP][VP] accumulator or state: row kap, NS columns
@@ -287,16 +288,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (C::kInPlace) {
                     constexpr uint32_t id = idesc_bf16_f32(KP, VP, 1, 1);
 #pragma unroll
-                    for (int x = 0; x < 3; ++x) {
+                    for (int x = 2; x >= 0; --x) {   // the smallest terms first
                         const uint32_t a = x == 0 ? k : x == 1 ? q : C::kOffS >> 4;
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            mma_ss(C::kDS, d_mn + a + ks * 128, d_mn + v + ks * 128, id, x > 0 || ks > 0, one);
+                            mma_ss(C::kDS, d_mn + a + ks * 128, d_mn + v + ks * 128, id, x < 2 || ks > 0, one);
                     }
                 } else if (C::kScaleV) {
-                    outer_sum<KP, VP>(C::kDS, d_mn, k, 0, X, XS, true, one);
+                    outer_sum<KP, VP>(C::kDS, d_mn, k, 0, X, XS, one);
                 } else {
-                    outer_sum<KP, VP>(C::kDS, d_mn, X, XS, v, 0, true, one);
+                    outer_sum<KP, VP>(C::kDS, d_mn, X, XS, v, 0, one);
                 }
                 mma_commit(b_ds, one);
                 if (!next_scores(true)) break;
@@ -526,9 +527,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // What a segment's tokens add to the state at its end, from a zero start
 // (REV: to the state's gradient at its start): Σ w_s k_s v_sᵀ (Σ w_t q_t dy_tᵀ)
 // with w the decay to the segment's end (from its start through t).  The walk
-// starts at that end, so w is a running product times the chunk's decay and
-// the whole segment is one sum in tensor memory: a chunk's terms are written
-// while the last one's products run.
+// starts at that end, so w is a running product times the chunk's decay and no
+// chunk's sum is scaled again: a chunk's terms are written while the last
+// one's products run.  The chunks' sums are added in registers, which round to
+// nearest: one accumulation in tensor memory over the segment lost up to 1e-6
+// of the state where gates are close to 1.
 template <int KP, int VP>
 struct SumCfg {
     static constexpr int kQ = KP / 64 * kTileBytes, kV = VP / 64 * kTileBytes, kStage = kQ + kV;
@@ -588,8 +591,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tc_fence_after();
             const uint32_t k = (i & 1) * (C::kStage >> 4), v = k + (C::kQ >> 4),
                            x = (C::kOffX + (i % C::kSets) * 3 * C::kTerm) >> 4, xs = C::kTerm >> 4;
-            if (C::kScaleV) outer_sum<KP, VP>(0, d_mn, k, 0, x, xs, i == 0, one);
-            else outer_sum<KP, VP>(0, d_mn, x, xs, v, 0, i == 0, one);
+            if (C::kScaleV) outer_sum<KP, VP>((i & 1) * VP, d_mn, k, 0, x, xs, one);
+            else outer_sum<KP, VP>((i & 1) * VP, d_mn, x, xs, v, 0, one);
             mma_commit(b_ds + (i & 1) * 8, one);
         }
         mma_commit(b_drain, one);
@@ -625,7 +628,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         decay_warp(p, bh, n, chunk_of, tab, b_tab, t_free, abort_flag);
     } else {
         const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-        float carry = 1.f;
+        const Part<KP, VP> part;
+        float carry = 1.f, S[Pt::NS];
+#pragma unroll
+        for (int e = 0; e < Pt::NS; ++e) S[e] = 0.f;
+        auto add = [&](int j) -> bool {   // chunk j's sum
+            if (!la_wait(b_ds + (j & 1) * 8, (j >> 1) & 1, abort_flag, limit)) return false;
+            tc_fence_after();
+            part.add(((uint32_t)(quarter * 32) << 16) + (j & 1) * VP, 1.f, S);
+            return true;
+        };
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             if (!(ok = la_wait(b_tab + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
@@ -636,8 +648,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(t_free + (i & 1) * 8);
             if (!(ok = la_wait(b_full + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
-            const int j = i - C::kSets;   // whose terms these replace
-            if (j >= 0 && !(ok = la_wait(b_ds + (j & 1) * 8, (j >> 1) & 1, abort_flag, limit))) break;
+            if (i >= C::kSets && !(ok = add(i - C::kSets))) break;   // whose terms these replace
             const uint8_t* src = smem + (i & 1) * C::kStage + (C::kScaleV ? C::kQ : 0);
             uint8_t* dst = smem + C::kOffX + (i % C::kSets) * 3 * C::kTerm;
             constexpr int kCh = C::kTerm / 128 / 16 / 4;
@@ -649,13 +660,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
             warp_arrive(r_k + (i & 1) * 8);
         }
-        if (ok && la_wait(b_ds + ((n - 1) & 1) * 8, ((n - 1) >> 1) & 1, abort_flag, limit)) {
-            tc_fence_after();
-            const Pt part;
-            float S[Pt::NS];
-#pragma unroll
-            for (int e = 0; e < Pt::NS; ++e) S[e] = 0.f;
-            part.add(tmem + ((uint32_t)(quarter * 32) << 16), 1.f, S);
+        for (int j = max(0, n - C::kSets); ok && j < n; ++j) ok = add(j);
+        if (ok) {
             part.store(p.seg_state + ((size_t)bh * p.segs + seg) * p.K * p.V, p.K, p.V, S);
             if (threadIdx.x == 0) seg_decay[(size_t)bh * p.segs + seg] = carry;
         }
@@ -725,14 +731,25 @@ float* decays_of(const LaParams& p) {   // behind the segment states in the work
 
 }  // namespace
 
-LaPlan la_fwd_plan(int B, int H, int T, int K, int V) {
-    const int chunks = (T + kLaChunk - 1) / kLaChunk, per_sm = 1;
-    const long long pairs = (long long)B * H, slots = (long long)kNumSMs * per_sm;
-    long long segs = 1;
-    if (pairs * 2 <= kNumSMs && chunks >= 4) segs = slots / pairs;
-    if (segs > chunks) segs = chunks;
-    if (segs < 1) segs = 1;
-    const int per = (int)((chunks + segs - 1) / segs);
+// Segments while there are SMs for them, if the chunks that a walk is spared
+// pay for the sums that run before it, a launch and a pass over k and v (q and
+// dy).  Those cost more the more CTAs share the memory.  Measured, us, one
+// walk against segments of T/128 chunks:
+//   forward   1 pair, 64 x 64:    4 chunks 14.8 / 15.7,   6  19.8 / 16.6
+//            24 pairs, 64 x 64:   6 chunks 19.8 / 20.1,   8  24.4 / 21.6
+//            48 pairs, 128 x 128: 16 chunks 75.5 / 87.4, 32  142 / 117
+//            74 pairs, 128 x 128: 32 chunks 143 / 149,   64  277 / 246
+//   backward  1 pair, 64 x 64:    2 chunks 17.5 / 19.5,   3  24.2 / 19.8
+//            48 pairs, 64 x 64:   4 chunks 30.8 / 31.0,   6  43.6 / 35.1
+//            74 pairs, 64 x 64:   6 chunks 47.1 / 45.7,   8  61.2 / 55.4
+//            74 pairs, 128 x 128: 6 chunks 93.8 / 104,   12  175 / 157
+LaPlan la_plan(int B, int H, int T, bool backward) {
+    const int chunks = (T + kLaChunk - 1) / kLaChunk;
+    const long long pairs = (long long)B * H;
+    if (pairs * 2 > kNumSMs) return {1, chunks};
+    const int most = kNumSMs / (int)pairs, want = most < chunks ? most : chunks, per = (chunks + want - 1) / want;
+    const int need = !backward ? 4 + (int)(pairs * pairs) / 256 : pairs < 48 ? 2 : 1 + (int)pairs / 24;
+    if (chunks - per < need) return {1, chunks};
     return {(chunks + per - 1) / per, per};
 }
 

@@ -50,12 +50,11 @@ size_t df_bytes(const m2rnn_la_dims* d) { return d->f_per_head ? round256(sizeof
 // pairs of 128 x 128: 11.1 against 13.8 and 14.4 against 13.7.
 bool fwd_on_tensor_cores(const m2rnn_la_dims* d) { return d->mode == M2RNN_MODE_BF16_TC && d->T > 11; }
 
-m2rnn::LaPlan fwd_plan(const m2rnn_la_dims* d) { return m2rnn::la_fwd_plan(d->B, d->H, d->T, d->K, d->V); }
-
 bool bwd_on_tensor_cores(const m2rnn_la_dims* d) { return d->mode == M2RNN_MODE_BF16_TC; }
-m2rnn::LaPlan bwd_plan(const m2rnn_la_dims* d) { return m2rnn::la_bwd_plan(d->B, d->H, d->T, d->K, d->V); }
-size_t bwd_seg_bytes(const m2rnn_la_dims* d) {
-    return bwd_on_tensor_cores(d) ? m2rnn::la_seg_bytes(bwd_plan(d), d->B, d->H, d->K, d->V) : 0;
+m2rnn::LaPlan plan_of(const m2rnn_la_dims* d, bool backward) { return m2rnn::la_plan(d->B, d->H, d->T, backward); }
+size_t seg_bytes(const m2rnn_la_dims* d, bool backward) {
+    if (!(backward ? bwd_on_tensor_cores(d) : fwd_on_tensor_cores(d))) return 0;
+    return m2rnn::la_seg_bytes(plan_of(d, backward), d->B, d->H, d->K, d->V);
 }
 
 m2rnn::LaParams params(const m2rnn_la_dims* d) {
@@ -89,8 +88,8 @@ extern "C" {
 size_t m2rnn_linear_attention_workspace(const m2rnn_la_dims* d, int backward) {
     if (check(d) != M2RNN_OK) return kRefused;
     if (pairs(d) * d->T == 0) return 0;
-    if (!backward) return fwd_on_tensor_cores(d) ? m2rnn::la_seg_bytes(fwd_plan(d), d->B, d->H, d->K, d->V) : 0;
-    return group_bytes(d) + df_bytes(d) + bwd_seg_bytes(d);
+    if (!backward) return seg_bytes(d, false);
+    return group_bytes(d) + df_bytes(d) + seg_bytes(d, true);
 }
 
 m2rnn_status m2rnn_linear_attention_forward(const m2rnn_la_dims* d, const void* k, const void* v, const void* q,
@@ -107,7 +106,7 @@ m2rnn_status m2rnn_linear_attention_forward(const m2rnn_la_dims* d, const void* 
     m2rnn::LaParams p = params(d);
     p.k = k; p.v = v; p.q = q; p.f = f; p.S0 = S0; p.y = y; p.ST = ST; p.ckpt = ckpt;
     if (!fwd_on_tensor_cores(d)) return status_of(m2rnn::launch_la_rec(p, s));
-    const m2rnn::LaPlan plan = fwd_plan(d);
+    const m2rnn::LaPlan plan = plan_of(d, false);
     p.segs = plan.segs; p.seg_chunks = plan.seg_chunks;
     p.seg_state = static_cast<float*>(workspace);
     return status_of(m2rnn::launch_la_fwd_tc(p, s));
@@ -145,7 +144,7 @@ m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void*
     if (d->f_per_head) p.df = reinterpret_cast<float*>(ws + group_bytes(d));
     cudaError_t e;
     if (bwd_on_tensor_cores(d)) {
-        const m2rnn::LaPlan plan = bwd_plan(d);
+        const m2rnn::LaPlan plan = plan_of(d, true);
         p.segs = plan.segs; p.seg_chunks = plan.seg_chunks;
         p.seg_state = reinterpret_cast<float*>(ws + group_bytes(d) + df_bytes(d));
         e = m2rnn::launch_la_bwd_tc(p, s);

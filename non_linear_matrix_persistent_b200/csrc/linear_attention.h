@@ -78,13 +78,12 @@ __device__ __forceinline__ __nv_bfloat16 la_from_f32<__nv_bfloat16>(float x) { r
 cudaError_t launch_la_rec(const LaParams& p, cudaStream_t s);
 // Chunked tensor-core forward (bf16): y, ST and the checkpoints.
 cudaError_t launch_la_fwd_tc(const LaParams& p, cudaStream_t s);
-LaPlan la_fwd_plan(int B, int H, int T, int K, int V);
+LaPlan la_plan(int B, int H, int T, bool backward);
 // Workspace of a plan: segment states and decays.
 size_t la_seg_bytes(const LaPlan& plan, int B, int H, int K, int V);
 cudaError_t la_fwd_tc_status(unsigned* word, cudaStream_t s);
 // Chunked tensor-core backward (bf16).
 cudaError_t launch_la_bwd_tc(const LaParams& p, cudaStream_t s);
-LaPlan la_bwd_plan(int B, int H, int T, int K, int V);
 // dL/dS at the segments' ends, into p.seg_state.
 cudaError_t launch_la_seg_grads(const LaParams& p, cudaStream_t s);
 cudaError_t la_bwd_tc_status(unsigned* word, cudaStream_t s);

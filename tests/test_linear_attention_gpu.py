@@ -124,8 +124,14 @@ def test_many_chunks(K, V, G):
 @pytest.mark.parametrize("K,V", [(64, 128), (128, 64), (128, 128), (64, 64)])
 @pytest.mark.parametrize("gate", ["edges", "head"])
 def test_segments(K, V, gate):
-    """Two pairs over 12 chunks: split along T forward and backward, an odd number of chunks a segment."""
+    """Two pairs over 12 chunks: a segment each, forward and backward."""
     check(*inputs(1, 2, 1500, K, V, G=1, gate=gate, seed=10))
+
+
+@pytest.mark.parametrize("K,V", [(64, 128), (128, 64), (128, 128), (64, 64)])
+def test_segments_of_several_chunks(K, V):
+    """37 pairs over 17 chunks with gates close to 1: segments of 5, the last of 2."""
+    check(*inputs(1, 37, 2100, K, V, gate="slow", seed=11))
 
 
 @pytest.mark.parametrize("K,V", [(64, 128), (128, 128), (64, 64)])
