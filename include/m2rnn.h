@@ -223,7 +223,7 @@ m2rnn_status m2rnn_backward_noalloc(const m2rnn_dims* d,
  * workspace needs no initialisation.  A wait inside a kernel that runs out is
  * reported by m2rnn_linear_attention_status. */
 typedef struct {
-    int B, H, T, K, V;  /* K, V in {16, 32, 64, 128} */
+    int B, H, T, K, V;  /* K, V in {16, 32, 64, 128}; B·H up to 2^24, T up to 2^30 */
     int mode;           /* M2RNN_MODE_BF16_TC or M2RNN_MODE_FP32_DEBUG */
     int qk_heads;       /* as in m2rnn_dims */
     int f_is_logit;     /* as in m2rnn_dims */
@@ -259,8 +259,8 @@ m2rnn_status m2rnn_linear_attention_status(m2rnn_stream_t stream);
  * (rms: m = 0).  x is [B][H][T][N], head-first like the readouts above; y is
  * token-first, [B][T][H][N]; weight w and bias b are [H][N] fp32.  Plain rows
  * with one weight are B = H = 1.  mean and rstd are fp32 [B][H][T].  Sums and
- * statistics are fp32 whatever the types.  Any N >= 1; pointers are 16-byte
- * aligned. */
+ * statistics are fp32 whatever the types.  Any N >= 1 up to 2^28, B·H up to
+ * 2^24, T up to 2^30 and B·H·T up to 2^35; pointers are 16-byte aligned. */
 typedef struct {
     int B, H, T, N;
     int x_fp32;         /* element type of x: 0 = bf16, 1 = fp32 */

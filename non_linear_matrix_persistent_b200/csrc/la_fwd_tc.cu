@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // Segment sums -> segment start states, in place: start_0 = init,
 // start_{i+1} = decay_i start_i + sum_i (reverse: from the last segment, for
 // the gradient at segment ends).  A thread takes four adjacent elements.
-__global__ void m2rnn_la_seg_scan_kernel(const LaParams p, const float* __restrict__ seg_decay, const float* init,
+__global__ void m2rnn_la_seg_scan_kernel(const LaParams p, const float* seg_decay, const float* init,
                                          int reverse) {
     const int kv4 = p.K * p.V / 4;
     const size_t e = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
@@ -728,6 +728,11 @@ cudaError_t launch_shape(const LaParams& p, const Maps& m, float* seg_decay, cud
 float* decays_of(const LaParams& p) {   // behind the segment states in the workspace
     return p.seg_state + (size_t)p.B * p.H * p.segs * p.K * p.V;
 }
+cudaError_t launch_scan(const LaParams& p, const float* init, int reverse, cudaStream_t s) {
+    const size_t n = (size_t)p.B * p.H * p.K * p.V / 4;
+    m2rnn_la_seg_scan_kernel<<<(unsigned)((n + 127) / 128), 128, 0, s>>>(p, decays_of(p), init, reverse);
+    return cudaGetLastError();
+}
 
 }  // namespace
 
@@ -767,10 +772,7 @@ cudaError_t launch_la_fwd_tc(const LaParams& q, cudaStream_t s) {
     if (p.segs > 1) {
         cudaError_t e = launch_shape<Sum<false>::Kernel>(p, m, decays_of(p), s);
         if (e != cudaSuccess) return e;
-        const size_t n = (size_t)p.B * p.H * p.K * p.V / 4;
-        m2rnn_la_seg_scan_kernel<<<(unsigned)((n + 127) / 128), 128, 0, s>>>(p, decays_of(p), p.S0, 0);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+        if ((e = launch_scan(p, p.S0, 0, s)) != cudaSuccess) return e;
     }
     return launch_shape<FwdKernel>(p, m, nullptr, s);
 }
@@ -783,11 +785,9 @@ cudaError_t launch_la_seg_grads(const LaParams& p, cudaStream_t s) {
         return cudaErrorNotSupported;
     m.q = m.k;
     m.y = m.v;
-    cudaError_t e = launch_shape<Sum<true>::Kernel>(p, m, decays_of(p), s);
+    const cudaError_t e = launch_shape<Sum<true>::Kernel>(p, m, decays_of(p), s);
     if (e != cudaSuccess) return e;
-    const size_t n = (size_t)p.B * p.H * p.K * p.V / 4;
-    m2rnn_la_seg_scan_kernel<<<(unsigned)((n + 127) / 128), 128, 0, s>>>(p, decays_of(p), p.dST, 1);
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : launch_scan(p, p.dST, 1, s);
 }
 
 // Reads and clears the status word of this file's kernels.

@@ -18,6 +18,7 @@
 // kernel adds the blocks in a fixed order: no atomics, the same bits every
 // time.
 #include "kernels.h"
+#include "launch.h"
 #include "layer_norm.h"
 
 #include <cuda_bf16.h>
@@ -142,68 +143,122 @@ __device__ __forceinline__ Block block_of(const NormParams& p) {
     return {(int)(blockIdx.x / p.chunks), chunk * per, min(p.T, (chunk + 1) * per)};
 }
 
+// Rows at a time and CTAs per SM: what hides the loads' latency within the
+// registers, and for rows that take the whole CTA the barriers too.  Measured,
+// us (see the kernels for the shapes):
+//   forward, rows of 2048: 2 rows and 4 CTAs 14.8, 4 and 2 17.1, 1 and 6 20.4;
+//            fp32 rows of 128: 4 rows and 2 CTAs 68, 2 and 4 82
+//   backward, rows of 64: 3 rows 22.4, 2 25.7; rows of 2048: 2 rows 26.7, 3 32.2
+constexpr int unroll_fwd(int values, bool cta) { return values >= 32 ? 1 : values >= 16 || cta ? 2 : 4; }
+constexpr int ctas_fwd(int values, bool cta) { return cta && values < 16 ? 4 : 2; }
+constexpr int unroll_bwd(int values, bool cta, bool bf16) { return values >= 16 ? 1 : cta || !bf16 ? 2 : 3; }
+
+// 1/sqrt(x) to the last place or two: the approximation and one Newton step,
+// which 0 and infinity do without.
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const float r = rsqrtf(x), e = fmaf(-x * r, r, 1.f);
+    return e == e ? fmaf(0.5f * r, e, r) : r;
+}
+
+// VEC values in pairs: additions, products and multiply-adds of two values take
+// one instruction.  (One value at a time, issue slots and not HBM bounded rows
+// of 64: forward 17.0 against 13.5 us, 134 MB moved.)
+template <int VEC, class F>
+__device__ __forceinline__ void by_pairs(F&& f) {   // f(i, i + 1)
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) f(e, VEC == 1 ? 0 : e + 1);
+}
+
 // LPR threads per row, CH groups of VEC values per thread (N <= LPR·VEC·CH), U
 // rows at a time.  A CTA takes items of kGroups·U consecutive rows of one
-// (b, h), blockIdx.x and every gridDim.x-th from there, and has the next one's
-// loads in flight while it works on one.
+// (b, h), a contiguous range of them, and has the next one's loads in flight
+// while it works on one.  Measured against the copy rate of 6.45 TB/s: 2^18
+// rows of 64 bf16 12.7 us (82%), 2^19 fp32 rows of 128 to bf16 68 us (92%),
+// 8191 rows of 2048 bf16 14.9 us (70%: two barriers of the CTA a row group).
 template <class X, class Y, int VEC, int LPR, int CH, int U>
-__global__ void __launch_bounds__(kThreads) m2rnn_norm_fwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kThreads, VEC == 8 && CH == 1 && LPR <= 32 ? 2 : 0)
+    m2rnn_norm_fwd_kernel(const NormParams p) {
     constexpr int kGroups = kThreads / LPR, kRows = kGroups * U;
+    constexpr bool kKeep = CH == 1 && VEC == 8;   // weight and bias stay in registers over the items of a head
     __shared__ float buf[2][kThreads / 32][U];
     const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, N = p.N;
     const float inv = 1.f / (float)N;
     const unsigned per = (p.T + kRows - 1) / kRows, items = (unsigned)(p.B * p.H) * per;
+    unsigned item = (unsigned)((unsigned long long)items * blockIdx.x / gridDim.x);
+    const unsigned end = (unsigned)((unsigned long long)items * (blockIdx.x + 1) / gridDim.x);
     Raw<X, VEC> next[U][CH];
-    auto fetch = [&](unsigned item) {
-        const unsigned bh = item / per;
-        const int t0 = (int)(item % per) * kRows + grp;
-        const X* x = static_cast<const X*>(p.x) + ((size_t)bh * p.T + t0) * N;
+    int nbh = item / per, nblk = item % per;   // of the item to be fetched
+    auto fetch = [&]() {
+        const int t0 = nblk * kRows + grp;
+        const X* x = static_cast<const X*>(p.x) + ((size_t)nbh * p.T + t0) * N;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const int i = (c * LPR + lane) * VEC;
-                if (item < items && t0 + u * kGroups < p.T && i < N) next[u][c].get(x + (size_t)u * kGroups * N + i);
+                if (t0 + u * kGroups < p.T && i < N) next[u][c].get(x + (size_t)u * kGroups * N + i);
                 else next[u][c].zero();
             }
+        if (++nblk == (int)per) { nblk = 0; ++nbh; }
     };
-    fetch(blockIdx.x);
-    for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {   // the same count for every thread
-        const int bh = (int)(item / per), t0 = (int)(item % per) * kRows + grp;
+    int bh = nbh, blk = nblk, h = bh % p.H, b = bh / p.H;
+    float w[kKeep ? VEC : 1], bias[kKeep ? VEC : 1];
+    auto affine = [&](int i, float* wv, float* bv) {
+        float x[VEC], z[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) { x[e] = 1.f; z[e] = 0.f; }
+        if (i < N && p.weight) load<VEC>(p.weight + (size_t)h * N + i, x);
+        if (i < N && p.bias) load<VEC>(p.bias + (size_t)h * N + i, z);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) { wv[e] = x[e]; bv[e] = z[e]; }
+    };
+    if (item < end) {
+        fetch();
+        if constexpr (kKeep) affine(lane * VEC, w, bias);
+    }
+    for (; item < end; ++item) {   // the same count for every thread
+        const int t0 = blk * kRows + grp;
         float v[U][CH][VEC], s[U], m[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            s[u] = 0.f;
+            float2 a = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
+            for (int c = 0; c < CH; ++c) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    v[u][c][e] = next[u][c][e];
-                    s[u] += v[u][c][e];
-                }
+                for (int e = 0; e < VEC; ++e) v[u][c][e] = next[u][c][e];
+                if constexpr (VEC == 1) a.x += v[u][c][0];
+                else by_pairs<VEC>([&](int i, int j) { a = __fadd2_rn(a, make_float2(v[u][c][i], v[u][c][j])); });
+            }
+            s[u] = a.x + a.y;
         }
-        fetch(item + gridDim.x);
+        if (item + 1 < end) fetch();
         if (!p.rms) row_sums<LPR, U>(s, buf[0]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             m[u] = p.rms ? 0.f : s[u] * inv;
-            s[u] = 0.f;
+            float2 a = make_float2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                const bool in = (c * LPR + lane) * VEC < N;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    v[u][c][e] -= m[u];
-                    s[u] = in ? fmaf(v[u][c][e], v[u][c][e], s[u]) : s[u];
+                const float d = (c * LPR + lane) * VEC < N ? -m[u] : 0.f;   // nothing beside the row
+                if constexpr (VEC == 1) {
+                    v[u][c][0] += d;
+                    a.x = fmaf(v[u][c][0], v[u][c][0], a.x);
+                } else {
+                    by_pairs<VEC>([&](int i, int j) {
+                        const float2 x = __fadd2_rn(make_float2(v[u][c][i], v[u][c][j]), make_float2(d, d));
+                        a = __ffma2_rn(x, x, a);
+                        v[u][c][i] = x.x; v[u][c][j] = x.y;
+                    });
                 }
             }
+            s[u] = a.x + a.y;
         }
         row_sums<LPR, U>(s, buf[1]);
         if constexpr (LPR > 32) __syncthreads();   // buf[] is free for the next rows
         float rs[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            rs[u] = 1.f / sqrtf(s[u] * inv + p.eps);
+            rs[u] = inv_sqrt(s[u] * inv + p.eps);
             const int t = t0 + u * kGroups;
             if (lane == 0 && t < p.T) {
                 const size_t r = (size_t)bh * p.T + t;
@@ -211,34 +266,48 @@ __global__ void __launch_bounds__(kThreads) m2rnn_norm_fwd_kernel(const NormPara
                 if (p.rstd) p.rstd[r] = rs[u];
             }
         }
-        const size_t wrow = (size_t)(bh % p.H) * N;
-        Y* y = static_cast<Y*>(p.y) + token_row(p, bh, t0) * N;
+        Y* y = static_cast<Y*>(p.y) + (((size_t)b * p.T + t0) * p.H + h) * N;
         const size_t ystep = (size_t)kGroups * p.H * N;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int i = (c * LPR + lane) * VEC;
             if (i >= N) continue;
-            float w[VEC], b[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) { w[e] = 1.f; b[e] = 0.f; }
-            if (p.weight) load<VEC>(p.weight + wrow + i, w);
-            if (p.bias) load<VEC>(p.bias + wrow + i, b);
+            float wv[VEC], bv[VEC];
+            if constexpr (!kKeep) affine(i, wv, bv);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (t0 + u * kGroups >= p.T) continue;
                 float o[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = fmaf(v[u][c][e] * rs[u], w[e], b[e]);
+                if constexpr (VEC == 1) {
+                    o[0] = fmaf(v[u][c][0] * rs[u], wv[0], bv[0]);
+                } else {
+                    by_pairs<VEC>([&](int e, int f) {
+                        const float2 x = __ffma2_rn(
+                            __fmul2_rn(make_float2(v[u][c][e], v[u][c][f]), make_float2(rs[u], rs[u])),
+                            kKeep ? make_float2(w[kKeep ? e : 0], w[kKeep ? f : 0]) : make_float2(wv[e], wv[f]),
+                            kKeep ? make_float2(bias[kKeep ? e : 0], bias[kKeep ? f : 0]) : make_float2(bv[e], bv[f]));
+                        o[e] = x.x; o[f] = x.y;
+                    });
+                }
                 store<VEC>(y + u * ystep + i, o);
             }
+        }
+        if (++blk == (int)per) {   // the next (b, h)
+            blk = 0;
+            ++bh;
+            if (++h == p.H) { h = 0; ++b; }
+            if constexpr (kKeep) if (item + 1 < end) affine(lane * VEC, w, bias);
         }
     }
 }
 
 // A CTA takes a block of rows of one (b, h), U·kGroups at a time, the next ones
-// in flight.
+// in flight.  Measured with the sums' kernel: 2^18 rows of 64 bf16 22.6 us,
+// 8191 rows of 2048 25.3 us, 101 MB each (15.6 us at the copy rate).  Bound by
+// the loads that fit in flight beside the sums in 128 registers a thread, and
+// by the second kernel (its early launch is worth 1 us).
 template <class X, class Y, class DX, int VEC, int LPR, int CH, int U>
-__global__ void __launch_bounds__(kThreads) m2rnn_norm_bwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kThreads, VEC == 8 && CH == 1 ? 2 : 0) m2rnn_norm_bwd_kernel(const NormParams p) {
     constexpr int kGroups = kThreads / LPR, kRows = kGroups * U;
     __shared__ float buf[kThreads / 32][2 * U];
     __shared__ float sums[LPR > 32 ? 1 : kThreads * VEC];   // row groups' partial sums, one chunk at a time
@@ -284,29 +353,43 @@ __global__ void __launch_bounds__(kThreads) m2rnn_norm_bwd_kernel(const NormPara
         float n[U][CH][VEC], g[U][CH][VEC], s[2 * U], rs[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const bool live = tb + u * kGroups + grp < b.t1;
             rs[u] = nr[u];
-            float s1 = 0.f, s2 = 0.f;
+            float2 s1 = make_float2(0.f, 0.f), s2 = s1;
+            const float2 r2 = make_float2(rs[u], rs[u]);
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                const bool in = live && (c * LPR + lane) * VEC < N;   // nothing of a NaN mean beside the row
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    n[u][c][e] = in ? (nx[u][c][e] - nm[u]) * rs[u] : 0.f;
-                    g[u][c][e] = ny[u][c][e];
-                    dw[c][e] = fmaf(g[u][c][e], n[u][c][e], dw[c][e]);
-                    db[c][e] += g[u][c][e];
-                    g[u][c][e] *= w[c][e];
-                    s1 += g[u][c][e];
-                    s2 = fmaf(g[u][c][e], n[u][c][e], s2);
+                // beside the row, and behind the last (rs = 0), n is 0
+                const float m = (c * LPR + lane) * VEC < N ? -nm[u] : 0.f;
+                if constexpr (VEC == 1) {
+                    const float a = (nx[u][c][0] + m) * rs[u], d = ny[u][c][0];
+                    dw[c][0] = fmaf(d, a, dw[c][0]);
+                    db[c][0] += d;
+                    n[u][c][0] = a;
+                    g[u][c][0] = d * w[c][0];
+                    s1.x += g[u][c][0];
+                    s2.x = fmaf(g[u][c][0], a, s2.x);
+                } else {
+                    by_pairs<VEC>([&](int e, int f) {
+                        const float2 a = __fmul2_rn(__fadd2_rn(make_float2(nx[u][c][e], nx[u][c][f]), make_float2(m, m)), r2),
+                                     d = make_float2(ny[u][c][e], ny[u][c][f]),
+                                     wd = __ffma2_rn(d, a, make_float2(dw[c][e], dw[c][f])),
+                                     bd = __fadd2_rn(make_float2(db[c][e], db[c][f]), d),
+                                     gg = __fmul2_rn(d, make_float2(w[c][e], w[c][f]));
+                        dw[c][e] = wd.x; dw[c][f] = wd.y;
+                        db[c][e] = bd.x; db[c][f] = bd.y;
+                        n[u][c][e] = a.x; n[u][c][f] = a.y;
+                        g[u][c][e] = gg.x; g[u][c][f] = gg.y;
+                        s1 = __fadd2_rn(s1, gg);
+                        s2 = __ffma2_rn(gg, a, s2);
+                    });
                 }
             }
-            s[2 * u] = s1;
-            s[2 * u + 1] = s2;
+            s[2 * u] = s1.x + s1.y;
+            s[2 * u + 1] = s2.x + s2.y;
         }
         fetch(tb + kRows + grp);
         row_sums<LPR, 2 * U>(s, buf);
-        if constexpr (LPR > 32) __syncthreads();
+        if constexpr (LPR > 32) __syncthreads();   // (two buffers in turn instead: no faster)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int t = tb + u * kGroups + grp;
@@ -318,13 +401,23 @@ __global__ void __launch_bounds__(kThreads) m2rnn_norm_bwd_kernel(const NormPara
                 const int i = (c * LPR + lane) * VEC;
                 if (i >= N) continue;
                 float o[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = rs[u] * (g[u][c][e] - m1 - n[u][c][e] * m2);
+                if constexpr (VEC == 1) {
+                    o[0] = rs[u] * (g[u][c][0] - m1 - n[u][c][0] * m2);
+                } else {
+                    by_pairs<VEC>([&](int e, int f) {
+                        const float2 x = __fmul2_rn(
+                            make_float2(rs[u], rs[u]),
+                            __ffma2_rn(make_float2(n[u][c][e], n[u][c][f]), make_float2(-m2, -m2),
+                                       __fadd2_rn(make_float2(g[u][c][e], g[u][c][f]), make_float2(-m1, -m1))));
+                        o[e] = x.x; o[f] = x.y;
+                    });
+                }
                 store<VEC>(dx + i, o);
             }
         }
     }
     if (!p.part) return;
+    cudaTriggerProgrammaticLaunchCompletion();   // the sums' kernel may be set up; it waits for this one's end
     float* part = p.part + (size_t)blockIdx.x * 2 * N;
     if constexpr (LPR > 32) {
 #pragma unroll
@@ -355,22 +448,24 @@ __global__ void __launch_bounds__(kThreads) m2rnn_norm_bwd_kernel(const NormPara
 }
 
 // dweight, dbias [H][N]: the row blocks' sums, added in ascending (b, block)
-// order by eight groups of threads and then over the groups.
-__global__ void __launch_bounds__(256) m2rnn_norm_dw_kernel(const NormParams p) {
-    __shared__ float s[8][32];
+// order by 32 groups of threads and then over the groups.  Launched while the
+// backward kernel runs out, whose end it waits for.
+__global__ void __launch_bounds__(1024) m2rnn_norm_dw_kernel(const NormParams p) {
+    __shared__ float s[32][32];
     const int N = p.N, h = blockIdx.y, lane = threadIdx.x % 32, grp = threadIdx.x / 32;
     const int e = blockIdx.x * 32 + lane;                    // column of [dw | db]
     const int n = p.B * p.chunks;
     float a = 0.f;
+    cudaGridDependencySynchronize();
     if (e < 2 * N)
 #pragma unroll 8
-        for (int j = grp; j < n; j += 8)
+        for (int j = grp; j < n; j += 32)
             a += p.part[((size_t)((j / p.chunks) * p.H + h) * p.chunks + j % p.chunks) * 2 * N + e];
     s[grp][lane] = a;
     __syncthreads();
     if (grp == 0 && e < 2 * N) {
 #pragma unroll
-        for (int g = 1; g < 8; ++g) a += s[g][lane];
+        for (int g = 1; g < 32; ++g) a += s[g][lane];
         float* out = e < N ? p.dweight : p.dbias;
         if (out) out[(size_t)h * N + (e < N ? e : e - N)] = a;
     }
@@ -476,10 +571,6 @@ bool by_length(int N, F&& f) {
     }
     return true;
 }
-// Rows at a time: up to 32 values a thread forward, 16 (of x and of dy) backward.
-constexpr int unroll_fwd(int values) { return values >= 32 ? 1 : values >= 16 ? 2 : 4; }
-constexpr int unroll_bwd(int values) { return values >= 16 ? 1 : 2; }
-
 unsigned capped(size_t want, int per_sm) {
     const size_t cap = (size_t)kNumSMs * per_sm;
     return (unsigned)(want < cap ? want : cap);
@@ -491,9 +582,9 @@ struct Fwd {
     cudaStream_t s;
     template <int VEC, int LPR, int CH>
     void operator()() {
-        constexpr int U = unroll_fwd(VEC * CH), kRows = kThreads / LPR * U;
+        constexpr int U = unroll_fwd(VEC * CH, LPR > 32), kRows = kThreads / LPR * U;
         const size_t items = (size_t)p.B * p.H * ((p.T + kRows - 1) / kRows);
-        m2rnn_norm_fwd_kernel<X, Y, VEC, LPR, CH, U><<<capped(items, 2), kThreads, 0, s>>>(p);
+        m2rnn_norm_fwd_kernel<X, Y, VEC, LPR, CH, U><<<capped(items, ctas_fwd(VEC * CH, LPR > 32)), kThreads, 0, s>>>(p);
     }
 };
 template <class X, class Y, class DX>
@@ -502,7 +593,8 @@ struct Bwd {
     cudaStream_t s;
     template <int VEC, int LPR, int CH>
     void operator()() {
-        m2rnn_norm_bwd_kernel<X, Y, DX, VEC, LPR, CH, unroll_bwd(VEC * CH)><<<p.B * p.H * p.chunks, kThreads, 0, s>>>(p);
+        constexpr int U = unroll_bwd(VEC * CH, LPR > 32, sizeof(X) + sizeof(Y) == 4);
+        m2rnn_norm_bwd_kernel<X, Y, DX, VEC, LPR, CH, U><<<p.B * p.H * p.chunks, kThreads, 0, s>>>(p);
     }
 };
 
@@ -550,8 +642,7 @@ int norm_bwd_chunks(int B, int H, int T, int N) { return chunks_for(B, H, T, N, 
 cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s) {
     cudaError_t e = p.y_fp32 ? bwd_x<float>(p, s) : bwd_x<__nv_bfloat16>(p, s);
     if (e != cudaSuccess || !p.part) return e;
-    m2rnn_norm_dw_kernel<<<dim3((2 * p.N + 31) / 32, p.H), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(m2rnn_norm_dw_kernel, dim3((2 * p.N + 31) / 32, p.H), 1024, 0, s, p);
 }
 
 }  // namespace m2rnn

@@ -172,8 +172,8 @@ static m2rnn_status check_norm(const m2rnn_norm_dims* d) {
     if ((d->x_fp32 & ~1) || (d->y_fp32 & ~1) || (d->dx_fp32 & ~1) || (d->rms & ~1)) return M2RNN_ERR_INVALID_ARG;
     if (d->dx_fp32 && !d->x_fp32) return M2RNN_ERR_INVALID_ARG;
     if (!(d->eps >= 0.f)) return M2RNN_ERR_INVALID_ARG;
-    // pairs index 32-bit grids, blocks of rows a 32-bit counter
-    if ((long long)d->B * d->H > (1 << 24) || d->N > (1 << 28)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
+    // pairs index 32-bit grids, rows and blocks of rows 32-bit counters
+    if ((long long)d->B * d->H > (1 << 24) || d->T > (1 << 30) || d->N > (1 << 28)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
     if ((long long)d->B * d->H * d->T > (1LL << 35)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
     return M2RNN_OK;
 }

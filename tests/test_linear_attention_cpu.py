@@ -103,6 +103,7 @@ def test_layer_norm_refuses(L):
         assert L.m2rnn_layer_norm_workspace(_norm(**bad)) == _lib.REFUSED
     assert fwd(None) == _lib.ERR_INVALID_ARG == bwd(None)
     assert fwd(_norm(B=1 << 13, H=1 << 12)) == _lib.ERR_UNSUPPORTED_SHAPE
+    assert fwd(_norm(B=1, H=1, T=(1 << 30) + 1, N=1)) == _lib.ERR_UNSUPPORTED_SHAPE
     for n in ("x", "y"):
         assert fwd(_norm(), **{n: None}) == _lib.ERR_INVALID_ARG
     for n in ("x", "w", "b", "y", "m", "r"):
