@@ -28,6 +28,13 @@
 // One CTA per (b, h) or time segment of it.  16 warps compute (thread = token
 // or state row = tensor-memory lane, the four warpgroups sharing the columns),
 // one issues the products, one moves tiles, one computes decays and df.
+//
+// Measured: 128 pairs of 64 x 64 over 2048 tokens 122 us (the reads of k, v, q,
+// dy and the checkpoints and the writes of dk, dv, dq take 42.6 us at the copy
+// rate of 6.45 TB/s), of 128 x 128 over 4096 tokens 459 us (191 us).  As in the
+// forward a chunk's chain of waits bounds it, 7.6 and 14.3 us a chunk (tensor
+// pipe 21 and 26%, issue 35 and 33%, HBM 21 and 25%), and 96 registers a thread,
+// of which 128 x 128 spills 71: one CTA an SM, 19 warps.
 #include "kernels.h"
 #include "la_tc.cuh"
 
