@@ -760,20 +760,20 @@ cudaError_t launch_scan(const LaParams& p, const float* init, int reverse, cudaS
 // pay for the sums that run before it, a launch and a pass over k and v (q and
 // dy).  Those cost more the more CTAs share the memory.  Measured, us, one
 // walk against segments of T/128 chunks:
-//   forward   1 pair, 64 x 64:    4 chunks 14.8 / 15.7,   6  19.8 / 16.6
-//            24 pairs, 64 x 64:   6 chunks 19.8 / 20.1,   8  24.4 / 21.6
-//            48 pairs, 128 x 128: 16 chunks 75.5 / 87.4, 32  142 / 117
-//            74 pairs, 128 x 128: 32 chunks 143 / 149,   64  277 / 246
-//   backward  1 pair, 64 x 64:    2 chunks 17.5 / 19.5,   3  24.2 / 19.8
-//            48 pairs, 64 x 64:   4 chunks 30.8 / 31.0,   6  43.6 / 35.1
-//            74 pairs, 64 x 64:   6 chunks 47.1 / 45.7,   8  61.2 / 55.4
-//            74 pairs, 128 x 128: 6 chunks 93.8 / 104,   12  175 / 157
+//   forward   1 pair, 64 x 64:     4 chunks 14.4 / 14.8,  5  16.5 / 14.6
+//            24 pairs, 64 x 64:    5 chunks 16.9 / 16.9,  6  19.3 / 17.6
+//            37 pairs, 128 x 128:  6 chunks 32.1 / 35.6,  8  40.9 / 38.6
+//            48 pairs, 128 x 128: 10 chunks 50.3 / 51.4, 12  58.6 / 56.8
+//            74 pairs, 128 x 128: 24 chunks 110 / 111,   32  143 / 136
+//   backward  1 pair, 64 x 64:     2 chunks 16.9 / 18.3,  3  23.7 / 18.6
+//            48 pairs, 64 x 64:    3 chunks 23.9 / 22.9,  6  43.4 / 33.0
+//            74 pairs, 64 x 64:    4 chunks 30.8 / 33.3,  6  43.8 / 42.7
 LaPlan la_plan(int B, int H, int T, bool backward) {
     const int chunks = (T + kLaChunk - 1) / kLaChunk;
     const long long pairs = (long long)B * H;
     if (pairs * 2 > kNumSMs) return {1, chunks};
     const int most = kNumSMs / (int)pairs, want = most < chunks ? most : chunks, per = (chunks + want - 1) / want;
-    const int need = !backward ? 4 + (int)(pairs * pairs) / 256 : pairs < 48 ? 2 : 1 + (int)pairs / 24;
+    const int need = backward ? 2 + (int)pairs / 64 : 4 + (int)(pairs * pairs) / 512;
     if (chunks - per < need) return {1, chunks};
     return {(chunks + per - 1) / per, per};
 }
