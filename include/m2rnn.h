@@ -216,7 +216,11 @@ m2rnn_status m2rnn_backward_noalloc(const m2rnn_dims* d,
  * Gates lie in [0, 1].  A gate of 0 (or below 2^-126, which fp32 arithmetic
  * here flushes to 0) discards the state before it.  A state that
  * holds an infinity or NaN is not discarded by a gate of 0 (0·inf = NaN, as in
- * the formula).
+ * the formula).  An infinity or NaN in a token's k, v, q, f or dy reaches what
+ * depends on it, and with mode M2RNN_MODE_BF16_TC it may reach the results of
+ * every token of its (b, h) and chunk of 128 (tokens 128c to 128c+127), the
+ * ones before it too: the chunk's masked products multiply it by 0.  Tokens
+ * that are to be ignored hold finite values.
  *
  * Errors, ownership, ordering and alignment are as above; ws may be NULL when
  * the workspace size is 0.  Tensors with no elements may be NULL.  The

@@ -345,7 +345,8 @@ def linear_attention(k, v, q, f, S0=None, *, want_ST: bool = True, want_ckpt: bo
     inputs' type, ST [B, H, K, V] is fp32.  ckpt [B, H, ceil(T/128), V/4, K, 4]
     holds the states that linear_attention_backward starts from (element (i, j)
     of a state at [j // 4, i, j % 4]).  `out` may hold buffers for y, ST and
-    ckpt; ST may be S0's."""
+    ckpt; ST may be S0's.  Padding holds finite values: a NaN in a bf16 token
+    may reach the earlier tokens of its 128-token chunk too."""
     (d, need, _), B, H, T, K, V = _la_inputs(k, v, q, f, S0, f_is_logit, True)
     y = _out(out, "y", k, (B, H, T, V), k.dtype)
     ST = _out(out, "ST", k, (B, H, K, V), torch.float32) if want_ST else None

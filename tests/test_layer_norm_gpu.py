@@ -210,3 +210,36 @@ def test_readout_of_the_scan_and_its_gradient():
     assert float((g["dx"].double() - wdx).norm() / wdx.norm()) <= 2.0 ** -8
     back = a.backward(x["k"], x["v"], x["q"], x["f"], x["W"], ck, g["dx"])
     assert all(bool(torch.isfinite(t).all()) for t in back.values())
+
+
+@pytest.mark.parametrize("shape,heads", [((2, 3, 500, 64), True), ((700, 2048), False)])
+def test_captured_and_replayed(shape, heads):
+    """A captured forward and backward, replayed on new inputs, gives the eager results, twice in a row too."""
+    a = api()
+    g = torch.Generator().manual_seed(31)
+    N = shape[-1]
+    x = torch.randn(*shape, generator=g).to(BF).to(DEV)
+    dy = torch.randn(*((shape[0], shape[2], shape[1], N) if heads else shape), generator=g).to(BF).to(DEV)
+    w = torch.randn(*((shape[1], N) if heads else (N,)), generator=g).to(DEV)
+
+    def work():
+        y, mean, rstd = a.layer_norm(x, w)
+        d = a.layer_norm_backward(dy, x, w, mean, rstd)
+        return [y, d["dx"], d["dweight"], d["dbias"]]
+
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first = work()
+        second = work()
+    for _ in range(2):
+        x.copy_(torch.randn(*shape, generator=g))
+        dy.copy_(torch.randn(*dy.shape, generator=g))
+        want = work()
+        for t in first + second:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got in (first, second):
+            assert all(torch.equal(p, q) for p, q in zip(got, want))

@@ -161,7 +161,7 @@ def test_buffers_on_16_bytes(K, V):
 
 
 def test_a_nan_reaches_what_it_should():
-    """A NaN in one pair's v: its later readouts and the states are NaN, other pairs and earlier tokens are not."""
+    """A NaN in one pair's v: its later readouts and the states are NaN, other pairs and earlier chunks are not."""
     a = api()
     x, _ = inputs(1, 2, 300, 64, 64, start=False, seed=14)
     x["v"][0, 0, 140, 3] = float("nan")
