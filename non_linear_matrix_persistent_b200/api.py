@@ -29,6 +29,7 @@ K = 32); longer strides (up to 16) run the general-shape backward.
 """
 from __future__ import annotations
 
+import functools
 from typing import Dict, Optional, Tuple
 
 import torch
@@ -370,7 +371,7 @@ def linear_attention_step(k, v, q, f, S, *, ST: Optional[torch.Tensor] = None, y
     else:
         _same("ST", ST, (B, H, K, V), torch.float32, k.device)
     if y is None:
-        y = k.new_empty((B, H, V))
+        y = torch.empty_like(v)
     else:
         _same("y", y, (B, H, V), k.dtype, k.device)
     ws, wp = _scratch(need, k)
@@ -408,6 +409,12 @@ def linear_attention_backward(k, v, q, f, ckpt, dy, dST=None, *, f_is_logit: boo
 _NORM_TYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
+@functools.lru_cache(maxsize=4096)
+def _norm_dims(*fields):
+    """The C dims of a shape: making them anew costs 1 us a call."""
+    return _lib.NormDims(*fields)
+
+
 def _norm_shape(x, weight, bias):
     """(B, H, T, N) of a call, and whether x is a head-first readout."""
     first = weight if weight is not None else bias
@@ -425,8 +432,8 @@ def _norm_shape(x, weight, bias):
         B, H, T = 1, 1, x.numel() // N if N else 0
     if N < 1:
         raise ValueError("the last dimension of x is empty")
-    if T >= 1 << 31:
-        raise ValueError("x has %d rows: at most 2^31 - 1 in one call" % T)
+    if T > 1 << 30:
+        raise ValueError("x has %d rows: at most 2^30 in one call" % T)
     dev = x.device
     _same("x", x, x.shape, x.dtype, dev)
     ps = (H, N) if heads else (N,)
@@ -456,7 +463,7 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = Fals
     y = _out(out, "y", x, (B, T, H, N) if heads else x.shape, yt)
     rstd = _out(out, "rstd", x, lead, torch.float32)
     mean = None if rms else _out(out, "mean", x, lead, torch.float32)
-    d = _lib.NormDims(B, H, T, N, _NORM_TYPES[x.dtype], _NORM_TYPES[yt], 0, 1 if rms else 0, eps)
+    d = _norm_dims(B, H, T, N, _NORM_TYPES[x.dtype], _NORM_TYPES[yt], 0, 1 if rms else 0, float(eps))
     _call("m2rnn_layer_norm_forward", x.device, _lib.lib().m2rnn_layer_norm_forward, d, x.data_ptr(), _ptr(weight),
           _ptr(bias), y.data_ptr(), _ptr(mean), rstd.data_ptr())
     return y, mean, rstd
@@ -488,7 +495,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, rms: bool = False, heads: 
     shape = (H, N) if per_head else (N,)
     for n, sh, t in (("dx", x.shape, dt), ("dweight", shape, torch.float32), ("dbias", shape, torch.float32)):
         g[n] = _out(g, n, x, sh, t)
-    d = _lib.NormDims(B, H, T, N, _NORM_TYPES[x.dtype], _NORM_TYPES[dy.dtype], _NORM_TYPES[dt], 1 if rms else 0, 0.0)
+    d = _norm_dims(B, H, T, N, _NORM_TYPES[x.dtype], _NORM_TYPES[dy.dtype], _NORM_TYPES[dt], 1 if rms else 0, 0.0)
     L = _lib.lib()
     need = L.m2rnn_layer_norm_workspace(d)
     if need == _lib.REFUSED:
