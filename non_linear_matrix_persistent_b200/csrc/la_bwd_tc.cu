@@ -21,7 +21,8 @@
 // below 2^-100 act as 2^-100 there, which keeps that quotient; every other
 // gradient has the gate itself.
 //
-// Rounding: P', dP' and the copy of G that gives dv are bf16 operands; S and G
+// Rounding: P', dP' and the copy of G that gives dv are bf16 operands (two terms
+// of them up to kShort tokens); S and G
 // enter the products that df also reads, and a_t q_t enters G, as three bf16
 // terms (fp32 accuracy).
 //
@@ -126,14 +127,15 @@ __device__ __forceinline__ float column_sums(float (&r)[N]) {
 // an exponential each.  (One body for diagonal and other blocks: the two would
 // not fit the instruction cache together.)
 // PW: columns at a time, 16 or, where registers are short, 8.
-template <bool ZERO, int PW, class Place>
+// SHORT: the low terms too, 64 columns on in tensor memory and to dp_lo(column).
+template <bool ZERO, int PW, bool SHORT, class Place, class PlaceLo>
 __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const LaTablesZ* tab, int t0, float Fs, float Is,
-                                             float Zs, float r, int first, float* cut, Place dp) {
+                                             float Zs, float r, int first, float* cut, Place dp, PlaceLo dp_lo) {
     const int lane = threadIdx.x & 31;
     float run = 0.f;
 #pragma unroll
     for (int h = 16; h >= 0; h -= 16) {
-        uint32_t pp[8], pd[8];
+        uint32_t pp[8], pd[8], ppl[SHORT ? 8 : 1], pdl[SHORT ? 8 : 1];
 #pragma unroll
         for (int g = 16 - PW; g >= 0; g -= PW) {
             uint32_t x[PW], y[PW];
@@ -179,8 +181,13 @@ __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const La
                     PD = __fmul2_rn(P, Zd);
                     QD = __fmul2_rn(Q, Zd);
                 }
-                pp[(g + e) / 2] = pack_bf16(PD.x, PD.y);
-                pd[(g + e) / 2] = pack_bf16(QD.x, QD.y);
+                const uint32_t hp = pack_bf16(PD.x, PD.y), hd = pack_bf16(QD.x, QD.y);
+                pp[(g + e) / 2] = hp;
+                pd[(g + e) / 2] = hd;
+                if constexpr (SHORT) {
+                    ppl[(g + e) / 2] = pack_bf16(PD.x - bf16lo_to_f32(hp), PD.y - bf16hi_to_f32(hp));
+                    pdl[(g + e) / 2] = pack_bf16(QD.x - bf16lo_to_f32(hd), QD.y - bf16hi_to_f32(hd));
+                }
                 run += W.y;
                 R[e + 1] = h + g + e + 1 > first ? run : 0.f;   // sources strictly before the gate
                 run += W.x;
@@ -193,11 +200,17 @@ __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const La
         tmem_st_32x32b<8>(tp + h + 8, pd);
         *reinterpret_cast<uint4*>(dp(t0 + h)) = make_uint4(pd[0], pd[1], pd[2], pd[3]);
         *reinterpret_cast<uint4*>(dp(t0 + h + 8)) = make_uint4(pd[4], pd[5], pd[6], pd[7]);
+        if constexpr (SHORT) {
+            tmem_st_32x32b<8>(tp + 64 + h, ppl);
+            tmem_st_32x32b<8>(tp + 64 + h + 8, pdl);
+            *reinterpret_cast<uint4*>(dp_lo(t0 + h)) = make_uint4(pdl[0], pdl[1], pdl[2], pdl[3]);
+            *reinterpret_cast<uint4*>(dp_lo(t0 + h + 8)) = make_uint4(pdl[4], pdl[5], pdl[6], pdl[7]);
+        }
     }
     return run;
 }
 
-template <int KP, int VP>
+template <int KP, int VP, bool SHORT>   // SHORT: up to kShort tokens
 __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
     m2rnn_la_bwd_tc_kernel(const LaParams p, const __grid_constant__ BwdMaps maps) {
     using C = BCfg<KP, VP>;
@@ -286,11 +299,13 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             const int ph = i & 1;
             uint32_t q, k, v, dy;
             tiles(i, q, k, v, dy);
-            auto inter_dv = [&]() {
+            auto inter_dv = [&]() {   // K G with G in one term, or two
 #pragma unroll
-                for (int ks = 0; ks < KP / 16; ++ks)
-                    mma_ss(C::kDV, d_tile + k + kmajor(ks, 128), d_op + X + (C::kG0 >> 4) + ks * 128, id_vi,
-                                  ks > 0, one);
+                for (int e = SHORT ? 1 : 0; e >= 0; --e)
+#pragma unroll
+                    for (int ks = 0; ks < KP / 16; ++ks)
+                        mma_ss(C::kDV, d_tile + k + kmajor(ks, 128), d_op + X + (C::kG0 >> 4) + e * OP + ks * 128, id_vi,
+                               e < (SHORT ? 1 : 0) || ks > 0, one);
             };
             if (!(ok = la_wait_warp(b_full + stage_of(i) * 8, stage_phase(i), abort_flag, limit))) break;
             if (C::kEarly) {
@@ -335,17 +350,17 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             }
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)      // contraction over s, the rows of the dP'ᵀ and k tiles
-                mma_ss(C::kDQ, d_mn + XP + ks * 128, d_mn + k + ks * 128, id_dq, 1, one);
+                mma_ss(C::kDQ, d_mn + XP + ks * 128, d_mn + k + (SHORT ? ks & 3 : ks) * 128, id_dq, 1, one);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)      // over t: P'ᵀ and dP'ᵀ of 16 sinks over their 16 score columns
-                mma_ts(C::kDK, C::kP + ks * 16 + 8, d_mn + q + ks * 128, id_dk, 1, one);
+                mma_ts(C::kDK, C::kP + ks * 16 + 8, d_mn + q + (SHORT ? ks & 3 : ks) * 128, id_dk, 1, one);
             if (!C::kOwnDv) {
                 if (!(ok = la_wait_warp(r_dv, ph, abort_flag, limit))) break;
                 tc_fence_after();
             }
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-                mma_ts(C::kDV, C::kP + ks * 16, d_mn + dy + ks * 128, id_vi, 1, one);
+                mma_ts(C::kDV, C::kP + ks * 16, d_mn + dy + (SHORT ? ks & 3 : ks) * 128, id_vi, 1, one);
             mma_commit(b_out, one);
             if (!(ok = sum_for_G())) break;
         }
@@ -701,12 +716,21 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             };
             // ---- P'ᵀ, dP'ᵀ and df's sums: source s = row, sinks of block wg
             float run = 0.f;
-            if (wg < quarter) {   // sinks before the source
+            auto place_lo = [&](int col) { return dp + (col >> 6) * kTileBytes + sw128(row + 64, (col & 63) >> 3); };
+            if (SHORT && (wg >= 2 || quarter >= 2)) {
+                // behind the last token: these rows' results are not kept, these places hold the low terms
+            } else if (wg < quarter) {   // sinks before the source
                 const uint32_t z[16] = {};
-                tmem_st16(mylane + C::kP + wg * 32, z);
-                tmem_st16(mylane + C::kP + wg * 32 + 16, z);
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(dp + tile_at(wg * 32 + e)) = make_uint4(0, 0, 0, 0);
+                for (int l = 0; l < (SHORT ? 128 : 64); l += 64) {   // (and the low terms)
+                    tmem_st16(mylane + C::kP + l + wg * 32, z);
+                    tmem_st16(mylane + C::kP + l + wg * 32 + 16, z);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    *reinterpret_cast<uint4*>(dp + tile_at(wg * 32 + e)) = make_uint4(0, 0, 0, 0);
+                    if (SHORT) *reinterpret_cast<uint4*>(place_lo(wg * 32 + e)) = make_uint4(0, 0, 0, 0);
+                }
             } else {
                 const uint32_t tp = mylane + C::kP + wg * 32, tdp = mylane + C::kDP + wg * 32;
                 float* cut = sc->cut[quarter];
@@ -717,9 +741,9 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 const float r = ex2_approx((Fp - Ft) + (Ip - It));
                 constexpr int N = C::NS <= 16 ? 16 : 8;
                 if (Ze != 0.f || tab->steep != 0.f)
-                    run = score_block<true, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place);
+                    run = score_block<true, N, SHORT>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place, place_lo);
                 else
-                    run = score_block<false, N>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place);
+                    run = score_block<false, N, SHORT>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place, place_lo);
             }
             sc->total[wg][row] = run;
             if (C::kRoomy && !scale_all()) break;
@@ -843,7 +867,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
 template <int KP, int VP>
 cudaError_t launch(const LaParams& p, const BwdMaps& m, cudaStream_t s) {
     using C = BCfg<KP, VP>;
-    auto kern = m2rnn_la_bwd_tc_kernel<KP, VP>;
+    auto kern = p.T <= kShort ? m2rnn_la_bwd_tc_kernel<KP, VP, true> : m2rnn_la_bwd_tc_kernel<KP, VP, false>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     kern<<<p.B * p.H * p.segs, C::kThreads, C::kSmem, s>>>(p, m);

@@ -14,8 +14,8 @@
 // state's sum -> S form a chain over the chunks; P of the next chunk is formed
 // while the sum of this one is computed.
 //
-// Rounding: the masked scores and the copy of S that multiplies Q are bf16
-// operands (each term of y passes through exactly one of them, and y is
+// Rounding: the masked scores (two terms of them up to kShort tokens) and the
+// copy of S that multiplies Q are bf16 operands (each term of y passes through exactly one of them, and y is
 // rounded to bf16 itself); b_s k_s enters as three bf16 terms, so the state
 // keeps fp32 accuracy over any number of chunks.
 //
@@ -197,7 +197,7 @@ struct Cfg {
     static constexpr int NY = VP / 4;                           // columns of y per thread
 };
 
-template <int KP, int VP>
+template <int KP, int VP, bool SHORT>   // SHORT: up to kShort tokens
 __global__ void __launch_bounds__(kFwdThreads, 1)
     m2rnn_la_fwd_tc_kernel(const LaParams p, const __grid_constant__ Maps maps) {
     using C = Cfg<KP, VP>;
@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)   // P: 16 columns of bf16 pairs at the start of each block's 32
-                    mma_ts(C::kPV, (i % C::kScores) * 128 + (ks >> 1) * 32 + (ks & 1) * 8, d_mn + v + ks * 128, id_v, ks > 0,
-                           one);
+                    mma_ts(C::kPV, (i % C::kScores) * 128 + (ks >> 1) * 32 + (ks & 1) * 8,
+                           d_mn + v + (SHORT ? ks & 3 : ks) * 128, id_v, ks > 0, one);
                 if (!la_wait_warp(r_s, ph, abort_flag, limit)) break;
                 tc_fence_after();
 #pragma unroll
@@ -409,10 +409,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (!la_wait(b_sc + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) return false;
             tc_fence_after();
             const uint32_t at_ = mine + (i % C::kScores) * 128 + wg * 32;
-            uint32_t pk[16];
-            if (wg > quarter) {
+            uint32_t pk[16], lo[SHORT ? 16 : 1];
+            auto put = [&](int e, float x, float y) {   // columns 2e and 2e + 1
+                pk[e] = pack_bf16(x, y);
+                if constexpr (SHORT) lo[e] = pack_bf16(x - bf16lo_to_f32(pk[e]), y - bf16hi_to_f32(pk[e]));
+            };
+            if (wg > quarter || (SHORT && wg >= 2)) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) pk[e] = 0;
+                for (int e = 0; e < 16; ++e) put(e, 0.f, 0.f);
             } else {
                 uint32_t sc[32];
                 tmem_ld<32>(at_, sc);
@@ -429,8 +433,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                                     make_float2(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1]))),
                                      y = __fmul2_rn(__fmul2_rn(r2, make_float2(cs.z, cs.w)),
                                                     make_float2(__uint_as_float(sc[e + 2]), __uint_as_float(sc[e + 3])));
-                        pk[e / 2] = pack_bf16(e <= last ? x.x : 0.f, e + 1 <= last ? x.y : 0.f);
-                        pk[e / 2 + 1] = pack_bf16(e + 2 <= last ? y.x : 0.f, e + 3 <= last ? y.y : 0.f);
+                        put(e / 2, e <= last ? x.x : 0.f, e + 1 <= last ? x.y : 0.f);
+                        put(e / 2 + 1, e + 2 <= last ? y.x : 0.f, e + 3 <= last ? y.y : 0.f);
                     }
                 } else {
 #pragma unroll
@@ -440,12 +444,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         auto d = [&](int o, float f, float w_) {
                             return e + o <= lane ? __uint_as_float(sc[e + o]) * ex2_approx((Ft - f) + (It - w_)) : 0.f;
                         };
-                        pk[e / 2] = pack_bf16(d(0, fs.x, is.x), d(1, fs.y, is.y));
-                        pk[e / 2 + 1] = pack_bf16(d(2, fs.z, is.z), d(3, fs.w, is.w));
+                        put(e / 2, d(0, fs.x, is.x), d(1, fs.y, is.y));
+                        put(e / 2 + 1, d(2, fs.z, is.z), d(3, fs.w, is.w));
                     }
                 }
             }
-            tmem_st16(at_, pk);
+            if (!SHORT || wg < 2) tmem_st16(at_, pk);
+            if constexpr (SHORT) {
+                if (wg < 2) tmem_st16(at_ + 64, lo);
+            }
             tc_wait_st();
             warp_arrive(r_p);
             return true;
@@ -717,7 +724,7 @@ __global__ void m2rnn_la_seg_scan_kernel(const LaParams p, const float* seg_deca
 template <int KP, int VP>
 struct FwdKernel {
     static cudaError_t launch(const LaParams& p, const Maps& m, float*, cudaStream_t s) {
-        auto kern = m2rnn_la_fwd_tc_kernel<KP, VP>;
+        auto kern = p.T <= kShort ? m2rnn_la_fwd_tc_kernel<KP, VP, true> : m2rnn_la_fwd_tc_kernel<KP, VP, false>;
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<KP, VP>::kSmem);
         if (e != cudaSuccess) return e;
         kern<<<p.B * p.H * p.segs, kFwdThreads, Cfg<KP, VP>::kSmem, s>>>(p, m);

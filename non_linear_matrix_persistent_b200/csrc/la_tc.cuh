@@ -131,6 +131,14 @@ __device__ __forceinline__ void la_tables(Tab* tab, const LaParams& p, const flo
         make_float4(ex2_approx(sign * ((fe - F[0]) + (we - I[0]))), ex2_approx(sign * ((fe - F[1]) + (we - I[1]))),
                     ex2_approx(sign * ((fe - F[2]) + (we - I[2]))), ex2_approx(sign * ((fe - F[3]) + (we - I[3]))));
 }
+// Up to kShort tokens a sequence fills half a tile at most, and the masked
+// scores' other half takes their low terms (hi + lo bf16 against the same rows of the
+// other operand): with few terms in a sum their roundings do not average out.
+// Relative errors of dk, dv, dq at T = 1: up to 4e-3 without, 1.7e-3 with, which
+// is the results' own rounding.  Time at 64 tokens, 128 pairs of 128 x 128,
+// against a sequence of 65: forward 12.3 and 11.9 us, backward 21.6 and 19.3.
+constexpr int kShort = 64;
+
 // The f inputs of chunk c for la_tables; 0 behind the last token.
 __device__ __forceinline__ void la_load_f(const LaParams& p, int bh, int c, float (&x)[4]) {
     const int t = c * kLaChunk + (threadIdx.x & 31) * 4;
