@@ -14,8 +14,8 @@
 // state's sum -> S form a chain over the chunks; P of the next chunk is formed
 // while the sum of this one is computed.
 //
-// Rounding: the masked scores (two terms of them up to kShort tokens) and the
-// copy of S that multiplies Q are bf16 operands (each term of y passes through exactly one of them, and y is
+// Rounding: the masked scores and the copy of S that multiplies Q are bf16
+// operands, in two terms up to kShort tokens (each term of y passes through exactly one of them, and y is
 // rounded to bf16 itself); b_s k_s enters as three bf16 terms, so the state
 // keeps fp32 accuracy over any number of chunks.
 //
@@ -189,6 +189,7 @@ struct Cfg {
     static constexpr int kBars = 22;
     static constexpr int kSmem = kOffBar + kBars * 8 + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(KP * VP * 2 <= kStage && kStages >= 2, "the state's second term");
     // tensor memory: scores (two of them where they fit: the next chunk's are
     // computed early), P·V, Q·S, the state's sum
     static constexpr int kScores = VP == 64 ? 2 : 1;
@@ -241,7 +242,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // ------------------------------------------------------ products
         constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, 0, 0), id_v = idesc_bf16_f32(128, VP, 0, 1);
         const Desc d_tile = sw128_desc(sbase, 16), d_mn = sw128_desc(sbase, kTileBytes),
-                       d_s = sw128_desc(sbase + C::kOffS, KP * 128);
+                       d_s = sw128_desc(sbase + C::kOffS, KP * 128),
+                       d_s_lo = sw128_desc(sbase + C::kStage, KP * 128);   // SHORT: the second stage has no tiles
         constexpr uint32_t X = C::kOffX >> 4, XS = C::kTerm >> 4;
         auto tile = [](int ks) { return (uint32_t)((ks >> 2) * (kTileBytes >> 4) + (ks & 3) * 2); };
         const uint32_t one = lane == 0;
@@ -283,9 +285,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                            d_mn + v + (SHORT ? ks & 3 : ks) * 128, id_v, ks > 0, one);
                 if (!la_wait_warp(r_s, ph, abort_flag, limit)) break;
                 tc_fence_after();
+                if constexpr (SHORT) {
+#pragma unroll
+                    for (int ks = 0; ks < KP / 16; ++ks)
+                        mma_ss(C::kQS, d_tile + q + tile(ks), d_s_lo + ks * 128, id_v, ks > 0, one);
+                }
 #pragma unroll
                 for (int ks = 0; ks < KP / 16; ++ks)
-                    mma_ss(C::kQS, d_tile + q + tile(ks), d_s + ks * 128, id_v, ks > 0, one);
+                    mma_ss(C::kQS, d_tile + q + tile(ks), d_s + ks * 128, id_v, SHORT || ks > 0, one);
                 mma_commit(b_pv, one);
                 // (of two score matrices the other is free since r_s: y of the chunk before had been read)
                 if (C::kScores == 2) next_scores(false);
@@ -383,10 +390,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         auto put_operand = [&](int c) {   // S before chunk c: its bf16 copy for Q·S, the checkpoint
             uint8_t* op = smem + C::kOffS + (part.v0 >> 6) * (KP * 128);
 #pragma unroll
-            for (int j = 0; j < Pt::NS; j += 8)
-                *reinterpret_cast<uint4*>(op + sw128(part.kap, ((part.v0 & 63) + j) >> 3)) =
-                    make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]), pack_bf16(S[j + 4], S[j + 5]),
-                               pack_bf16(S[j + 6], S[j + 7]));
+            for (int j = 0; j < Pt::NS; j += 8) {
+                const uint4 hi = make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]),
+                                            pack_bf16(S[j + 4], S[j + 5]), pack_bf16(S[j + 6], S[j + 7]));
+                const uint32_t at = sw128(part.kap, ((part.v0 & 63) + j) >> 3);
+                *reinterpret_cast<uint4*>(op + at) = hi;
+                if constexpr (SHORT) {
+                    auto rest = [&](uint32_t h, int e) {
+                        return pack_bf16(S[e] - bf16lo_to_f32(h), S[e + 1] - bf16hi_to_f32(h));
+                    };
+                    *reinterpret_cast<uint4*>(op - C::kOffS + C::kStage + at) =
+                        make_uint4(rest(hi.x, j), rest(hi.y, j + 2), rest(hi.z, j + 4), rest(hi.w, j + 6));
+                }
+            }
             warp_arrive(r_s);
             if (p.ckpt && part.kap < p.K) {   // [V/4][K][4]: a warp's rows are adjacent
                 float* ck = p.ckpt + ((size_t)bh * nchunks + c) * p.K * p.V;

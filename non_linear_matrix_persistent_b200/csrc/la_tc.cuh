@@ -135,8 +135,9 @@ __device__ __forceinline__ void la_tables(Tab* tab, const LaParams& p, const flo
 // scores' other half takes their low terms (hi + lo bf16 against the same rows of the
 // other operand): with few terms in a sum their roundings do not average out.
 // Relative errors of dk, dv, dq at T = 1: up to 4e-3 without, 1.7e-3 with, which
-// is the results' own rounding.  Time at 64 tokens, 128 pairs of 128 x 128,
-// against a sequence of 65: forward 12.3 and 11.9 us, backward 21.6 and 19.3.
+// is the results' own rounding.  Time, 16 pairs of 64 x 64 and of 128 x 128 at 32
+// tokens, against sequences of 65: forward 7.5 / 7.5 and 12.1 / 11.7 us, backward
+// 10.0 / 11.0 and 21.3 / 19.2.
 constexpr int kShort = 64;
 
 // The f inputs of chunk c for la_tables; 0 behind the last token.

@@ -216,18 +216,20 @@ def test_few_pairs_and_many(B, H, T, K, V):
 
 @pytest.mark.parametrize("T", [1, 2, 5, 33, 64])
 @pytest.mark.parametrize("K,V", [(16, 16), (64, 128), (128, 64), (128, 128), (64, 64)])
-def test_short_gradients_are_rounded_once(T, K, V):
-    """Up to 64 tokens no bf16 operand adds to the gradients' own rounding: half a step of bf16, 2^-9 of the value at
+def test_short_results_are_rounded_once(T, K, V):
+    """Up to 64 tokens no bf16 operand adds to the results' own rounding: half a step of bf16, 2^-9 of the value at
     its binade's top and 2^-8 at its bottom, plus 2^-15 of the sums of absolute values for the operands' second terms
     (2^-16 each, two of them in a product's path)."""
     a = api()
     x, logit = inputs(2, 3, T, K, V, G=1, gate="logit", seed=40 + T)
     args = (x["k"], x["v"], x["q"], x["f"])
-    _, _, ck = a.linear_attention(*args, x["S0"], want_ckpt=True, f_is_logit=logit)
+    y, _, ck = a.linear_attention(*args, x["S0"], want_ckpt=True, f_is_logit=logit)
     got = a.linear_attention_backward(*args, ck, x["dy"], x["dST"], f_is_logit=logit)
     want = ref.backward(*args, x["dy"], x["S0"], x["dST"], logit)
     bound = ref.backward(*args, x["dy"], x["S0"], x["dST"], logit, bound=True)
-    for n in ("dk", "dv", "dq"):
+    got["y"], want["y"] = y, ref.forward(*args, x["S0"], logit)[0]
+    bound["y"] = ref.forward(*args, x["S0"], logit, bound=True)[0]
+    for n in ("y", "dk", "dv", "dq"):
         err = (got[n].double() - want[n]).abs() - (2.0 ** -8 * want[n].abs() + 2.0 ** -15 * bound[n] + 1e-37)
         assert float(err.max()) <= 0, (n, float(err.max()))
 
