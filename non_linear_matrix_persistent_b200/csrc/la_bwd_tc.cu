@@ -307,12 +307,12 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                         mma_ss(C::kDV, d_tile + k + kmajor(ks, 128), d_op + X + (C::kG0 >> 4) + e * OP + ks * 128, id_vi,
                                e < (SHORT ? 1 : 0) || ks > 0, one);
             };
-            if (!(ok = la_wait_warp(b_full + stage_of(i) * 8, stage_phase(i), abort_flag, limit))) break;
+            if (!(ok = la_wait(b_full + stage_of(i) * 8, stage_phase(i), abort_flag, limit))) break;
             if (C::kEarly) {
-                if (i > 0 && !(ok = la_wait_warp(b_out, ph ^ 1, abort_flag, limit))) break;
+                if (i > 0 && !(ok = la_wait(b_out, ph ^ 1, abort_flag, limit))) break;
                 scores(i);
             }
-            if (!(ok = la_wait_warp(r_s, ph, abort_flag, limit))) break;
+            if (!(ok = la_wait(r_s, ph, abort_flag, limit))) break;
             tc_fence_after();
             if (!C::kEarly && C::kRoomy) scores(i);
             times_state(C::kDQ, dy, X);                     // dY Sᵀ
@@ -323,13 +323,13 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             mma_commit(b_in, one);
             if (!C::kRoomy) scores(i);
             if (!C::kRoomy) {
-                if (!(ok = la_wait_warp(r_g, ph, abort_flag, limit))) break;
+                if (!(ok = la_wait(r_g, ph, abort_flag, limit))) break;
                 tc_fence_after();
                 times_state(C::kDK, v, X);
                 mma_commit(b_g, one);
             }
             auto sum_for_G = [&]() -> bool {
-                if (!la_wait_warp(r_aq, ph, abort_flag, limit)) return false;
+                if (!la_wait(r_aq, ph, abort_flag, limit)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int x = 2; x >= 0; --x) {      // the terms of a q
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 mma_commit(b_dg, one);
                 return true;
             };
-            if (!(ok = la_wait_warp(r_p, ph, abort_flag, limit))) break;
+            if (!(ok = la_wait(r_p, ph, abort_flag, limit))) break;
             tc_fence_after();
             if (!C::kOwnDv) {
                 inter_dv();
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             for (int ks = 0; ks < 8; ++ks)      // over t: P'ᵀ and dP'ᵀ of 16 sinks over their 16 score columns
                 mma_ts(C::kDK, C::kP + ks * 16 + 8, d_mn + q + (SHORT ? ks & 3 : ks) * 128, id_dk, 1, one);
             if (!C::kOwnDv) {
-                if (!(ok = la_wait_warp(r_dv, ph, abort_flag, limit))) break;
+                if (!(ok = la_wait(r_dv, ph, abort_flag, limit))) break;
                 tc_fence_after();
             }
 #pragma unroll
@@ -410,16 +410,16 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             for (; i < n; ++i) {
                 prefetch(i + 1);
                 if (!C::kRoomy) {
-                    if (!(ok = la_wait(r_aq, i & 1, abort_flag, limit) &&
-                          la_wait(r_df + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
+                    if (!(ok = la_wait_lane(r_aq, i & 1, abort_flag, limit) &&
+                          la_wait_lane(r_df + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
                     if (i + 1 < n) load(i + 1, true, false);
-                    if (!(ok = la_wait(b_dg, i & 1, abort_flag, limit))) break;
+                    if (!(ok = la_wait_lane(b_dg, i & 1, abort_flag, limit))) break;
                     if (i + 1 < n) load(i + 1, false, true);
                     continue;
                 }
                 const int ph = i & 1, t = chunk_of(i) * kLaChunk;
                 const uint32_t base = sbase + stage_of(i) * C::kStage;
-                if (!(ok = la_wait(r_out, ph, abort_flag, limit))) break;
+                if (!(ok = la_wait_lane(r_out, ph, abort_flag, limit))) break;
                 if (!p.dkq_fp32)
                     for (int x = 0; x < KP / 64; ++x)
                         if (x * 64 < p.K) {
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 tma_store_commit();
                 tma_store_wait_read();
                 mbar_arrive(b_free);
-                if (!(ok = la_wait(r_df + ph * 8, (i >> 1) & 1, abort_flag, limit))) break;
+                if (!(ok = la_wait_lane(r_df + ph * 8, (i >> 1) & 1, abort_flag, limit))) break;
                 if (i + C::kStages < n) load(i + C::kStages, true, true);
             }
             if (!ok) {   // leave no copy in flight

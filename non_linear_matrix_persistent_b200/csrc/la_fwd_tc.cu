@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         };
         // P V, Q S (which waits for S) and the state's sum of a chunk in this order,
         // the next chunk's scores as soon as its tiles are there and their place is free
-        if (la_wait_warp(b_qk, 0, abort_flag, limit)) {
+        if (la_wait(b_qk, 0, abort_flag, limit)) {
             scores(0);
             for (int i = 0; i < n; ++i) {
                 const int ph = i & 1, s = stage_of(i), s1 = stage_of(i + 1);
@@ -266,8 +266,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 auto next_scores = [&](bool wait) -> bool {
                     if (next) return true;
                     if (wait) {
-                        if (C::kScores == 1 && !la_wait_warp(b_pv, ph, abort_flag, limit)) return false;
-                        if (!la_wait_warp(b_qk + s1 * 8, stage_phase(i + 1), abort_flag, limit)) return false;
+                        if (C::kScores == 1 && !la_wait(b_pv, ph, abort_flag, limit)) return false;
+                        if (!la_wait(b_qk + s1 * 8, stage_phase(i + 1), abort_flag, limit)) return false;
                     } else if (!__all_sync(~0u, (C::kScores == 2 || mbar_test_wait(b_pv, ph)) &&
                                                     mbar_test_wait(b_qk + s1 * 8, stage_phase(i + 1)))) {
                         return true;
@@ -276,14 +276,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     next = true;
                     return true;
                 };
-                if (!la_wait_warp(b_v + s * 8, stage_phase(i), abort_flag, limit)) break;
-                if (!la_wait_warp(r_p, ph, abort_flag, limit)) break;
+                if (!la_wait(b_v + s * 8, stage_phase(i), abort_flag, limit)) break;
+                if (!la_wait(r_p, ph, abort_flag, limit)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)   // P: 16 columns of bf16 pairs at the start of each block's 32
                     mma_ts(C::kPV, (i % C::kScores) * 128 + (ks >> 1) * 32 + (ks & 1) * 8,
                            d_mn + v + (SHORT ? ks & 3 : ks) * 128, id_v, ks > 0, one);
-                if (!la_wait_warp(r_s, ph, abort_flag, limit)) break;
+                if (!la_wait(r_s, ph, abort_flag, limit)) break;
                 tc_fence_after();
                 if constexpr (SHORT) {
 #pragma unroll
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 mma_commit(b_pv, one);
                 // (of two score matrices the other is free since r_s: y of the chunk before had been read)
                 if (C::kScores == 2) next_scores(false);
-                if (!la_wait_warp(r_k, ph, abort_flag, limit)) break;
+                if (!la_wait(r_k, ph, abort_flag, limit)) break;
                 tc_fence_after();
                 if (C::kScores == 1) next_scores(false);
                 if (C::kInPlace) {
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             bool ok = true;
             for (int i = 0; i < n; ++i) {
                 // the stage is free: its products are done, y has been staged
-                if (!(ok = la_wait(r_y + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
+                if (!(ok = la_wait_lane(r_y + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
                 if (C::kStageY) {
 #pragma unroll
                     for (int x = 0; x < VP / 64; ++x)
@@ -616,8 +616,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const Desc d_mn = sw128_desc(sbase, kTileBytes);
         const uint32_t one = lane == 0;
         for (int i = 0; i < n; ++i) {
-            if (!la_wait_warp(b_full + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) break;
-            if (!la_wait_warp(r_k + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) break;
+            if (!la_wait(b_full + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) break;
+            if (!la_wait(r_k + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) break;
             tc_fence_after();
             const uint32_t k = (i & 1) * (C::kStage >> 4), v = k + (C::kQ >> 4),
                            x = (C::kOffX + (i % C::kSets) * 3 * C::kTerm) >> 4, xs = C::kTerm >> 4;
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (n > 1) load(1);
             bool ok = true;
             for (int i = 0; i + 2 < n; ++i) {
-                if (!(ok = la_wait(b_ds + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
+                if (!(ok = la_wait_lane(b_ds + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit))) break;
                 load(i + 2);
             }
             if (!ok)

@@ -275,9 +275,38 @@ __device__ __forceinline__ bool la_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// Bounded mbarrier wait: false when it runs longer than the limit or another
-// thread of the CTA has given up.
+// Bounded mbarrier wait of a whole warp: false when it runs longer than the
+// limit or another thread of the CTA has given up.  The outcome is the warp's:
+// what follows it (tensor-memory accesses, shuffles, the way out) takes all 32
+// lanes, and lanes that answered for themselves could part between a phase that
+// completes and a limit that runs out.  Nor does a barrier move on by two phases
+// while some lanes see the first: the next one waits for this warp.  The vote
+// also tells the compiler that the outcome is uniform, so that what the issuing
+// warp computes stays in uniform registers, where the products take their
+// operands from.  (64 attempts in an asm loop and a vote behind them: 128 pairs
+// of 128 x 128 forward 164 against 154 us.)
 __device__ __forceinline__ bool la_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (int k = 1;; ++k) {
+        if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+        if ((k & 63) == 0) {
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            const bool late = t - t0 > limit_ns;
+            if (__any_sync(~0u, late || *abort_flag)) {
+                if (late) {
+                    *abort_flag = 1;
+                    atomicOr(&g_la_status, 1u);
+                }
+                __syncwarp();
+                return false;
+            }
+        }
+    }
+}
+// The same for a single lane, which the rest of its warp awaits at a __syncwarp.
+__device__ __forceinline__ bool la_wait_lane(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                             uint64_t limit_ns) {
     uint64_t t0 = 0;
     for (int k = 1;; ++k) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -290,43 +319,6 @@ __device__ __forceinline__ bool la_wait(uint32_t bar, uint32_t parity, volatile 
                 atomicOr(&g_la_status, 1u);
                 return false;
             }
-        }
-    }
-}
-// The same for the warp that issues the products, with an outcome that the
-// compiler knows to be the warp's: the attempts are one asm loop and the
-// answers are voted on, so that everything it computes stays in uniform
-// registers, where the products take their operands from.
-__device__ __forceinline__ bool la_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                             uint64_t limit_ns) {
-    uint64_t t0 = 0;
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-            "mov.u32 n, 64;\n\t"
-            "LA_TRY_%=:\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "@p bra LA_DONE_%=;\n\t"
-            "sub.u32 n, n, 1;\n\t"
-            "setp.ne.u32 q, n, 0;\n\t"
-            "@q bra LA_TRY_%=;\n\t"
-            "LA_DONE_%=:\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (__all_sync(~0u, ok)) return true;
-        const uint64_t t = globaltimer_ns();
-        if (t0 == 0) t0 = t;
-        const bool late = t - t0 > limit_ns;
-        if (__any_sync(~0u, late || *abort_flag)) {
-            if (late) {
-                *abort_flag = 1;
-                atomicOr(&g_la_status, 1u);
-            }
-            __syncwarp();
-            return false;
         }
     }
 }
