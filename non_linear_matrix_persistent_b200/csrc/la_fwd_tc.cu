@@ -14,10 +14,11 @@
 // state's sum -> S form a chain over the chunks; P of the next chunk is formed
 // while the sum of this one is computed.
 //
-// Rounding: the masked scores and the copy of S that multiplies Q are bf16
-// operands, in two terms up to kShort tokens (each term of y passes through exactly one of them, and y is
-// rounded to bf16 itself); b_s k_s enters as three bf16 terms, so the state
-// keeps fp32 accuracy over any number of chunks.
+// Rounding: the masked scores and the copy of S that multiplies Q enter in two
+// bf16 terms each (2^-16 of them is left out; each term of y passes through
+// exactly one of them), so what rounds y is its own bf16: relative error 1.7e-3
+// of the whole, against 2.3e-3 with one term each.  b_s k_s enters as three
+// terms, so the state keeps fp32 accuracy over any number of chunks.
 //
 // Decays without an exponential per score: for a row t and a block of 32
 // columns, D_ts = 2^(L_t - L_e)·2^(L_e - L_s) with e the block's last token.
@@ -26,12 +27,12 @@
 // fp32's range unless the block decays by more than 2^-90: such chunks take one
 // exponential per score there.
 //
-// Measured: 128 pairs of 64 x 64 over 2048 tokens 47 us (137 MB: 21.3 us at the
-// copy rate of 6.45 TB/s), of 128 x 128 over 4096 tokens 145 us (547 MB: 84.9
-// us).  Neither HBM (30 to 60%) nor the tensor pipe (25%) nor issue (35 to 39%)
-// is full: a chunk's waits from product to elementwise work and back (2.4 and
-// 4.1 us a chunk) bound it, with one CTA an SM (shared and tensor memory) and
-// 128 of the 148 SMs.
+// Measured: 128 pairs of 64 x 64 over 2048 tokens 56 us (137 MB: 21.3 us at the
+// copy rate of 6.45 TB/s), of 128 x 128 over 4096 tokens 177 us (547 MB: 84.9
+// us); the second terms are 8 and 30 us of these.  Neither HBM nor the tensor pipe
+// nor issue is full: a chunk's waits from product to elementwise work and back
+// (2.9 and 5.1 us a chunk) bound it, with one CTA an SM (shared and tensor memory)
+// and 128 of the 148 SMs.
 #include <mutex>
 
 #include "kernels.h"
@@ -70,9 +71,9 @@ struct Maps {
 
 constexpr int kNW = 16, kFwdThreads = (kNW + 3) * 32;   // compute warps; one each for products, copies, decays
 
-// Three bf16 terms of eight scaled values of a tile's row, to three places.
-__device__ __forceinline__ void put_scaled(const uint8_t* src, uint8_t* d0, uint8_t* d1, uint8_t* d2, float w) {
-    const uint4 x = *reinterpret_cast<const uint4*>(src);
+// Three bf16 terms of eight scaled values: two to their places, the third
+// returned, or all three to their places.
+__device__ __forceinline__ uint4 put_scaled(uint4 x, uint8_t* d0, uint8_t* d1, float w) {
     uint4 hi, mid, lo;
     split3(w * bf16lo_to_f32(x.x), w * bf16hi_to_f32(x.x), hi.x, mid.x, lo.x);
     split3(w * bf16lo_to_f32(x.y), w * bf16hi_to_f32(x.y), hi.y, mid.y, lo.y);
@@ -80,7 +81,10 @@ __device__ __forceinline__ void put_scaled(const uint8_t* src, uint8_t* d0, uint
     split3(w * bf16lo_to_f32(x.w), w * bf16hi_to_f32(x.w), hi.w, mid.w, lo.w);
     *reinterpret_cast<uint4*>(d0) = hi;
     *reinterpret_cast<uint4*>(d1) = mid;
-    *reinterpret_cast<uint4*>(d2) = lo;
+    return lo;
+}
+__device__ __forceinline__ void put_scaled(uint4 x, uint8_t* d0, uint8_t* d1, uint8_t* d2, float w) {
+    *reinterpret_cast<uint4*>(d2) = put_scaled(x, d0, d1, w);
 }
 
 // A warp's writes are done (shared memory for the products, tensor memory):
@@ -179,17 +183,23 @@ struct Cfg {
     static constexpr bool kScaleV = VP < KP;                    // the narrower side carries the decays
     static constexpr int kTerm = kScaleV ? kV : kQ;
     // 128 x 128 has no room for the scaled side's three terms: they go over the
-    // k tile, the q tile and the state operand, once Q S is done
+    // k tile, the q tile and the state operand, once Q S is done.  The state's low
+    // term goes over the k tile before that, whose values wait in registers.
     static constexpr bool kInPlace = KP * VP == 128 * 128;
+    // 128 x 64 has room for all but the state's low term: it shares its place
+    // with the scaled side's third
+    static constexpr bool kShareLo = KP == 128 && VP == 64;
     static constexpr bool kStageY = !kInPlace && VP <= KP;      // y by TMA, over the q tile; else from registers
     static constexpr int kOffS = kStages * kStage;              // bf16 state operand [KP][VP]
     static constexpr int kOffX = kOffS + KP * VP * 2;           // the terms
-    static constexpr int kOffTab = kOffX + (kInPlace ? 0 : 3 * kTerm);
+    static constexpr int kOffLo = kOffX + (kShareLo ? 2 : 3) * kTerm;   // the state operand's low term
+    static constexpr int kOffTab = kInPlace ? kOffX : kOffLo + KP * VP * 2;
     static constexpr int kOffBar = kOffTab + 2 * (int)sizeof(LaTables);
     static constexpr int kBars = 22;
     static constexpr int kSmem = kOffBar + kBars * 8 + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory");
-    static_assert(KP * VP * 2 <= kStage && kStages >= 2, "the state's second term");
+    static_assert(!kInPlace || KP * VP * 2 <= kQ, "the state's low term over the k tile");
+    static_assert(!kShareLo || KP * VP * 2 <= kTerm, "the state's low term over the third of the scaled side");
     // tensor memory: scores (two of them where they fit: the next chunk's are
     // computed early), P·V, Q·S, the state's sum
     static constexpr int kScores = VP == 64 ? 2 : 1;
@@ -198,7 +208,7 @@ struct Cfg {
     static constexpr int NY = VP / 4;                           // columns of y per thread
 };
 
-template <int KP, int VP, bool SHORT>   // SHORT: up to kShort tokens
+template <int KP, int VP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     m2rnn_la_fwd_tc_kernel(const LaParams p, const __grid_constant__ Maps maps) {
     using C = Cfg<KP, VP>;
@@ -217,14 +227,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     // b_qk, b_v: one per stage; pairs of barriers serve chunks in turn, where one side may be a chunk ahead
     const uint32_t b_qk = bar(0), b_v = bar(3), b_sc = bar(6), b_tab = bar(8), t_free = bar(10), r_y = bar(12),
-                   r_p = bar(14), r_s = bar(15), r_k = bar(16), b_pv = bar(17), b_ds = bar(18), b_drain = bar(19);
+                   r_p = bar(14), r_s = bar(15), r_k = bar(16), b_pv = bar(17), b_ds = bar(18), b_drain = bar(19),
+                   r_raw = bar(20);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint64_t limit = p.wait_limit_ns;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 20; ++i) mbar_init(bar(i), 1);
-        for (uint32_t b : {t_free, t_free + 8, r_y, r_y + 8, r_p, r_s, r_k}) mbar_init(b, kNW);
+        for (int i = 0; i < 21; ++i) mbar_init(bar(i), 1);
+        for (uint32_t b : {t_free, t_free + 8, r_y, r_y + 8, r_p, r_s, r_k, r_raw}) mbar_init(b, kNW);
         *abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -242,8 +253,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // ------------------------------------------------------ products
         constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, 0, 0), id_v = idesc_bf16_f32(128, VP, 0, 1);
         const Desc d_tile = sw128_desc(sbase, 16), d_mn = sw128_desc(sbase, kTileBytes),
-                       d_s = sw128_desc(sbase + C::kOffS, KP * 128),
-                       d_s_lo = sw128_desc(sbase + C::kStage, KP * 128);   // SHORT: the second stage has no tiles
+                       d_op = sw128_desc(sbase, KP * 128);   // the state operand's terms
         constexpr uint32_t X = C::kOffX >> 4, XS = C::kTerm >> 4;
         auto tile = [](int ks) { return (uint32_t)((ks >> 2) * (kTileBytes >> 4) + (ks & 3) * 2); };
         const uint32_t one = lane == 0;
@@ -280,19 +290,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (!la_wait(r_p, ph, abort_flag, limit)) break;
                 tc_fence_after();
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)   // P: 16 columns of bf16 pairs at the start of each block's 32
-                    mma_ts(C::kPV, (i % C::kScores) * 128 + (ks >> 1) * 32 + (ks & 1) * 8,
-                           d_mn + v + (SHORT ? ks & 3 : ks) * 128, id_v, ks > 0, one);
+                for (int x = 1; x >= 0; --x)         // the low terms first
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)   // P: of each block's 32 columns 16 of high terms (bf16 pairs), 16 of low ones
+                        mma_ts(C::kPV, (i % C::kScores) * 128 + (ks >> 1) * 32 + x * 16 + (ks & 1) * 8, d_mn + v + ks * 128,
+                               id_v, x < 1 || ks > 0, one);
                 if (!la_wait(r_s, ph, abort_flag, limit)) break;
                 tc_fence_after();
-                if constexpr (SHORT) {
+#pragma unroll
+                for (int x = 1; x >= 0; --x) {
+                    const uint32_t op = x == 0 ? C::kOffS >> 4 : C::kInPlace ? k : C::kOffLo >> 4;
 #pragma unroll
                     for (int ks = 0; ks < KP / 16; ++ks)
-                        mma_ss(C::kQS, d_tile + q + tile(ks), d_s_lo + ks * 128, id_v, ks > 0, one);
+                        mma_ss(C::kQS, d_tile + q + tile(ks), d_op + op + ks * 128, id_v, x < 1 || ks > 0, one);
                 }
-#pragma unroll
-                for (int ks = 0; ks < KP / 16; ++ks)
-                    mma_ss(C::kQS, d_tile + q + tile(ks), d_s + ks * 128, id_v, SHORT || ks > 0, one);
                 mma_commit(b_pv, one);
                 // (of two score matrices the other is free since r_s: y of the chunk before had been read)
                 if (C::kScores == 2) next_scores(false);
@@ -387,32 +398,40 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                   : p.S0     ? p.S0 + (size_t)bh * p.K * p.V
                              : nullptr,
                   p.K, p.V, S);
-        auto put_operand = [&](int c) {   // S before chunk c: its bf16 copy for Q·S, the checkpoint
+        // S before chunk i of the walk: its two bf16 terms for Q·S, the checkpoint
+        auto put_operand = [&](int i) -> bool {
+            if (C::kInPlace && !la_wait(r_raw, i & 1, abort_flag, limit)) return false;   // every k is in registers
             uint8_t* op = smem + C::kOffS + (part.v0 >> 6) * (KP * 128);
+            uint8_t* lo = smem + (C::kInPlace ? stage_of(i) * C::kStage + C::kQ : C::kOffLo) + (part.v0 >> 6) * (KP * 128);
 #pragma unroll
             for (int j = 0; j < Pt::NS; j += 8) {
-                const uint4 hi = make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]),
-                                            pack_bf16(S[j + 4], S[j + 5]), pack_bf16(S[j + 6], S[j + 7]));
+                uint4 hi, rest;
+                split2(S[j], S[j + 1], hi.x, rest.x);
+                split2(S[j + 2], S[j + 3], hi.y, rest.y);
+                split2(S[j + 4], S[j + 5], hi.z, rest.z);
+                split2(S[j + 6], S[j + 7], hi.w, rest.w);
                 const uint32_t at = sw128(part.kap, ((part.v0 & 63) + j) >> 3);
                 *reinterpret_cast<uint4*>(op + at) = hi;
-                if constexpr (SHORT) {
-                    auto rest = [&](uint32_t h, int e) {
-                        return pack_bf16(S[e] - bf16lo_to_f32(h), S[e + 1] - bf16hi_to_f32(h));
-                    };
-                    *reinterpret_cast<uint4*>(op - C::kOffS + C::kStage + at) =
-                        make_uint4(rest(hi.x, j), rest(hi.y, j + 2), rest(hi.z, j + 4), rest(hi.w, j + 6));
-                }
+                *reinterpret_cast<uint4*>(lo + at) = rest;
             }
             warp_arrive(r_s);
             if (p.ckpt && part.kap < p.K) {   // [V/4][K][4]: a warp's rows are adjacent
-                float* ck = p.ckpt + ((size_t)bh * nchunks + c) * p.K * p.V;
+                float* ck = p.ckpt + ((size_t)bh * nchunks + chunk_of(i)) * p.K * p.V;
 #pragma unroll
                 for (int j = 0; j < Pt::NS; j += 4)
                     if (part.v0 + j < p.V)
                         *reinterpret_cast<float4*>(ck + ((size_t)((part.v0 + j) >> 2) * p.K + part.kap) * 4) =
                             make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
             }
+            return true;
         };
+        // the scaled side: its tile's place in a stage, 16-byte chunks of the row for this thread
+        constexpr int kOffTerm = C::kScaleV ? 2 * C::kQ : C::kQ, kCh = C::kTerm / 128 / 16 / 4;
+        auto pos_of = [&](int j) {
+            const int ch = wg * kCh + j;
+            return (uint32_t)((ch >> 3) * kTileBytes + sw128(row, ch & 7));
+        };
+        uint4 raw[C::kInPlace ? kCh : 1];        // of k, kept while the state's low term is in its tile
         float at = 0.f, w = 0.f, A = 0.f;        // of the chunk whose P has been formed last
         // P = masked, decayed scores in bf16, over the scores: row `row`, block wg of 32 columns
         auto put_P = [&](int i) -> bool {
@@ -425,14 +444,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (!la_wait(b_sc + (i & 1) * 8, (i >> 1) & 1, abort_flag, limit)) return false;
             tc_fence_after();
             const uint32_t at_ = mine + (i % C::kScores) * 128 + wg * 32;
-            uint32_t pk[16], lo[SHORT ? 16 : 1];
-            auto put = [&](int e, float x, float y) {   // columns 2e and 2e + 1
-                pk[e] = pack_bf16(x, y);
-                if constexpr (SHORT) lo[e] = pack_bf16(x - bf16lo_to_f32(pk[e]), y - bf16hi_to_f32(pk[e]));
-            };
-            if (wg > quarter || (SHORT && wg >= 2)) {
+            uint32_t pk[16], lo[16];
+            if (wg > quarter) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) put(e, 0.f, 0.f);
+                for (int e = 0; e < 16; ++e) pk[e] = lo[e] = 0;
             } else {
                 uint32_t sc[32];
                 tmem_ld<32>(at_, sc);
@@ -449,8 +464,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                                     make_float2(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1]))),
                                      y = __fmul2_rn(__fmul2_rn(r2, make_float2(cs.z, cs.w)),
                                                     make_float2(__uint_as_float(sc[e + 2]), __uint_as_float(sc[e + 3])));
-                        put(e / 2, e <= last ? x.x : 0.f, e + 1 <= last ? x.y : 0.f);
-                        put(e / 2 + 1, e + 2 <= last ? y.x : 0.f, e + 3 <= last ? y.y : 0.f);
+                        split2(e <= last ? x.x : 0.f, e + 1 <= last ? x.y : 0.f, pk[e / 2], lo[e / 2]);
+                        split2(e + 2 <= last ? y.x : 0.f, e + 3 <= last ? y.y : 0.f, pk[e / 2 + 1], lo[e / 2 + 1]);
                     }
                 } else {
 #pragma unroll
@@ -460,42 +475,54 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         auto d = [&](int o, float f, float w_) {
                             return e + o <= lane ? __uint_as_float(sc[e + o]) * ex2_approx((Ft - f) + (It - w_)) : 0.f;
                         };
-                        put(e / 2, d(0, fs.x, is.x), d(1, fs.y, is.y));
-                        put(e / 2 + 1, d(2, fs.z, is.z), d(3, fs.w, is.w));
+                        split2(d(0, fs.x, is.x), d(1, fs.y, is.y), pk[e / 2], lo[e / 2]);
+                        split2(d(2, fs.z, is.z), d(3, fs.w, is.w), pk[e / 2 + 1], lo[e / 2 + 1]);
                     }
                 }
             }
-            if (!SHORT || wg < 2) tmem_st16(at_, pk);
-            if constexpr (SHORT) {
-                if (wg < 2) tmem_st16(at_ + 64, lo);
-            }
+            tmem_st16(at_, pk);
+            tmem_st16(at_ + 16, lo);
             tc_wait_st();
             warp_arrive(r_p);
+            if constexpr (C::kInPlace) {   // (the scores, which read the k tile too, are done)
+                if (!la_wait(b_qk + stage_of(i) * 8, stage_phase(i), abort_flag, limit)) return false;
+#pragma unroll
+                for (int j = 0; j < kCh; ++j)
+                    raw[j] = *reinterpret_cast<const uint4*>(smem + stage_of(i) * C::kStage + kOffTerm + pos_of(j));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(r_raw);
+            }
             return true;
         };
         // the scaled side's terms of chunk i (their buffer is free: the last sum is done)
         auto put_terms = [&](int i) -> bool {
-            const uint32_t full = C::kScaleV ? b_v : b_qk;
-            if (!la_wait(full + stage_of(i) * 8, stage_phase(i), abort_flag, limit)) return false;
-            if (C::kInPlace && !la_wait(b_pv, i & 1, abort_flag, limit)) return false;   // Q S has read q and S
             uint8_t* stage = smem + stage_of(i) * C::kStage;
-            constexpr int kCh = C::kTerm / 128 / 16 / 4;         // 16-byte chunks of the row for this thread
+            if constexpr (C::kInPlace) {
+                if (!la_wait(b_pv, i & 1, abort_flag, limit)) return false;   // Q S has read q and S
 #pragma unroll
-            for (int j = 0; j < kCh; ++j) {
-                const int ch = wg * kCh + j;
-                const uint32_t pos = (ch >> 3) * kTileBytes + sw128(row, ch & 7);
-                uint8_t* src = stage + (C::kScaleV ? 2 * C::kQ : C::kQ) + pos;
-                uint8_t* X = smem + C::kOffX + pos;
-                if (C::kInPlace) put_scaled(src, src, stage + pos, smem + C::kOffS + pos, w);
-                else put_scaled(src, X, X + C::kTerm, X + 2 * C::kTerm, w);
+                for (int j = 0; j < kCh; ++j) {
+                    const uint32_t pos = pos_of(j);
+                    put_scaled(raw[j], stage + kOffTerm + pos, stage + pos, smem + C::kOffS + pos, w);
+                }
+            } else {
+                if (!la_wait((C::kScaleV ? b_v : b_qk) + stage_of(i) * 8, stage_phase(i), abort_flag, limit)) return false;
+                uint8_t* X = smem + C::kOffX;
+                uint4 third[kCh];
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) {
+                    const uint32_t pos = pos_of(j);
+                    third[j] = put_scaled(*reinterpret_cast<const uint4*>(stage + kOffTerm + pos), X + pos, X + C::kTerm + pos, w);
+                }
+                if (C::kShareLo && !la_wait(b_pv, i & 1, abort_flag, limit)) return false;   // Q S has read the low term
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) *reinterpret_cast<uint4*>(X + 2 * C::kTerm + pos_of(j)) = third[j];
             }
             warp_arrive(r_k);
             if (lane == 0) mbar_arrive(t_free + (i & 1) * 8);    // this chunk's tables are no longer read
             return true;
         };
         bool ok = true;
-        put_operand(c0);
-        ok = put_P(0) && put_terms(0);
+        ok = (C::kInPlace || put_operand(0)) && put_P(0) && (!C::kInPlace || put_operand(0)) && put_terms(0);
         for (int i = 0; ok && i < n; ++i) {
             const int ph = i & 1;
             const float at_i = at, A_i = A;
@@ -538,8 +565,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             part.add(mine + C::kDS, A_i, S);
             warp_arrive(r_y + (i & 1) * 8);
             if (i + 1 < n) {
-                put_operand(chunk_of(i + 1));
-                ok = put_terms(i + 1);
+                ok = put_operand(i + 1) && put_terms(i + 1);
             }
         }
         if (p.ST && c0 + n == nchunks) part.store(p.ST + (size_t)bh * p.K * p.V, p.K, p.V, S);
@@ -686,7 +712,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int e = 0; e < kCh; ++e) {
                 const int ch = wg * kCh + e;
                 const uint32_t pos = (ch >> 3) * kTileBytes + sw128(row, ch & 7);
-                put_scaled(src + pos, dst + pos, dst + pos + C::kTerm, dst + pos + 2 * C::kTerm, w);
+                put_scaled(*reinterpret_cast<const uint4*>(src + pos), dst + pos, dst + pos + C::kTerm, dst + pos + 2 * C::kTerm, w);
             }
             warp_arrive(r_k + (i & 1) * 8);
         }
@@ -740,7 +766,7 @@ __global__ void m2rnn_la_seg_scan_kernel(const LaParams p, const float* seg_deca
 template <int KP, int VP>
 struct FwdKernel {
     static cudaError_t launch(const LaParams& p, const Maps& m, float*, cudaStream_t s) {
-        auto kern = p.T <= kShort ? m2rnn_la_fwd_tc_kernel<KP, VP, true> : m2rnn_la_fwd_tc_kernel<KP, VP, false>;
+        auto kern = m2rnn_la_fwd_tc_kernel<KP, VP>;
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<KP, VP>::kSmem);
         if (e != cudaSuccess) return e;
         kern<<<p.B * p.H * p.segs, kFwdThreads, Cfg<KP, VP>::kSmem, s>>>(p, m);

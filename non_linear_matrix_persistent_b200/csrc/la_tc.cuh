@@ -226,6 +226,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+// x = hi + lo to 2^-16 of x: lo is what hi left over (exact in fp32), rounded to
+// nearest.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16(x0, x1);
+    lo = pack_bf16(x0 - bf16lo_to_f32(hi), x1 - bf16hi_to_f32(hi));
+}
 // x = hi + mid + lo to about 2^-26 of x: each term is what the bf16 before it
 // left over (exact in fp32), rounded to nearest.
 __device__ __forceinline__ void split3(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
