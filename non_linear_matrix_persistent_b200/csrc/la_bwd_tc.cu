@@ -8,8 +8,8 @@
 //   dv_s = b_s (K G)_s   + (P'ᵀ dY)_s
 //   G'   = a_end G + Σ_t (a_t q_t) dy_tᵀ
 // The scores are computed transposed (lane = source s, column = sink t): P'ᵀ
-// and dP'ᵀ then stay in tensor memory as the A operands of dv and dk, and only
-// dP' also goes to shared memory, for dq.
+// then stays in tensor memory as the A operand of dv, and dP'ᵀ goes to shared
+// memory, for dq and dk (for K = 64 dk's copy stays in tensor memory too).
 //
 // The gate's gradient.  f_u df_u is the sum over all paths from a source
 // s < u (a token, or S) to a sink t >= u (a token, or G):
@@ -21,21 +21,22 @@
 // below 2^-100 act as 2^-100 there, which keeps that quotient; every other
 // gradient has the gate itself.
 //
-// Rounding: P', dP' and the copy of G that gives dv are bf16 operands (two terms
-// of them up to kShort tokens); S and G
-// enter the products that df also reads, and a_t q_t enters G, as three bf16
-// terms (fp32 accuracy).
+// Rounding: P', dP' and the copy of G that gives dv enter in two bf16 terms each
+// (2^-16 of them is left out), so what rounds dq, dk and dv is their own bf16:
+// relative error 1.7e-3, against 2.4e-3 with one term each.  S and G enter the
+// products that df also reads, and a_t q_t enters G, as three terms (fp32
+// accuracy).
 //
 // One CTA per (b, h) or time segment of it.  16 warps compute (thread = token
 // or state row = tensor-memory lane, the four warpgroups sharing the columns),
 // one issues the products, one moves tiles, one computes decays and df.
 //
-// Measured: 128 pairs of 64 x 64 over 2048 tokens 122 us (the reads of k, v, q,
+// Measured: 128 pairs of 64 x 64 over 2048 tokens 139 us (the reads of k, v, q,
 // dy and the checkpoints and the writes of dk, dv, dq take 42.6 us at the copy
-// rate of 6.45 TB/s), of 128 x 128 over 4096 tokens 459 us (191 us).  As in the
-// forward a chunk's chain of waits bounds it, 7.6 and 14.3 us a chunk (tensor
-// pipe 21 and 26%, issue 35 and 33%, HBM 21 and 25%), and 96 registers a thread,
-// of which 128 x 128 spills 71: one CTA an SM, 19 warps.
+// rate of 6.45 TB/s), of 128 x 128 over 4096 tokens 530 us (191 us); the second
+// terms are 16 and 62 us of these.  As in the forward a chunk's chain of waits
+// bounds it, 8.7 and 16.5 us a chunk, and 96 registers a thread, of which
+// 128 x 128 spills 63: one CTA an SM, 19 warps.
 #include "kernels.h"
 #include "la_tc.cuh"
 
@@ -51,9 +52,8 @@ struct DfScratch {
     float alpha[4][128], beta[4][128];   // parts of the dot products, by warpgroup
     float total[4][128];                 // by source: its paths to each block of 32 sinks
     float cut[4][128];                   // by gate u: paths from each block of sources to sinks u.. of u's block
-    float gamma[16];                     // parts of a_end <S, G>, by warp
 };
-static_assert(sizeof(DfScratch) <= kTileBytes, "scratch");
+static_assert(sizeof(DfScratch) <= kTileBytes / 2, "half a tile");
 
 // Two schedules.  Up to 64 x 128 and 128 x 64 (kRoomy) the terms of S, of G
 // and of a q have shared memory of their own: both states' products run while
@@ -62,6 +62,10 @@ static_assert(sizeof(DfScratch) <= kTileBytes, "scratch");
 // buffers and the place of dP'; dq, dk and dv go to global memory from
 // registers, so that the next tiles are fetched as soon as a q has been formed
 // and nothing waits for staged outputs to leave.
+//
+// dP'ᵀ [s][t] takes two tiles a term.  Sinks before their source have none, so of
+// the low term's first tile (t < 64) the rows s >= 64 are neither written nor
+// used: the products that would read them leave those lanes of the result alone.
 template <int KP, int VP>
 struct BCfg {
     static constexpr int NW = 16, kThreads = (NW + 3) * 32;
@@ -69,20 +73,36 @@ struct BCfg {
     static constexpr int kStages = KP == 64 && VP == 64 ? 2 : 1;
     static constexpr bool kRoomy = KP * VP < 128 * 128;
     static constexpr int kOp = KP * VP * 2;                     // one bf16 term of a state
-    static constexpr int kOffX = kStages * kStage;              // the states' terms
+    // 64 x 64: the low term of dP'ᵀ waits in tensor memory until the states' products
+    // are done and then goes to 8 KB of its own (t < 64) and the v tile
+    static constexpr bool kLateLo = KP == 64 && VP == 64;
+    static constexpr int kOffStage = kLateLo ? kTileBytes / 2 : 0;
+    static constexpr int kOffX = kOffStage + kStages * kStage;  // the states' terms
     static constexpr int kX = (kRoomy ? 6 : 2) * kOp;
     static constexpr int kOffP = kOffX + kX;                    // dP'ᵀ [s][t], 32 KB
-    // df's scratch: its own place, or the v tile once V Gᵀ is done
+    // df's scratch: its own place, or the v tile once V Gᵀ is done (for 128 x 128
+    // the quarter of it that the low term of dP' does not use)
     static constexpr bool kOwnScratch = KP == 64 && VP == 64;
+    static constexpr int kAtScratch = kRoomy ? 0 : kTileBytes / 2;
     static constexpr int kOffScratch = kOffP + 2 * kTileBytes;
     static constexpr int kOffTab = kOffScratch + (kOwnScratch ? (int)sizeof(DfScratch) : 0);
     static constexpr int kOffBar = kOffTab + (int)sizeof(LaTablesZ);
     static constexpr int kBars = 19;
-    static constexpr int kSmem = kOffBar + kBars * 8 + 16;
+    static constexpr int kOffGamma = kOffBar + kBars * 8 + 8;   // parts of a_end <S, G>, by warp
+    static constexpr int kSmem = kOffGamma + NW * 4;
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(kX >= (kRoomy ? 3 : 2) * kQ && kOp <= 2 * kTileBytes, "terms of a q; third terms");
     // where the terms of G go, from kOffX; without room the third terms are at kOffP
     static constexpr int kG0 = kRoomy ? 3 * kOp : 0;
+    // the low term of dP'ᵀ of the other shapes: over state terms that are no longer
+    // read (those of S, or where G's are done too and those of a q come early, of G),
+    // or the v tile.  Where it shares its place with a q, a q waits for the outputs'
+    // products (64 x 64 so: 152 us for the training shape below, not 139).
+    static constexpr bool kEarlyAq = KP == 64;
+    static constexpr int kOffLo = kRoomy ? kOffX + (kEarlyAq ? kG0 : 0) : 2 * kQ;
+    static_assert(!kEarlyAq || kLateLo || (kG0 >= 3 * kQ && kX - kG0 >= 2 * kTileBytes), "a q beside the low term of dP'");
+    static_assert(kRoomy ? kLateLo || kX >= 2 * kTileBytes : kV >= 2 * kTileBytes && kStages == 1, "room for the low term of dP'");
+    static_assert(!kRoomy || KP == 64 || kG0 >= 2 * kTileBytes, "G's terms are still read");
     // Tensor memory: the two score matrices, dq, dk, dv and the sum for G.
     // Where the last two do not fit beside the others they go over dY·Vᵀ once
     // the scores have been read (for 128 x 128 the sum for G over dq instead).
@@ -117,8 +137,9 @@ __device__ __forceinline__ float column_sums(float (&r)[N]) {
 }
 
 // One source's block of 32 sinks: from the raw scores (lane = source s, 32
-// columns of sinks t0..t0+31) P'ᵀ and dP'ᵀ in bf16, back over the scores in
-// tensor memory and, dP'ᵀ, to its place `dp(column)` in shared memory; returns
+// columns of sinks t0..t0+31) P'ᵀ and dP'ᵀ in two bf16 terms, back over the scores
+// in tensor memory (8 columns of high terms, 8 of low ones for every 16 sinks;
+// dP'ᵀ where TS) and, dP'ᵀ, to `dp(column)` and, where LO, `dp_lo(column)` in shared memory; returns
 // the source's sum of paths into the block, and leaves in cut[] by gate u the
 // sums over the warp's sources before u of the paths to sinks u.. of the block.
 // The decay is r·c[t].  `first`: the lane in the source's own block (sinks t >=
@@ -127,15 +148,14 @@ __device__ __forceinline__ float column_sums(float (&r)[N]) {
 // an exponential each.  (One body for diagonal and other blocks: the two would
 // not fit the instruction cache together.)
 // PW: columns at a time, 16 or, where registers are short, 8.
-// SHORT: the low terms too, 64 columns on in tensor memory and to dp_lo(column).
-template <bool ZERO, int PW, bool SHORT, class Place, class PlaceLo>
+template <bool ZERO, int PW, bool TS, bool LO, class Place, class PlaceLo>
 __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const LaTablesZ* tab, int t0, float Fs, float Is,
                                              float Zs, float r, int first, float* cut, Place dp, PlaceLo dp_lo) {
     const int lane = threadIdx.x & 31;
     float run = 0.f;
 #pragma unroll
     for (int h = 16; h >= 0; h -= 16) {
-        uint32_t pp[8], pd[8], ppl[SHORT ? 8 : 1], pdl[SHORT ? 8 : 1];
+        uint32_t pp[8], ppl[8], pd[8], pdl[8];
 #pragma unroll
         for (int g = 16 - PW; g >= 0; g -= PW) {
             uint32_t x[PW], y[PW];
@@ -181,36 +201,33 @@ __device__ __forceinline__ float score_block(uint32_t tp, uint32_t tdp, const La
                     PD = __fmul2_rn(P, Zd);
                     QD = __fmul2_rn(Q, Zd);
                 }
-                const uint32_t hp = pack_bf16(PD.x, PD.y), hd = pack_bf16(QD.x, QD.y);
-                pp[(g + e) / 2] = hp;
-                pd[(g + e) / 2] = hd;
-                if constexpr (SHORT) {
-                    ppl[(g + e) / 2] = pack_bf16(PD.x - bf16lo_to_f32(hp), PD.y - bf16hi_to_f32(hp));
-                    pdl[(g + e) / 2] = pack_bf16(QD.x - bf16lo_to_f32(hd), QD.y - bf16hi_to_f32(hd));
-                }
+                split2(PD.x, PD.y, pp[(g + e) / 2], ppl[(g + e) / 2]);
+                split2(QD.x, QD.y, pd[(g + e) / 2], pdl[(g + e) / 2]);
                 run += W.y;
                 R[e + 1] = h + g + e + 1 > first ? run : 0.f;   // sources strictly before the gate
                 run += W.x;
                 R[e] = h + g + e > first ? run : 0.f;
             }
+#pragma unroll
+            for (int e = 0; e < PW; e += 8) {
+                const int w = (g + e) / 2;
+                *reinterpret_cast<uint4*>(dp(t0 + h + g + e)) = make_uint4(pd[w], pd[w + 1], pd[w + 2], pd[w + 3]);
+                if (LO) *reinterpret_cast<uint4*>(dp_lo(t0 + h + g + e)) = make_uint4(pdl[w], pdl[w + 1], pdl[w + 2], pdl[w + 3]);
+            }
             const float c = column_sums(R);
             if (!(lane & (32 / PW - 1))) cut[t0 + h + g + lane / (32 / PW)] = c;
         }
         tmem_st_32x32b<8>(tp + h, pp);       // inside the half that has been read
-        tmem_st_32x32b<8>(tp + h + 8, pd);
-        *reinterpret_cast<uint4*>(dp(t0 + h)) = make_uint4(pd[0], pd[1], pd[2], pd[3]);
-        *reinterpret_cast<uint4*>(dp(t0 + h + 8)) = make_uint4(pd[4], pd[5], pd[6], pd[7]);
-        if constexpr (SHORT) {
-            tmem_st_32x32b<8>(tp + 64 + h, ppl);
-            tmem_st_32x32b<8>(tp + 64 + h + 8, pdl);
-            *reinterpret_cast<uint4*>(dp_lo(t0 + h)) = make_uint4(pdl[0], pdl[1], pdl[2], pdl[3]);
-            *reinterpret_cast<uint4*>(dp_lo(t0 + h + 8)) = make_uint4(pdl[4], pdl[5], pdl[6], pdl[7]);
+        tmem_st_32x32b<8>(tp + h + 8, ppl);
+        if constexpr (TS) {
+            tmem_st_32x32b<8>(tdp + h, pd);
+            tmem_st_32x32b<8>(tdp + h + 8, pdl);
         }
     }
     return run;
 }
 
-template <int KP, int VP, bool SHORT>   // SHORT: up to kShort tokens
+template <int KP, int VP>
 __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
     m2rnn_la_bwd_tc_kernel(const LaParams p, const __grid_constant__ BwdMaps maps) {
     using C = BCfg<KP, VP>;
@@ -233,6 +250,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                    r_df = bar(17);   // two, for chunks in turn: the copies may be a chunk behind df
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    float* gammas = reinterpret_cast<float*>(smem + C::kOffGamma);
     const uint64_t limit = p.wait_limit_ns;
 
     if (threadIdx.x == 0) {
@@ -278,7 +296,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             }
         };
         auto tiles = [&](int i, uint32_t& q, uint32_t& k, uint32_t& v, uint32_t& dy) {
-            q = stage_of(i) * (C::kStage >> 4);
+            q = (C::kOffStage + stage_of(i) * C::kStage) >> 4;
             k = q + (C::kQ >> 4);
             v = k + (C::kQ >> 4);
             dy = v + (C::kV >> 4);
@@ -299,13 +317,13 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             const int ph = i & 1;
             uint32_t q, k, v, dy;
             tiles(i, q, k, v, dy);
-            auto inter_dv = [&]() {   // K G with G in one term, or two
+            auto inter_dv = [&]() {   // K G with G's first two terms
 #pragma unroll
-                for (int e = SHORT ? 1 : 0; e >= 0; --e)
+                for (int e = 1; e >= 0; --e)
 #pragma unroll
                     for (int ks = 0; ks < KP / 16; ++ks)
                         mma_ss(C::kDV, d_tile + k + kmajor(ks, 128), d_op + X + (C::kG0 >> 4) + e * OP + ks * 128, id_vi,
-                               e < (SHORT ? 1 : 0) || ks > 0, one);
+                               e < 1 || ks > 0, one);
             };
             if (!(ok = la_wait(b_full + stage_of(i) * 8, stage_phase(i), abort_flag, limit))) break;
             if (C::kEarly) {
@@ -348,19 +366,35 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 inter_dv();
                 mma_commit(b_dv, one);
             }
+            // the low terms first.  dq: contraction over s, the rows of the dP'ᵀ and k tiles
+            const uint32_t lo = C::kOffLo >> 4;   // (the v tile has one stage where it takes the low term)
+            const Desc d_lo = C::kLateLo ? sw128_desc(sbase, C::kOffStage + stage_of(i) * C::kStage + 2 * C::kQ) : d_mn + lo;
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)      // contraction over s, the rows of the dP'ᵀ and k tiles
-                mma_ss(C::kDQ, d_mn + XP + ks * 128, d_mn + k + (SHORT ? ks & 3 : ks) * 128, id_dq, 1, one);
+            for (int ks = 0; ks < 8; ++ks) {
+                if (ks < 4) mma_ss(C::kDQ, d_lo + ks * 128, d_mn + k + ks * 128, id_dq, 1, one);
+                else mma_ss_half<true>(C::kDQ, d_lo + ks * 128, d_mn + k + ks * 128, id_dq, one);   // sinks t >= 64
+            }
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)      // over t: P'ᵀ and dP'ᵀ of 16 sinks over their 16 score columns
-                mma_ts(C::kDK, C::kP + ks * 16 + 8, d_mn + q + (SHORT ? ks & 3 : ks) * 128, id_dk, 1, one);
+            for (int ks = 0; ks < 8; ++ks) mma_ss(C::kDQ, d_mn + XP + ks * 128, d_mn + k + ks * 128, id_dq, 1, one);
+            // dk and dv: over t, 16 sinks at a time, A from tensor memory (8 columns each term) or the dP'ᵀ tiles
+#pragma unroll
+            for (int x = 1; x >= 0; --x)
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const Desc b = d_mn + q + ks * 128;
+                    if (KP == 64) mma_ts(C::kDK, C::kDP + ks * 16 + x * 8, b, id_dk, 1, one);
+                    else if (x == 0) mma_ss(C::kDK, d_tile + XP + kmajor(ks, 128), b, id_dk, 1, one);
+                    else if (ks >= 4) mma_ss(C::kDK, d_tile + lo + kmajor(ks, 128), b, id_dk, 1, one);
+                    else mma_ss_half<false>(C::kDK, d_tile + lo + kmajor(ks, 128), b, id_dk, one);   // sources s < 64
+                }
             if (!C::kOwnDv) {
                 if (!(ok = la_wait(r_dv, ph, abort_flag, limit))) break;
                 tc_fence_after();
             }
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                mma_ts(C::kDV, C::kP + ks * 16, d_mn + dy + (SHORT ? ks & 3 : ks) * 128, id_vi, 1, one);
+            for (int x = 1; x >= 0; --x)
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) mma_ts(C::kDV, C::kP + ks * 16 + x * 8, d_mn + dy + ks * 128, id_vi, 1, one);
             mma_commit(b_out, one);
             if (!(ok = sum_for_G())) break;
         }
@@ -377,7 +411,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 if (rest) started = i + 1;
                 if (dys) loaded = i + 1;
                 const int t = chunk_of(i) * kLaChunk;
-                const uint32_t base = sbase + stage_of(i) * C::kStage, full = b_full + stage_of(i) * 8;
+                const uint32_t base = sbase + C::kOffStage + stage_of(i) * C::kStage, full = b_full + stage_of(i) * 8;
                 if (C::kRoomy) {
                     mbar_arrive_expect_tx(full, C::kStage);
                 } else {
@@ -418,7 +452,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                     continue;
                 }
                 const int ph = i & 1, t = chunk_of(i) * kLaChunk;
-                const uint32_t base = sbase + stage_of(i) * C::kStage;
+                const uint32_t base = sbase + C::kOffStage + stage_of(i) * C::kStage;
                 if (!(ok = la_wait_lane(r_out, ph, abort_flag, limit))) break;
                 if (!p.dkq_fp32)
                     for (int x = 0; x < KP / 64; ++x)
@@ -454,7 +488,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             const int ph = i & 1, c = chunk_of(i);
             if (!la_wait(r_p, ph, abort_flag, limit)) break;
             const DfScratch* sc = reinterpret_cast<const DfScratch*>(
-                smem + (C::kOwnScratch ? C::kOffScratch : stage_of(i) * C::kStage + 2 * C::kQ));
+                smem + (C::kOwnScratch ? C::kOffScratch : C::kOffStage + stage_of(i) * C::kStage + 2 * C::kQ + C::kAtScratch));
             const int block = lane >> 3, t0 = lane * 4;
             float x[4] = {0.f, 0.f, 0.f, 0.f}, al[4], be[4], past[3][4];
 #pragma unroll
@@ -473,7 +507,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             }
             float gamma = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) gamma += sc->gamma[w];
+            for (int w = 0; w < NW; ++w) gamma += gammas[w];
             __syncwarp();
             if (lane == 0) mbar_arrive(r_df + ph * 8);
             // sums over sources before each token of this lane (exclusive)
@@ -616,7 +650,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
 
         for (int i = 0; i < n; ++i) {
             const int ph = i & 1, c = chunk_of(i);
-            uint8_t* stage = smem + stage_of(i) * C::kStage;
+            uint8_t* stage = smem + C::kOffStage + stage_of(i) * C::kStage;
             float gamma = gamma_next;
             if (kLoadEarly && i + 1 < n) load_S(chunk_of(i + 1));
             if (!la_wait(b_tab, ph, abort_flag, limit)) break;
@@ -671,7 +705,8 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                     tmem_st16(mylane + C::kDV + col, x);
                 }
             };
-            DfScratch* sc = reinterpret_cast<DfScratch*>(C::kOwnScratch ? smem + C::kOffScratch : stage + 2 * C::kQ);
+            DfScratch* sc = reinterpret_cast<DfScratch*>(C::kOwnScratch ? smem + C::kOffScratch
+                                                                        : stage + 2 * C::kQ + C::kAtScratch);
             auto scale_all = [&]() -> bool {
                 if (!la_wait(b_in, ph, abort_flag, limit)) return false;
                 tc_fence_after();
@@ -682,13 +717,13 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 if (C::kOwnDv) scale_dv();
                 sc->alpha[wg][row] = alpha;
                 sc->beta[wg][row] = beta;
-                if (lane == 0) sc->gamma[warp] = gamma;
+                if (lane == 0) gammas[warp] = gamma;
                 return true;
             };
             if (!C::kRoomy) {
                 if (!scale_all()) break;
             } else {
-                // the scratch and dP' may be written: df has been read, or V Gᵀ is done and dq has left
+                // the scratch and dP' may be written: df has been read, the states' products are done, dq has left
                 if (!C::kOwnScratch && !la_wait(b_in, ph, abort_flag, limit)) break;
                 if (C::kOwnScratch && i > 0 && !la_wait(r_df + (ph ^ 1) * 8, ((i - 1) >> 1) & 1, abort_flag, limit)) break;
                 if (!C::kOwnScratch && i > 0 && !la_wait(b_free, ph ^ 1, abort_flag, limit)) break;
@@ -716,20 +751,22 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             };
             // ---- P'ᵀ, dP'ᵀ and df's sums: source s = row, sinks of block wg
             float run = 0.f;
-            auto place_lo = [&](int col) { return dp + (col >> 6) * kTileBytes + sw128(row + 64, (col & 63) >> 3); };
-            if (SHORT && (wg >= 2 || quarter >= 2)) {
-                // behind the last token: these rows' results are not kept, these places hold the low terms
-            } else if (wg < quarter) {   // sinks before the source
+            auto place_lo = [&](int col) -> uint8_t* {
+                if constexpr (C::kLateLo) return (col < 64 ? smem : stage + 2 * C::kQ) + sw128(row, (col & 63) >> 3);
+                else return (C::kRoomy ? smem : stage) + C::kOffLo + tile_at(col);
+            };
+            const bool low = wg >= 2 || quarter < 2;   // the low term's rows s >= 64 of sinks t < 64 are not read
+            if (wg < quarter) {   // sinks before the source
                 const uint32_t z[16] = {};
 #pragma unroll
-                for (int l = 0; l < (SHORT ? 128 : 64); l += 64) {   // (and the low terms)
-                    tmem_st16(mylane + C::kP + l + wg * 32, z);
-                    tmem_st16(mylane + C::kP + l + wg * 32 + 16, z);
+                for (int e = 0; e < 32; e += 16) {
+                    tmem_st16(mylane + C::kP + wg * 32 + e, z);
+                    if (KP == 64) tmem_st16(mylane + C::kDP + wg * 32 + e, z);
                 }
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
                     *reinterpret_cast<uint4*>(dp + tile_at(wg * 32 + e)) = make_uint4(0, 0, 0, 0);
-                    if (SHORT) *reinterpret_cast<uint4*>(place_lo(wg * 32 + e)) = make_uint4(0, 0, 0, 0);
+                    if (!C::kLateLo && low) *reinterpret_cast<uint4*>(place_lo(wg * 32 + e)) = make_uint4(0, 0, 0, 0);
                 }
             } else {
                 const uint32_t tp = mylane + C::kP + wg * 32, tdp = mylane + C::kDP + wg * 32;
@@ -741,13 +778,24 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 const float r = ex2_approx((Fp - Ft) + (Ip - It));
                 constexpr int N = C::NS <= 16 ? 16 : 8;
                 if (Ze != 0.f || tab->steep != 0.f)
-                    run = score_block<true, N, SHORT>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place, place_lo);
+                    run = score_block<true, N, KP == 64, !C::kLateLo>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place, place_lo);
                 else
-                    run = score_block<false, N, SHORT>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place, place_lo);
+                    run = score_block<false, N, KP == 64, !C::kLateLo>(tp, tdp, tab, wg * 32, Ft, It, Zt, r, first, cut, place, place_lo);
             }
             sc->total[wg][row] = run;
             if (C::kRoomy && !scale_all()) break;
             tc_wait_st();
+            if (C::kLateLo && low) {
+#pragma unroll
+                for (int h = 0; h < 32; h += 16) {
+                    uint32_t x[8];
+                    tmem_ld<8>(mylane + C::kDP + wg * 32 + h + 8, x);
+                    tc_wait_ld();
+                    reg_fence(x);
+                    *reinterpret_cast<uint4*>(place_lo(wg * 32 + h)) = make_uint4(x[0], x[1], x[2], x[3]);
+                    *reinterpret_cast<uint4*>(place_lo(wg * 32 + h + 8)) = make_uint4(x[4], x[5], x[6], x[7]);
+                }
+            }
             arrive(r_p);
             if (!kLoadEarly && i + 1 < n) load_S(chunk_of(i + 1));
             if (!C::kOwnDv) {
@@ -757,9 +805,10 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                 tc_wait_st();
                 arrive(r_dv);
             }
-            if (C::kRoomy) put_aq();   // over the states' terms, whose products are done
+            if (C::kEarlyAq) put_aq();   // over the terms of S, whose products are done
             if (!la_wait(b_out, ph, abort_flag, limit)) break;
             tc_fence_after();
+            if (C::kRoomy && !C::kEarlyAq) put_aq();   // over the states' terms and the low term of dP'
             const int t = c * kLaChunk + row;
             // 16 columns of dq, dk or dv: the per-head parts of a shared q's or k's gradient, or packed
             auto take = [&](uint32_t col, uint32_t (&x)[16]) {
@@ -867,7 +916,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
 template <int KP, int VP>
 cudaError_t launch(const LaParams& p, const BwdMaps& m, cudaStream_t s) {
     using C = BCfg<KP, VP>;
-    auto kern = p.T <= kShort ? m2rnn_la_bwd_tc_kernel<KP, VP, true> : m2rnn_la_bwd_tc_kernel<KP, VP, false>;
+    auto kern = m2rnn_la_bwd_tc_kernel<KP, VP>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     kern<<<p.B * p.H * p.segs, C::kThreads, C::kSmem, s>>>(p, m);

@@ -131,15 +131,6 @@ __device__ __forceinline__ void la_tables(Tab* tab, const LaParams& p, const flo
         make_float4(ex2_approx(sign * ((fe - F[0]) + (we - I[0]))), ex2_approx(sign * ((fe - F[1]) + (we - I[1]))),
                     ex2_approx(sign * ((fe - F[2]) + (we - I[2]))), ex2_approx(sign * ((fe - F[3]) + (we - I[3]))));
 }
-// Up to kShort tokens a sequence fills half a tile at most, and the masked
-// scores' other half takes their low terms (hi + lo bf16 against the same rows of the
-// other operand): with few terms in a sum their roundings do not average out.
-// Relative errors of dk, dv, dq at T = 1: up to 4e-3 without, 1.7e-3 with, which
-// is the results' own rounding.  Time, 16 pairs of 64 x 64 and of 128 x 128 at 32
-// tokens, against sequences of 65: forward 7.5 / 7.5 and 12.1 / 11.7 us, backward
-// 10.0 / 11.0 and 21.3 / 19.2.
-constexpr int kShort = 64;
-
 // The f inputs of chunk c for la_tables; 0 behind the last token.
 __device__ __forceinline__ void la_load_f(const LaParams& p, int bh, int c, float (&x)[4]) {
     const int t = c * kLaChunk + (threadIdx.x & 31) * 4;
@@ -176,6 +167,20 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, Desc a, Desc b, uint32_t
         "setp.ne.b32 q, %7, 0;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
         "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+// The same, leaving 64 lanes of D as they are: the lower half, or the upper one.
+template <bool LOWER>
+__device__ __forceinline__ void mma_ss_half(uint32_t d_tmem, Desc a, Desc b, uint32_t idesc, uint32_t one) {
+    constexpr uint32_t lo = LOWER ? 0xFFFFFFFFu : 0u, hi = ~lo;   // lanes 0-63, lanes 64-127 not written
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, {%7, %7, %8, %8}, p;\n\t}" ::"r"(d_tmem),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(one), "r"(lo), "r"(hi)
         : "memory");
 }
 // The same with A in tensor memory: 128 lanes, two bf16 per 32-bit column.
