@@ -264,7 +264,8 @@ m2rnn_status m2rnn_linear_attention_status(m2rnn_stream_t stream);
  * token-first, [B][T][H][N]; weight w and bias b are [H][N] fp32.  Plain rows
  * with one weight are B = H = 1.  mean and rstd are fp32 [B][H][T].  Sums and
  * statistics are fp32 whatever the types.  Any N >= 1 up to 2^28, B·H up to
- * 2^24, T up to 2^30 and B·H·T up to 2^35; pointers are 16-byte aligned. */
+ * 2^24, T up to 2^30 and B·H·T up to 2^35 (the backward's dweight and dbias:
+ * H·ceil(N/16) up to 2^31 - 1); pointers are 16-byte aligned. */
 typedef struct {
     int B, H, T, N;
     int x_fp32;         /* element type of x: 0 = bf16, 1 = fp32 */

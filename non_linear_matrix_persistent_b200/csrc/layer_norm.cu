@@ -449,11 +449,14 @@ __global__ void __launch_bounds__(kThreads, VEC == 8 && CH == 1 ? 2 : 0) m2rnn_n
 
 // dweight, dbias [H][N]: the row blocks' sums, added in ascending (b, block)
 // order by 32 groups of threads and then over the groups.  Launched while the
-// backward kernel runs out, whose end it waits for.
+// backward kernel runs out, whose end it waits for.  A CTA takes 32 columns of a
+// head; heads and column blocks share the grid's first dimension, since the others
+// end at 65535.
 __global__ void __launch_bounds__(1024) m2rnn_norm_dw_kernel(const NormParams p) {
     __shared__ float s[32][32];
-    const int N = p.N, h = blockIdx.y, lane = threadIdx.x % 32, grp = threadIdx.x / 32;
-    const int e = blockIdx.x * 32 + lane;                    // column of [dw | db]
+    const int N = p.N, lane = threadIdx.x % 32, grp = threadIdx.x / 32;
+    const unsigned blocks = norm_dw_blocks(N), h = blockIdx.x / blocks;
+    const int e = (int)(blockIdx.x % blocks) * 32 + lane;    // column of [dw | db]
     const int n = p.B * p.chunks;
     float a = 0.f;
     cudaGridDependencySynchronize();
@@ -642,7 +645,7 @@ int norm_bwd_chunks(int B, int H, int T, int N) { return chunks_for(B, H, T, N, 
 cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s) {
     cudaError_t e = p.y_fp32 ? bwd_x<float>(p, s) : bwd_x<__nv_bfloat16>(p, s);
     if (e != cudaSuccess || !p.part) return e;
-    return launch_dependent(m2rnn_norm_dw_kernel, dim3((2 * p.N + 31) / 32, p.H), 1024, 0, s, p);
+    return launch_dependent(m2rnn_norm_dw_kernel, dim3(norm_dw_blocks(p.N) * p.H), 1024, 0, s, p);
 }
 
 }  // namespace m2rnn

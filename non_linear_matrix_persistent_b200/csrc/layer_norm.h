@@ -28,6 +28,8 @@ struct NormParams {
 
 cudaError_t launch_norm_fwd(const NormParams& p, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s);
+// Column blocks of a head's [dweight | dbias]; those of all heads are at most 2^31 - 1.
+__host__ __device__ inline unsigned norm_dw_blocks(int N) { return (2u * N + 31) / 32; }
 // Row blocks per (b, h) of the backward: fixes the order of the weight gradient's sum.
 int norm_bwd_chunks(int B, int H, int T, int N);
 

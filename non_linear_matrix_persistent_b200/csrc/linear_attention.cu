@@ -177,6 +177,12 @@ static m2rnn_status check_norm(const m2rnn_norm_dims* d) {
     if ((long long)d->B * d->H * d->T > (1LL << 35)) return M2RNN_ERR_UNSUPPORTED_SHAPE;
     return M2RNN_OK;
 }
+// The weight's and bias's gradients are summed by one CTA for 32 of their columns.
+static m2rnn_status check_norm_sums(const m2rnn_norm_dims* d) {
+    const m2rnn_status st = check_norm(d);
+    if (st != M2RNN_OK) return st;
+    return (long long)m2rnn::norm_dw_blocks(d->N) * d->H > 0x7FFFFFFFLL ? M2RNN_ERR_UNSUPPORTED_SHAPE : M2RNN_OK;
+}
 
 static m2rnn::NormParams norm_params(const m2rnn_norm_dims* d) {
     m2rnn::NormParams p;
@@ -199,7 +205,7 @@ m2rnn_status m2rnn_layer_norm_forward(const m2rnn_norm_dims* d, const void* x, c
 }
 
 size_t m2rnn_layer_norm_workspace(const m2rnn_norm_dims* d) {
-    if (check_norm(d) != M2RNN_OK) return kRefused;
+    if (check_norm_sums(d) != M2RNN_OK) return kRefused;
     if ((size_t)d->B * d->H * d->T == 0) return 0;
     return sizeof(float) * 2 * d->N * ((size_t)d->B * d->H * m2rnn::norm_bwd_chunks(d->B, d->H, d->T, d->N));
 }
@@ -207,7 +213,8 @@ size_t m2rnn_layer_norm_workspace(const m2rnn_norm_dims* d) {
 m2rnn_status m2rnn_layer_norm_backward(const m2rnn_norm_dims* d, const void* dy, const void* x, const float* weight,
                                        const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
                                        void* workspace, size_t ws_bytes, m2rnn_stream_t stream) {
-    const m2rnn_status st = check_norm(d);
+    const bool sums = dweight || dbias;
+    const m2rnn_status st = sums ? check_norm_sums(d) : check_norm(d);
     if (st != M2RNN_OK) return st;
     if (any_misaligned({dy, x, weight, mean, rstd, dx, dweight, dbias, workspace})) return M2RNN_ERR_MISALIGNED;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -218,7 +225,6 @@ m2rnn_status m2rnn_layer_norm_backward(const m2rnn_norm_dims* d, const void* dy,
         return M2RNN_OK;
     }
     if (!dy || !x || !rstd || !dx || (!d->rms && !mean)) return M2RNN_ERR_INVALID_ARG;
-    const bool sums = dweight || dbias;
     if (sums && (!workspace || ws_bytes < m2rnn_layer_norm_workspace(d))) return M2RNN_ERR_WORKSPACE;
     m2rnn::NormParams p = norm_params(d);
     p.dy = dy; p.x = x; p.weight = weight; p.mean = const_cast<float*>(mean); p.rstd = const_cast<float*>(rstd);
