@@ -72,7 +72,15 @@ m2rnn::LaParams params(const m2rnn_la_dims* d) {
     return p;
 }
 
-m2rnn_status status_of(cudaError_t e) { return e == cudaSuccess ? M2RNN_OK : M2RNN_ERR_CUDA; }
+// What a failed CUDA call leaves behind for cudaGetLastError(), which the
+// launches ask: taken away where a call fails, and before one begins, so that an
+// error is reported by the call that it belongs to alone.
+void drop_last_error() { (void)cudaGetLastError(); }
+m2rnn_status status_of(cudaError_t e) {
+    if (e == cudaSuccess) return M2RNN_OK;
+    drop_last_error();
+    return M2RNN_ERR_CUDA;
+}
 
 // No tokens: the state (or its gradient) passes through.
 m2rnn_status pass_through(float* out, const float* in, size_t n, cudaStream_t s) {
@@ -102,6 +110,7 @@ m2rnn_status m2rnn_linear_attention_forward(const m2rnn_la_dims* d, const void* 
     const size_t need = m2rnn_linear_attention_workspace(d, 0);
     if (need > 0 && (!workspace || ws_bytes < need)) return M2RNN_ERR_WORKSPACE;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    drop_last_error();
     if (pairs(d) * d->T == 0) return pass_through(ST, S0, pairs(d) * d->K * d->V, s);
     m2rnn::LaParams p = params(d);
     p.k = k; p.v = v; p.q = q; p.f = f; p.S0 = S0; p.y = y; p.ST = ST; p.ckpt = ckpt;
@@ -125,10 +134,11 @@ m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void*
     const size_t need = m2rnn_linear_attention_workspace(d, 1);
     if (need > 0 && (!workspace || ws_bytes < need)) return M2RNN_ERR_WORKSPACE;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    drop_last_error();
     if (pairs(d) * d->T == 0) {
         if (d->f_per_head && d->H > 0) {
-            const cudaError_t e = cudaMemsetAsync(df, 0, sizeof(float) * d->H, s);
-            if (e != cudaSuccess) return M2RNN_ERR_CUDA;
+            const m2rnn_status z = status_of(cudaMemsetAsync(df, 0, sizeof(float) * d->H, s));
+            if (z != M2RNN_OK) return z;
         }
         return pass_through(dS0, dST, pairs(d) * d->K * d->V, s);
     }
@@ -160,8 +170,8 @@ m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void*
 m2rnn_status m2rnn_linear_attention_status(m2rnn_stream_t stream) {
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     unsigned word = 0, bwd = 0;
-    if (m2rnn::la_fwd_tc_status(&word, s) != cudaSuccess || m2rnn::la_bwd_tc_status(&bwd, s) != cudaSuccess)
-        return M2RNN_ERR_CUDA;
+    for (cudaError_t e : {m2rnn::la_fwd_tc_status(&word, s), m2rnn::la_bwd_tc_status(&bwd, s)})
+        if (e != cudaSuccess) return status_of(e);
     return word | bwd ? M2RNN_ERR_DEVICE_TIMEOUT : M2RNN_OK;
 }
 
@@ -199,6 +209,7 @@ m2rnn_status m2rnn_layer_norm_forward(const m2rnn_norm_dims* d, const void* x, c
     if ((size_t)d->B * d->H * d->T == 0) return M2RNN_OK;
     if (!x || !y) return M2RNN_ERR_INVALID_ARG;
     if (any_misaligned({x, weight, bias, y, mean, rstd})) return M2RNN_ERR_MISALIGNED;
+    drop_last_error();
     m2rnn::NormParams p = norm_params(d);
     p.x = x; p.weight = weight; p.bias = bias; p.y = y; p.mean = mean; p.rstd = rstd;
     return status_of(m2rnn::launch_norm_fwd(p, reinterpret_cast<cudaStream_t>(stream)));
@@ -218,10 +229,13 @@ m2rnn_status m2rnn_layer_norm_backward(const m2rnn_norm_dims* d, const void* dy,
     if (st != M2RNN_OK) return st;
     if (any_misaligned({dy, x, weight, mean, rstd, dx, dweight, dbias, workspace})) return M2RNN_ERR_MISALIGNED;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    drop_last_error();
     if ((size_t)d->B * d->H * d->T == 0) {
         for (float* g : {dweight, dbias})
-            if (g && d->H > 0 && cudaMemsetAsync(g, 0, sizeof(float) * d->H * d->N, s) != cudaSuccess)
-                return M2RNN_ERR_CUDA;
+            if (g && d->H > 0) {
+                const m2rnn_status z = status_of(cudaMemsetAsync(g, 0, sizeof(float) * d->H * d->N, s));
+                if (z != M2RNN_OK) return z;
+            }
         return M2RNN_OK;
     }
     if (!dy || !x || !rstd || !dx || (!d->rms && !mean)) return M2RNN_ERR_INVALID_ARG;
