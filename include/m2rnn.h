@@ -251,9 +251,13 @@ m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void*
                                              void* dk, void* dv, void* dq, float* df, float* dS0, void* workspace,
                                              size_t ws_bytes, m2rnn_stream_t stream);
 
-/* Synchronises `stream`, reads and clears the current device's status of the
- * linear-attention kernels (every stream of the device shares it): M2RNN_OK,
- * M2RNN_ERR_DEVICE_TIMEOUT or M2RNN_ERR_CUDA. */
+/* Status of the linear-attention calls made on `stream` since it was last asked
+ * for: synchronises the stream, reads and clears it; M2RNN_OK,
+ * M2RNN_ERR_DEVICE_TIMEOUT or M2RNN_ERR_CUDA.  Returns M2RNN_OK at once where
+ * there is none to read.  Calls that were captured into a graph have one status
+ * for each device, which is part of every stream's answer and told to the first
+ * that asks; streams beyond the first 255 that made calls share it (the library
+ * remembers these streams' ids, and nothing else, from call to call). */
 m2rnn_status m2rnn_linear_attention_status(m2rnn_stream_t stream);
 
 /* ------------------------------------------------------------------------

@@ -204,8 +204,9 @@ def backward(k, v, q, f, W, ckpt, dy, dHT=None, *, ckpt_stride: int = 8, out: Op
 
 def device_status(device=None) -> int:
     """Synchronises the current stream and returns (and clears) the device
-    status of the workspace cached for that stream, and that of the device's
-    linear-attention kernels (which all streams share)."""
+    status of the workspace cached for that stream, and that of the
+    linear-attention calls made on it or captured into graphs on this device.
+    Returns at once where there are neither."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     key = _ws_key(dev)
     ws = _workspaces.get(key)

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     float* gammas = reinterpret_cast<float*>(smem + C::kOffGamma);
-    const uint64_t limit = p.wait_limit_ns;
+    const LaLimit limit = p.limit;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 19; ++i) mbar_init(bar(i), 1);
@@ -946,7 +946,6 @@ cudaError_t launch_la_bwd_tc(const LaParams& q, cudaStream_t s) {
     return p.V <= 64 ? launch<128, 64>(p, m, s) : launch<128, 128>(p, m, s);
 }
 
-// Reads and clears the status word of this file's kernels.
-cudaError_t la_bwd_tc_status(unsigned* word, cudaStream_t s) { return la_read_status(word, s); }
+cudaError_t la_bwd_tc_status(unsigned slot, unsigned* word, cudaStream_t s) { return la_read_status(slot, word, s); }
 
 }  // namespace m2rnn

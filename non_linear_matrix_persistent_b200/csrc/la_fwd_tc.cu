@@ -164,7 +164,7 @@ __device__ __forceinline__ void decay_warp(const LaParams& p, int bh, int n, Chu
     la_load_f(p, bh, chunk_of(0), fx);
     for (int i = 0; i < n; ++i) {
         if (i + 1 < n) la_load_f(p, bh, chunk_of(i + 1), fnext);
-        if (i >= 2 && !la_wait(t_free + (i & 1) * 8, ((i - 2) >> 1) & 1, abort_flag, p.wait_limit_ns)) break;
+        if (i >= 2 && !la_wait(t_free + (i & 1) * 8, ((i - 2) >> 1) & 1, abort_flag, p.limit)) break;
         la_tables(tab + (i & 1), p, fx, p.T - chunk_of(i) * kLaChunk, kLogFloorFwd);
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(b_tab + (i & 1) * 8);
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                    r_raw = bar(20);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const uint64_t limit = p.wait_limit_ns;
+    const LaLimit limit = p.limit;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 21; ++i) mbar_init(bar(i), 1);
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t b_full = bar(0), b_tab = bar(2), t_free = bar(4), b_ds = bar(6), r_k = bar(8), b_drain = bar(10);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const uint64_t limit = p.wait_limit_ns;
+    const LaLimit limit = p.limit;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 11; ++i) mbar_init(bar(i), 1);
         for (uint32_t b : {t_free, t_free + 8, r_k, r_k + 8}) mbar_init(b, kNW);
@@ -859,7 +859,6 @@ cudaError_t launch_la_seg_grads(const LaParams& p, cudaStream_t s) {
     return e != cudaSuccess ? e : launch_scan(p, p.dST, 1, s);
 }
 
-// Reads and clears the status word of this file's kernels.
-cudaError_t la_fwd_tc_status(unsigned* word, cudaStream_t s) { return la_read_status(word, s); }
+cudaError_t la_fwd_tc_status(unsigned slot, unsigned* word, cudaStream_t s) { return la_read_status(slot, word, s); }
 
 }  // namespace m2rnn

@@ -19,9 +19,9 @@ namespace m2rnn {
 
 constexpr int kTileBytes = 128 * 128;   // 128 tokens x 64 bf16
 
-// The kernels' device status: one word per source file, read and cleared by
-// m2rnn_linear_attention_status.  A wait that runs out sets it.
-static __device__ unsigned g_la_status;
+// The kernels' device status: words for each source file, read and cleared by
+// m2rnn_linear_attention_status.  A wait that runs out sets its call's.
+static __device__ unsigned g_la_status[kLaSlots];
 
 // Floor of a gate's base-2 logarithm.  Forward: 2^-256, which every product of
 // decays flushes to 0, so a gate of 0 (or below 2^-126) discards the state.
@@ -296,18 +296,18 @@ __device__ __forceinline__ bool la_try(uint32_t bar, uint32_t parity) {
 // warp computes stays in uniform registers, where the products take their
 // operands from.  (64 attempts in an asm loop and a vote behind them: 128 pairs
 // of 128 x 128 forward 164 against 154 us.)
-__device__ __forceinline__ bool la_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+__device__ __forceinline__ bool la_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, LaLimit limit) {
     uint64_t t0 = 0;
     for (int k = 1;; ++k) {
         if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
         if ((k & 63) == 0) {
             const uint64_t t = globaltimer_ns();
             if (t0 == 0) t0 = t;
-            const bool late = t - t0 > limit_ns;
+            const bool late = t - t0 > limit.ns;
             if (__any_sync(~0u, late || *abort_flag)) {
                 if (late) {
                     *abort_flag = 1;
-                    atomicOr(&g_la_status, 1u);
+                    atomicOr(&g_la_status[limit.slot], 1u);
                 }
                 __syncwarp();
                 return false;
@@ -317,7 +317,7 @@ __device__ __forceinline__ bool la_wait(uint32_t bar, uint32_t parity, volatile 
 }
 // The same for a single lane, which the rest of its warp awaits at a __syncwarp.
 __device__ __forceinline__ bool la_wait_lane(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                             uint64_t limit_ns) {
+                                             LaLimit limit) {
     uint64_t t0 = 0;
     for (int k = 1;; ++k) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -325,32 +325,33 @@ __device__ __forceinline__ bool la_wait_lane(uint32_t bar, uint32_t parity, vola
             if (*abort_flag) return false;
             const uint64_t t = globaltimer_ns();
             if (t0 == 0) t0 = t;
-            if (t - t0 > limit_ns) {
+            if (t - t0 > limit.ns) {
                 *abort_flag = 1;
-                atomicOr(&g_la_status, 1u);
+                atomicOr(&g_la_status[limit.slot], 1u);
                 return false;
             }
         }
     }
 }
 // The same without the abort flag: for copies and products in flight before the CTA exits.
-__device__ __forceinline__ void la_drain(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+__device__ __forceinline__ void la_drain(uint32_t bar, uint32_t parity, LaLimit limit) {
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > limit_ns) {
-            atomicOr(&g_la_status, 1u);
+        if (globaltimer_ns() - t0 > limit.ns) {
+            atomicOr(&g_la_status[limit.slot], 1u);
             return;
         }
 }
 
 // ---------------------------------------------------------------- host
-// Reads and clears this source file's status word.
-static inline cudaError_t la_read_status(unsigned* word, cudaStream_t s) {
+// Reads and clears a status word of this source file.
+static inline cudaError_t la_read_status(unsigned slot, unsigned* word, cudaStream_t s) {
     const unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_la_status, sizeof *word, 0, cudaMemcpyDeviceToHost, s);
+    const size_t at = slot * sizeof zero;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_la_status, sizeof *word, at, cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e == cudaSuccess && *word) {
-        e = cudaMemcpyToSymbolAsync(g_la_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
+        e = cudaMemcpyToSymbolAsync(g_la_status, &zero, sizeof zero, at, cudaMemcpyHostToDevice, s);
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     }
     return e;

@@ -4,6 +4,7 @@
 
 #include <cstring>
 #include <initializer_list>
+#include <mutex>
 
 #include "../../include/m2rnn.h"
 #include "kernels.h"
@@ -67,7 +68,7 @@ m2rnn::LaParams params(const m2rnn_la_dims* d) {
     p.f_per_head = d->f_per_head;
     p.segs = 1;
     p.seg_chunks = (d->T + m2rnn::kLaChunk - 1) / m2rnn::kLaChunk;
-    p.wait_limit_ns = m2rnn::wait_limit_ns();
+    p.limit = {m2rnn::wait_limit_ns(), 0};
     p.fault = m2rnn::injected_fault();
     return p;
 }
@@ -80,6 +81,53 @@ m2rnn_status status_of(cudaError_t e) {
     if (e == cudaSuccess) return M2RNN_OK;
     drop_last_error();
     return M2RNN_ERR_CUDA;
+}
+
+// The status words in use: a stream's is found by its device and its id, which no
+// other stream is given in the life of the process.
+struct StatusWords {
+    std::mutex lock;
+    unsigned count = 1;         // word 0 is the shared one
+    bool shared = false;        // it has been given to a call
+    int device[m2rnn::kLaSlots];
+    unsigned long long id[m2rnn::kLaSlots];
+};
+StatusWords g_words;
+
+// A stream by its device and id.  One that is being captured is not told apart:
+// its calls are those of the stream that will replay them.
+struct StreamKey {
+    int device = 0;
+    unsigned long long id = 0;
+    bool known = false, capturing = false;
+};
+StreamKey key_of(cudaStream_t s) {
+    StreamKey k;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaGetDevice(&k.device) == cudaSuccess && cudaStreamIsCapturing(s, &capture) == cudaSuccess) {
+        k.capturing = capture != cudaStreamCaptureStatusNone;
+        k.known = !k.capturing && cudaStreamGetId(s, &k.id) == cudaSuccess;
+    }
+    if (!k.known) drop_last_error();
+    return k;
+}
+unsigned find_word(const StreamKey& k) {   // (with the lock held) 0: none
+    for (unsigned i = 1; k.known && i < g_words.count; ++i)
+        if (g_words.id[i] == k.id && g_words.device[i] == k.device) return i;
+    return 0;
+}
+// The word of a call that is about to be launched.
+unsigned word_for_call(cudaStream_t s) {
+    const StreamKey k = key_of(s);
+    const std::lock_guard<std::mutex> hold(g_words.lock);
+    if (const unsigned i = find_word(k)) return i;
+    if (k.known && g_words.count < m2rnn::kLaSlots) {
+        g_words.device[g_words.count] = k.device;
+        g_words.id[g_words.count] = k.id;
+        return g_words.count++;
+    }
+    g_words.shared = true;
+    return 0;
 }
 
 // No tokens: the state (or its gradient) passes through.
@@ -115,6 +163,7 @@ m2rnn_status m2rnn_linear_attention_forward(const m2rnn_la_dims* d, const void* 
     m2rnn::LaParams p = params(d);
     p.k = k; p.v = v; p.q = q; p.f = f; p.S0 = S0; p.y = y; p.ST = ST; p.ckpt = ckpt;
     if (!fwd_on_tensor_cores(d)) return status_of(m2rnn::launch_la_rec(p, s));
+    p.limit.slot = word_for_call(s);
     const m2rnn::LaPlan plan = plan_of(d, false);
     p.segs = plan.segs; p.seg_chunks = plan.seg_chunks;
     p.seg_state = static_cast<float*>(workspace);
@@ -154,6 +203,7 @@ m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void*
     if (d->f_per_head) p.df = reinterpret_cast<float*>(ws + group_bytes(d));
     cudaError_t e;
     if (bwd_on_tensor_cores(d)) {
+        p.limit.slot = word_for_call(s);
         const m2rnn::LaPlan plan = plan_of(d, true);
         p.segs = plan.segs; p.seg_chunks = plan.seg_chunks;
         p.seg_state = reinterpret_cast<float*>(ws + group_bytes(d) + df_bytes(d));
@@ -169,10 +219,20 @@ m2rnn_status m2rnn_linear_attention_backward(const m2rnn_la_dims* d, const void*
 
 m2rnn_status m2rnn_linear_attention_status(m2rnn_stream_t stream) {
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    unsigned word = 0, bwd = 0;
-    for (cudaError_t e : {m2rnn::la_fwd_tc_status(&word, s), m2rnn::la_bwd_tc_status(&bwd, s)})
-        if (e != cudaSuccess) return status_of(e);
-    return word | bwd ? M2RNN_ERR_DEVICE_TIMEOUT : M2RNN_OK;
+    const StreamKey k = key_of(s);
+    unsigned slots[2], n = 0, any = 0;
+    {
+        const std::lock_guard<std::mutex> hold(g_words.lock);
+        if (const unsigned i = find_word(k)) slots[n++] = i;
+        if (g_words.shared || k.capturing) slots[n++] = 0;   // (a stream that is being captured cannot be synchronised: an error)
+    }
+    for (unsigned i = 0; i < n; ++i) {
+        unsigned word[2] = {0, 0};
+        for (cudaError_t e : {m2rnn::la_fwd_tc_status(slots[i], &word[0], s), m2rnn::la_bwd_tc_status(slots[i], &word[1], s)})
+            if (e != cudaSuccess) return status_of(e);
+        any |= word[0] | word[1];
+    }
+    return any ? M2RNN_ERR_DEVICE_TIMEOUT : M2RNN_OK;
 }
 
 // ------------------------------------------------------------------ layer norm

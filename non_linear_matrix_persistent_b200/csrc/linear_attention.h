@@ -16,6 +16,15 @@ namespace m2rnn {
 // Tokens between the checkpointed states (and per chunk of the tensor-core kernels).
 constexpr int kLaChunk = 128;
 
+// The limit of a kernel's waits, and the status word that one which runs out sets.
+struct LaLimit {
+    uint64_t ns;
+    unsigned slot;
+};
+// Status words: 0 is shared by captured calls and by streams beyond the others,
+// which have one each.
+constexpr unsigned kLaSlots = 256;
+
 struct LaParams {
     int B, H, G, T, K, V;   // G: head groups of k and q (divides H)
     int bf16;               // k, v, q, dy, y, dk, dv, dq are bf16 (else fp32)
@@ -40,7 +49,7 @@ struct LaParams {
     int segs;               // CTAs along T for each (b, h)
     int seg_chunks;         // chunks of 128 tokens per segment
     float* seg_state;       // [B*H][segs][K][V] (workspace)
-    uint64_t wait_limit_ns;
+    LaLimit limit;
     int fault;              // injected fault (m2rnn_debug_set_fault), 0 = none
 };
 
@@ -81,12 +90,13 @@ cudaError_t launch_la_fwd_tc(const LaParams& p, cudaStream_t s);
 LaPlan la_plan(int B, int H, int T, bool backward);
 // Workspace of a plan: segment states and decays.
 size_t la_seg_bytes(const LaPlan& plan, int B, int H, int K, int V);
-cudaError_t la_fwd_tc_status(unsigned* word, cudaStream_t s);
+// Reads status word `slot` of the file's kernels, and clears it if it is set.
+cudaError_t la_fwd_tc_status(unsigned slot, unsigned* word, cudaStream_t s);
 // Chunked tensor-core backward (bf16).
 cudaError_t launch_la_bwd_tc(const LaParams& p, cudaStream_t s);
 // dL/dS at the segments' ends, into p.seg_state.
 cudaError_t launch_la_seg_grads(const LaParams& p, cudaStream_t s);
-cudaError_t la_bwd_tc_status(unsigned* word, cudaStream_t s);
+cudaError_t la_bwd_tc_status(unsigned slot, unsigned* word, cudaStream_t s);
 // fp32-arithmetic backward on the CUDA cores, both types.
 cudaError_t launch_la_bwd_simt(const LaParams& p, cudaStream_t s);
 // dk, dq [B, G, T, K] (bf16 or fp32) = sums of fp32 per-head partials over each group's heads, ascending.
