@@ -4,11 +4,13 @@ Every (b, h) pair of the recurrence is independent, so ranks can shard it
 two ways with no exchange inside the forward or backward kernels:
 * the batch (data parallel): the one exchange is the gradient of the shared
   per-head W, a sum over the global batch, so each rank's dW (already summed
-  over its own batch rows) is all-reduced (allreduce_dW);
+  over its own batch rows) is all-reduced (allreduce_dW; a norm's dweight and
+  dbias, and the df of gates that are one constant per head, are such sums too);
 * the heads, a whole number of k / q head groups per rank (the topology-aware
   tensor-parallel strategy of the pages, gist.science technical summary §2.2):
   a rank holds its groups' k and q and their heads' v, f, W and state, so
   nothing at all is exchanged (head_shard).
+Linear attention and the readout norm are sharded the same two ways.
 """
 from __future__ import annotations
 
@@ -48,27 +50,32 @@ def max_over_ranks(x: float, device=None) -> float:
     return float(t.item())
 
 
+# Where a problem's tensors hold their heads: the second dimension, except
+_HEADS_FIRST = ("W", "dW", "weight", "bias", "dweight", "dbias")    # one row (or matrix) for each head
+_HEADS_THIRD = ("n", "dn")                                          # a norm's token-first rows and their gradient
+_PER_GROUP = ("k", "q", "dk", "dq")                                 # G groups, not H heads
+
+
 def head_shard(x: dict, rank: int, world: int) -> dict:
     """The part of a problem that rank `rank` of `world` holds when heads are
     sharded: head groups [r·G/N, (r+1)·G/N) of k, q (and dk, dq) and the heads
-    of those groups of every per-head tensor (v, f, W, H0, HT, dY, y, dv, df,
-    dW, dH0, ckpt).  G is k's head count (= H when k and q are per head) and
-    must be a multiple of world.  Returns contiguous slices; None stays None."""
+    of those groups of every per-head tensor: v, f, W, H0, HT, dY, y, dv, df,
+    dW, dH0, ckpt, linear attention's S0, ST, dST, dS0 (f and df may be [H]), a
+    readout norm's x, dx, mean, rstd, its weight, bias, dweight, dbias ([H, N])
+    and, token-first, its rows n and their gradient dn.  G is k's head count
+    (= H when k and q are per head) and must be a multiple of world.  Returns
+    contiguous slices; None stays None."""
     G, H = x["k"].shape[1], x["v"].shape[1]
     if G % world or H % G:
         raise ValueError("%d k/q head groups of %d heads cannot be split over %d ranks" % (G, H, world))
-    g0, g1 = rank * G // world, (rank + 1) * G // world
-    h0, h1 = g0 * (H // G), g1 * (H // G)
-    group_dim1 = ("k", "q", "dk", "dq")
-    head_dim0 = ("W", "dW")
     out = {}
     for n, t in x.items():
         if t is None:
             out[n] = None
-        elif n in group_dim1:
-            out[n] = t[:, g0:g1].contiguous()
-        elif n in head_dim0:
-            out[n] = t[h0:h1].contiguous()
-        else:
-            out[n] = t[:, h0:h1].contiguous()
+            continue
+        heads = G if n in _PER_GROUP else H
+        dim = 0 if n in _HEADS_FIRST or (n in ("f", "df") and t.dim() == 1) else 2 if n in _HEADS_THIRD else 1
+        if n in _HEADS_FIRST and t.dim() < 2 or t.dim() <= dim or t.shape[dim] != heads:
+            raise ValueError("%s has shape %s: %d heads are expected in dimension %d" % (n, tuple(t.shape), heads, dim))
+        out[n] = t.narrow(dim, rank * heads // world, heads // world).contiguous()
     return out
