@@ -416,15 +416,20 @@ def _norm_dims(*fields):
     return _lib.NormDims(*fields)
 
 
-def _norm_shape(x, weight, bias):
-    """(B, H, T, N) of a call, and whether x is a head-first readout."""
+def _norm_shape(x, weight, bias, heads=None):
+    """(B, H, T, N) of a call, and whether x is a head-first readout: by the
+    weight (or bias), or where there is none by `heads`."""
     first = weight if weight is not None else bias
-    heads = first is not None and first.dim() == 2
+    if first is not None:
+        if heads is not None and bool(heads) != (first.dim() == 2):
+            raise ValueError("heads=%s contradicts a weight of %d dimensions" % (bool(heads), first.dim()))
+        heads = first.dim() == 2
     if x.dtype not in _NORM_TYPES:
         raise TypeError("x must be bfloat16 or float32, got %s" % x.dtype)
     if heads:
         if x.dim() != 4:
-            raise ValueError("a norm with one weight per head takes x [B, H, T, N], got %d dimensions" % x.dim())
+            raise ValueError("a norm with one weight per head%s takes x [B, H, T, N], got %d dimensions"
+                             % (" (heads=True)" if first is None else "", x.dim()))
         B, H, T, N = x.shape
     else:
         if x.dim() < 1:
@@ -442,7 +447,7 @@ def _norm_shape(x, weight, bias):
         _same("weight", weight, ps, torch.float32, dev)
     if bias is not None:
         _same("bias", bias, ps, torch.float32, dev)
-    return B, H, T, N, heads
+    return B, H, T, N, bool(heads)
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = False,
@@ -474,13 +479,13 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, rms: bool = False, heads: 
                         dx_dtype: Optional[torch.dtype] = None, out: Optional[dict] = None) -> dict:
     """Gradients of layer_norm: dict dx (x's shape; type dx_dtype, x's by
     default), dweight and dbias (fp32, in weight's shape).  dy has y's shape
-    and type.  With weight=None, `heads` says which form x was in (a readout
-    with dy [B, T, H, N], or plain rows)."""
-    if weight is None and heads and x.dim() != 4:
-        raise ValueError("heads=True takes x [B, H, T, N], got %d dimensions" % x.dim())
-    B, H, T, N, per_head = _norm_shape(x, weight, None)
-    if weight is None and heads:
-        (B, H, T, N), per_head = x.shape, True
+    and type.  With weight=None, `heads` says which form x was in: a readout
+    with dy [B, T, H, N] (True), or plain rows (False, and what None takes
+    unless dy's shape fits both)."""
+    if weight is None and heads is None and x.dim() == 4 and x.shape[1] == x.shape[2] > 1:
+        raise ValueError("without a weight, x of shape %s may be a readout or plain rows: say which with heads=True "
+                         "or heads=False" % (tuple(x.shape),))
+    B, H, T, N, per_head = _norm_shape(x, weight, None, heads)
     dev = x.device
     dt = x.dtype if dx_dtype is None else dx_dtype
     if dy.dtype not in _NORM_TYPES or dt not in _NORM_TYPES or (dt == torch.float32 and x.dtype != torch.float32):
