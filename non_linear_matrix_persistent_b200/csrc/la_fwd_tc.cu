@@ -763,9 +763,13 @@ __global__ void m2rnn_la_seg_scan_kernel(const LaParams p, const float* seg_deca
     }
 }
 
+float* decays_of(const LaParams& p) {   // behind the segment states in the workspace
+    return p.seg_state + (size_t)p.B * p.H * p.segs * p.K * p.V;
+}
+
 template <int KP, int VP>
 struct FwdKernel {
-    static cudaError_t launch(const LaParams& p, const Maps& m, float*, cudaStream_t s) {
+    static cudaError_t launch(const LaParams& p, const Maps& m, cudaStream_t s) {
         auto kern = m2rnn_la_fwd_tc_kernel<KP, VP>;
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<KP, VP>::kSmem);
         if (e != cudaSuccess) return e;
@@ -777,26 +781,23 @@ template <bool REV>
 struct Sum {
     template <int KP, int VP>
     struct Kernel {
-        static cudaError_t launch(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
+        static cudaError_t launch(const LaParams& p, const Maps& m, cudaStream_t s) {
             auto kern = m2rnn_la_sum_tc_kernel<KP, VP, REV>;
             const cudaError_t e =
                 cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SumCfg<KP, VP>::kSmem);
             if (e != cudaSuccess) return e;
-            kern<<<p.B * p.H * p.segs, kFwdThreads, SumCfg<KP, VP>::kSmem, s>>>(p, m, seg_decay);
+            kern<<<p.B * p.H * p.segs, kFwdThreads, SumCfg<KP, VP>::kSmem, s>>>(p, m, decays_of(p));
             return cudaGetLastError();
         }
     };
 };
 template <template <int, int> class Kernel>
-cudaError_t launch_shape(const LaParams& p, const Maps& m, float* seg_decay, cudaStream_t s) {
+cudaError_t launch_shape(const LaParams& p, const Maps& m, cudaStream_t s) {
     if (p.K <= 64)
-        return p.V <= 64 ? Kernel<64, 64>::launch(p, m, seg_decay, s) : Kernel<64, 128>::launch(p, m, seg_decay, s);
-    return p.V <= 64 ? Kernel<128, 64>::launch(p, m, seg_decay, s) : Kernel<128, 128>::launch(p, m, seg_decay, s);
+        return p.V <= 64 ? Kernel<64, 64>::launch(p, m, s) : Kernel<64, 128>::launch(p, m, s);
+    return p.V <= 64 ? Kernel<128, 64>::launch(p, m, s) : Kernel<128, 128>::launch(p, m, s);
 }
 
-float* decays_of(const LaParams& p) {   // behind the segment states in the workspace
-    return p.seg_state + (size_t)p.B * p.H * p.segs * p.K * p.V;
-}
 cudaError_t launch_scan(const LaParams& p, const float* init, int reverse, cudaStream_t s) {
     const size_t n = (size_t)p.B * p.H * p.K * p.V / 4;
     m2rnn_la_seg_scan_kernel<<<(unsigned)((n + 127) / 128), 128, 0, s>>>(p, decays_of(p), init, reverse);
@@ -839,11 +840,11 @@ cudaError_t launch_la_fwd_tc(const LaParams& q, cudaStream_t s) {
         !la_tensor_map(&m.v, p.v, p.V, p.T, (size_t)p.B * p.H) || !la_tensor_map(&m.y, p.y, p.V, p.T, (size_t)p.B * p.H))
         return cudaErrorNotSupported;
     if (p.segs > 1) {
-        cudaError_t e = launch_shape<Sum<false>::Kernel>(p, m, decays_of(p), s);
+        cudaError_t e = launch_shape<Sum<false>::Kernel>(p, m, s);
         if (e != cudaSuccess) return e;
         if ((e = launch_scan(p, p.S0, 0, s)) != cudaSuccess) return e;
     }
-    return launch_shape<FwdKernel>(p, m, nullptr, s);
+    return launch_shape<FwdKernel>(p, m, s);
 }
 
 // The same sums for the gradient: what a segment's tokens add to dL/dS at its
@@ -854,8 +855,7 @@ cudaError_t launch_la_seg_grads(const LaParams& p, cudaStream_t s) {
         return cudaErrorNotSupported;
     m.q = m.k;
     m.y = m.v;
-    const cudaError_t e = launch_shape<Sum<true>::Kernel>(p, m, decays_of(p), s);
-    if (e != cudaSuccess) return e;
+    const cudaError_t e = launch_shape<Sum<true>::Kernel>(p, m, s);
     return e != cudaSuccess ? e : launch_scan(p, p.dST, 1, s);
 }
 

@@ -112,7 +112,7 @@ cudaError_t rec_k(const LaParams& p, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------ backward
-// fp32 arithmetic on the CUDA cores, one CTA per (b, h) pair, walking blocks
+// fp32 on the CUDA cores (the debug mode), one CTA per (b, h) pair, walking blocks
 // of kSub tokens from the last to the first with G = dL/dS at the block's end
 // in shared memory.  Inside a block, with D_ts = f_{s+1}···f_t, a_t = f_1···f_t
 // and b_s = D_{end,s} (all direct products, so a gate of exactly 0 is exact),
@@ -129,7 +129,6 @@ __host__ __device__ inline size_t bwd_smem_floats(int K, int V) {
     return (size_t)2 * K * V + kSub * (4 * K + 2 * V) + 3 * kSub * (kSub + 1) + kSub + 64;
 }
 
-template <class IO, class OKQ>
 __global__ void __launch_bounds__(kBwdThreads) m2rnn_la_bwd_simt_kernel(const LaParams p) {
     extern __shared__ float sm[];
     const int K = p.K, V = p.V, tid = threadIdx.x, bh = blockIdx.x;
@@ -147,6 +146,9 @@ __global__ void __launch_bounds__(kBwdThreads) m2rnn_la_bwd_simt_kernel(const La
     float* f = D + kSub * (kSub + 1);
     float* red = f + kSub;
     const int ld = kSub + 1;
+    const float *k_in = static_cast<const float*>(p.k), *v_in = static_cast<const float*>(p.v),
+                *q_in = static_cast<const float*>(p.q), *dy_in = static_cast<const float*>(p.dy);
+    float *dk_out = static_cast<float*>(p.dk), *dq_out = static_cast<float*>(p.dq), *dv_out = static_cast<float*>(p.dv);
     const size_t qk0 = (size_t)la_qk_pair(p, bh) * p.T * K, vy0 = (size_t)bh * p.T * V, kq_out = (size_t)bh * p.T * K;
     const int nck = (p.T + kLaChunk - 1) / kLaChunk;
     for (int i = tid; i < K * V; i += kBwdThreads) G[i] = p.dST ? p.dST[(size_t)bh * K * V + i] : 0.f;
@@ -160,17 +162,16 @@ __global__ void __launch_bounds__(kBwdThreads) m2rnn_la_bwd_simt_kernel(const La
             float s = p.ckpt[((size_t)bh * nck + c) * K * V + ((colv >> 2) * K + row) * 4 + (colv & 3)];
             for (int t = c * kLaChunk; t < t0; ++t)
                 s = fmaf(la_gate(p, la_f_input(p, bh, t)), s,
-                         la_to_f32(static_cast<const IO*>(p.k)[qk0 + (size_t)t * K + row]) *
-                             la_to_f32(static_cast<const IO*>(p.v)[vy0 + (size_t)t * V + colv]));
+                         k_in[qk0 + (size_t)t * K + row] * v_in[vy0 + (size_t)t * V + colv]);
             S[i] = s;
         }
         for (int i = tid; i < n * K; i += kBwdThreads) {
-            k[i] = la_to_f32(static_cast<const IO*>(p.k)[qk0 + (size_t)t0 * K + i]);
-            q[i] = la_to_f32(static_cast<const IO*>(p.q)[qk0 + (size_t)t0 * K + i]);
+            k[i] = k_in[qk0 + (size_t)t0 * K + i];
+            q[i] = q_in[qk0 + (size_t)t0 * K + i];
         }
         for (int i = tid; i < n * V; i += kBwdThreads) {
-            v[i] = la_to_f32(static_cast<const IO*>(p.v)[vy0 + (size_t)t0 * V + i]);
-            dy[i] = la_to_f32(static_cast<const IO*>(p.dy)[vy0 + (size_t)t0 * V + i]);
+            v[i] = v_in[vy0 + (size_t)t0 * V + i];
+            dy[i] = dy_in[vy0 + (size_t)t0 * V + i];
         }
         if (tid < n) f[tid] = la_gate(p, la_f_input(p, bh, t0 + tid));
         __syncthreads();
@@ -206,8 +207,8 @@ __global__ void __launch_bounds__(kBwdThreads) m2rnn_la_bwd_simt_kernel(const La
             float dq = Sdy[e] * (D[t * ld] * f[0]), dk = Gv[e] * D[(n - 1) * ld + t];
             for (int s = 0; s <= t; ++s) dq = fmaf(D[t * ld + s] * YV[t * ld + s], k[s * K + i], dq);
             for (int s = t; s < n; ++s) dk = fmaf(D[s * ld + t] * YV[s * ld + t], q[s * K + i], dk);
-            static_cast<OKQ*>(p.dq)[kq_out + (size_t)t0 * K + e] = la_from_f32<OKQ>(dq);
-            static_cast<OKQ*>(p.dk)[kq_out + (size_t)t0 * K + e] = la_from_f32<OKQ>(dk);
+            dq_out[kq_out + (size_t)t0 * K + e] = dq;
+            dk_out[kq_out + (size_t)t0 * K + e] = dk;
         }
         for (int e = tid; e < n * V; e += kBwdThreads) {
             const int s = e / V, j = e % V;
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kBwdThreads) m2rnn_la_bwd_simt_kernel(const La
             for (int i = 0; i < K; ++i) a = fmaf(G[i * V + j], k[s * K + i], a);
             a *= D[(n - 1) * ld + s];
             for (int t = s; t < n; ++t) a = fmaf(D[t * ld + s] * QK[t * ld + s], dy[t * V + j], a);
-            static_cast<IO*>(p.dv)[vy0 + (size_t)t0 * V + e] = la_from_f32<IO>(a);
+            dv_out[vy0 + (size_t)t0 * V + e] = a;
         }
         if (tid < n) {
             const int u = tid;
@@ -252,16 +253,6 @@ __global__ void __launch_bounds__(kBwdThreads) m2rnn_la_bwd_simt_kernel(const La
     }
     __syncthreads();
     for (int i = tid; i < K * V; i += kBwdThreads) p.dS0[(size_t)bh * K * V + i] = G[i];
-}
-
-template <class IO, class OKQ>
-cudaError_t bwd_simt(const LaParams& p, cudaStream_t s) {
-    const size_t bytes = sizeof(float) * bwd_smem_floats(p.K, p.V);
-    cudaError_t e = cudaFuncSetAttribute(m2rnn_la_bwd_simt_kernel<IO, OKQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)bytes);
-    if (e != cudaSuccess) return e;
-    m2rnn_la_bwd_simt_kernel<IO, OKQ><<<p.B * p.H, kBwdThreads, bytes, s>>>(p);
-    return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ sums
@@ -314,8 +305,12 @@ cudaError_t launch_la_rec(const LaParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_la_bwd_simt(const LaParams& p, cudaStream_t s) {
-    if (!p.bf16) return bwd_simt<float, float>(p, s);
-    return p.dkq_fp32 ? bwd_simt<__nv_bfloat16, float>(p, s) : bwd_simt<__nv_bfloat16, __nv_bfloat16>(p, s);
+    const size_t bytes = sizeof(float) * bwd_smem_floats(p.K, p.V);
+    const cudaError_t e =
+        cudaFuncSetAttribute(m2rnn_la_bwd_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    m2rnn_la_bwd_simt_kernel<<<p.B * p.H, kBwdThreads, bytes, s>>>(p);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_la_group_sum(const LaParams& p, const float* dk_part, const float* dq_part, void* dk, void* dq,

@@ -272,20 +272,6 @@ __device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk
 __device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 // ---------------------------------------------------------------- waits
-// One attempt, suspended by the hardware until the phase completes or about 0.1
-// ms have passed: warps that poll instead take issue slots from those at work
-// and from the one that feeds the tensor core.
-__device__ __forceinline__ bool la_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(100000u)
-        : "memory");
-    return ok != 0;
-}
 // Bounded mbarrier wait of a whole warp: false when it runs longer than the
 // limit or another thread of the CTA has given up.  The outcome is the warp's:
 // what follows it (tensor-memory accesses, shuffles, the way out) takes all 32

@@ -32,16 +32,6 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <int VEC>
-__device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
-        v[0] = bf16lo_to_f32(w.x); v[1] = bf16hi_to_f32(w.x); v[2] = bf16lo_to_f32(w.y); v[3] = bf16hi_to_f32(w.y);
-        v[4] = bf16lo_to_f32(w.z); v[5] = bf16hi_to_f32(w.z); v[6] = bf16lo_to_f32(w.w); v[7] = bf16hi_to_f32(w.w);
-    } else {
-        v[0] = __bfloat162float(*p);
-    }
-}
-template <int VEC>
 __device__ __forceinline__ void load(const float* p, float (&v)[VEC]) {
     if constexpr (VEC == 8) {
         const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);

@@ -97,7 +97,7 @@ cudaError_t launch_la_bwd_tc(const LaParams& p, cudaStream_t s);
 // dL/dS at the segments' ends, into p.seg_state.
 cudaError_t launch_la_seg_grads(const LaParams& p, cudaStream_t s);
 cudaError_t la_bwd_tc_status(unsigned slot, unsigned* word, cudaStream_t s);
-// fp32-arithmetic backward on the CUDA cores, both types.
+// fp32 backward on the CUDA cores.
 cudaError_t launch_la_bwd_simt(const LaParams& p, cudaStream_t s);
 // dk, dq [B, G, T, K] (bf16 or fp32) = sums of fp32 per-head partials over each group's heads, ascending.
 cudaError_t launch_la_group_sum(const LaParams& p, const float* dk_part, const float* dq_part, void* dk, void* dq,
