@@ -809,15 +809,18 @@ cudaError_t launch_scan(const LaParams& p, const float* init, int reverse, cudaS
 // Segments while there are SMs for them, if the chunks that a walk is spared
 // pay for the sums that run before it, a launch and a pass over k and v (q and
 // dy).  Those cost more the more CTAs share the memory.  Measured, us, one
-// walk against segments of T/128 chunks:
-//   forward   1 pair, 64 x 64:     4 chunks 14.4 / 14.8,  5  16.5 / 14.6
-//            24 pairs, 64 x 64:    5 chunks 16.9 / 16.9,  6  19.3 / 17.6
-//            37 pairs, 128 x 128:  6 chunks 32.1 / 35.6,  8  40.9 / 38.6
-//            48 pairs, 128 x 128: 10 chunks 50.3 / 51.4, 12  58.6 / 56.8
-//            74 pairs, 128 x 128: 24 chunks 110 / 111,   32  143 / 136
-//   backward  1 pair, 64 x 64:     2 chunks 16.9 / 18.3,  3  23.7 / 18.6
-//            48 pairs, 64 x 64:    3 chunks 23.9 / 22.9,  6  43.4 / 33.0
-//            74 pairs, 64 x 64:    4 chunks 30.8 / 33.3,  6  43.8 / 42.7
+// walk against segments of T/128 chunks (64 x 128 and 128 x 64 lie between the
+// two shapes and turn at the same lengths):
+//   forward            64 x 64                                128 x 128
+//    1 pair    4 chunks 15.3 / 15.2,  5  17.9 / 15.3     4  26.8 / 26.1,   5  31.6 / 25.9
+//   24 pairs   5        17.9 / 17.2,  6  20.5 / 18.0     5  31.9 / 29.8,   6  36.8 / 30.8
+//   37 pairs   6        20.8 / 20.6,  8  26.3 / 22.1     6  37.5 / 37.5,   8  48.4 / 41.2
+//   48 pairs  10        32.1 / 32.2, 12  37.5 / 32.5    10  58.5 / 57.5,  12  68.6 / 60.1
+//   74 pairs  24        70.7 / 77.1                     16  90.0 / 96.4,  24   130 / 125
+//   backward
+//    1 pair    2 chunks 19.5 / 19.8,  3  26.8 / 19.9     2  37.6 / 35.6,   3  52.9 / 35.6
+//   48 pairs   3        26.9 / 24.7,  6  51.2 / 35.9     2  38.4 / 40.3,   3  55.2 / 44.8
+//   74 pairs   4        36.1 / 36.4,  6  52.4 / 48.7     4  73.9 / 75.4,   6   107 / 97
 LaPlan la_plan(int B, int H, int T, bool backward) {
     const int chunks = (T + kLaChunk - 1) / kLaChunk;
     const long long pairs = (long long)B * H;

@@ -152,7 +152,7 @@ __device__ __forceinline__ float inv_sqrt(float x) {
 
 // VEC values in pairs: additions, products and multiply-adds of two values take
 // one instruction.  (One value at a time, issue slots and not HBM bounded rows
-// of 64: forward 17.0 against 13.5 us, 134 MB moved.)
+// of 64: forward 17.0 against 13.5 us, 67 MB moved.)
 template <int VEC, class F>
 __device__ __forceinline__ void by_pairs(F&& f) {   // f(i, i + 1)
 #pragma unroll

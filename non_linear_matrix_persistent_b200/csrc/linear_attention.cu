@@ -46,9 +46,14 @@ size_t group_bytes(const m2rnn_la_dims* d) {
 size_t df_bytes(const m2rnn_la_dims* d) { return d->f_per_head ? round256(sizeof(float) * pairs(d) * d->T) : 0; }
 
 // Prompts run on the tensor cores, whose chunk costs the same at any fill;
-// short ones run token by token, which costs a step each.  Measured, 16 pairs
-// of 64 x 64: 5.9 (tokens) against 7.2 us at T = 8, 7.3 against 6.9 at 12; 128
-// pairs of 128 x 128: 11.1 against 13.8 and 14.4 against 13.7.
+// short ones run token by token, which costs a step each.  Measured, us, tokens
+// against chunks at T = 8, 11, 12 and 16:
+//    16 pairs of 16 x 16      5.3 / 6.8,  6.8 / 6.8,  7.3 / 6.8,  9.2 / 6.8
+//    16 pairs of 64 x 64      5.2 / 7.0,  6.5 / 7.0,  6.8 / 7.0,  8.6 / 6.9
+//   128 pairs of 64 x 64      6.2 / 8.1,  7.8 / 8.0,  8.2 / 8.0, 10.3 / 8.1
+//   128 pairs of 128 x 128   10.4 / 12.5, 13.1 / 12.6, 13.8 / 12.6, 17.2 / 12.4
+// (More pairs than SMs would turn later, up to T = 20: 512 pairs of 64 x 64 22.0
+// against 26.5 at 16.)
 bool fwd_on_tensor_cores(const m2rnn_la_dims* d) { return d->mode == M2RNN_MODE_BF16_TC && d->T > 11; }
 
 bool bwd_on_tensor_cores(const m2rnn_la_dims* d) { return d->mode == M2RNN_MODE_BF16_TC; }
