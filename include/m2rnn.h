@@ -195,9 +195,13 @@ m2rnn_status m2rnn_backward_noalloc(const m2rnn_dims* d,
 
 /* ------------------------------------------------------------------------
  * Linear attention with a decay for each head: the same state, gates, head
- * groups and layouts without the transition S·W and the tanh,
+ * groups and layouts without the transition S·W, the tanh and the factor
+ * (1 - f_t) in front of the input,
  *   S_t = f_t S_{t-1} + k_t v_tᵀ,    y_t = S_tᵀ q_t,
- * for the linear layers that a hybrid stack places between M²RNN layers.
+ * for the linear layers that a hybrid stack places between M²RNN layers.  (With
+ * the factor: (1 - f_t) v_t takes the place of v_t; with dv_t the gradient of
+ * that, v_t's is (1 - f_t) dv_t, and f_t's has -v_t·dv_t beside df_t; a logit's
+ * has f_t (1 - f_t) times that.)
  *
  * Tensors are dense and head-first as above: k, q, dk, dq [B][G][T][K];
  * v, y, dy, dv [B][H][T][V]; S0, ST, dST, dS0 [B][H][K][V] fp32; f, df fp32
@@ -222,7 +226,8 @@ m2rnn_status m2rnn_backward_noalloc(const m2rnn_dims* d,
  * ones before it too: the chunk's masked products multiply it by 0.  Tokens
  * that are to be ignored hold finite values.
  *
- * Errors, ownership, ordering and alignment are as above; ws may be NULL when
+ * Errors, ownership, ordering and alignment are as above; outputs overlap neither
+ * inputs nor one another, except where a call says so; ws may be NULL when
  * the workspace size is 0.  Tensors with no elements may be NULL.  The
  * workspace needs no initialisation.  A wait inside a kernel that runs out is
  * reported by m2rnn_linear_attention_status. */
@@ -289,7 +294,8 @@ size_t m2rnn_layer_norm_workspace(const m2rnn_norm_dims* d);
 /* dx from dy and the forward's x, mean (ignored with rms) and rstd.  dweight
  * and dbias, [H][N] fp32, are the sums over batch and time in a fixed order;
  * both NULL leaves them out (and needs no workspace).  dx may be the buffer of
- * x when their types are the same. */
+ * x when their types are the same; no other output overlaps an input, here or in
+ * the forward. */
 m2rnn_status m2rnn_layer_norm_backward(const m2rnn_norm_dims* d, const void* dy, const void* x, const float* weight,
                                        const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
                                        void* workspace, size_t ws_bytes, m2rnn_stream_t stream);

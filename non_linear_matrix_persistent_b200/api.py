@@ -340,6 +340,8 @@ def linear_attention(k, v, q, f, S0=None, *, want_ST: bool = True, want_ckpt: bo
                      f_is_logit: bool = False, out: Optional[dict] = None):
     """Linear attention with a decay for each head, over a whole sequence:
     S_t = f_t S_{t-1} + k_t v_tᵀ, y_t = S_tᵀ q_t.  Returns (y, ST or None, ckpt or None).
+    (Unlike the M²RNN scan's, the input has no factor 1 - f_t: where it is wanted,
+    v is scaled by it, and the sum of -v·dv over the last dimension added to df.)
 
     k, q [B, G, T, K] and v [B, H, T, V] (bf16, or fp32 for the debug mode),
     f [B, H, T] fp32 in [0, 1] (or logits, with f_is_logit) or [H], one
@@ -347,7 +349,7 @@ def linear_attention(k, v, q, f, S0=None, *, want_ST: bool = True, want_ckpt: bo
     inputs' type, ST [B, H, K, V] is fp32.  ckpt [B, H, ceil(T/128), V/4, K, 4]
     holds the states that linear_attention_backward starts from (element (i, j)
     of a state at [j // 4, i, j % 4]).  `out` may hold buffers for y, ST and
-    ckpt; ST may be S0's.  Padding holds finite values: a NaN in a bf16 token
+    ckpt; ST may be S0's, and no other is an input's.  Padding holds finite values: a NaN in a bf16 token
     may reach the earlier tokens of its 128-token chunk too."""
     (d, need, _), B, H, T, K, V = _la_inputs(k, v, q, f, S0, f_is_logit, True)
     y = _out(out, "y", k, (B, H, T, V), k.dtype)
@@ -460,7 +462,8 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = Fals
     [B, T, H, N]: the rows of the output projection.  weight and bias [N] or
     None: plain rows, y has x's shape.  x is bf16 or fp32; y has type out_dtype
     (x's by default).  mean and rstd (fp32, x's leading shape) feed
-    layer_norm_backward.  `out` may hold buffers for y, mean and rstd."""
+    layer_norm_backward.  `out` may hold buffers for y, mean and rstd (none of
+    them x's)."""
     B, H, T, N, heads = _norm_shape(x, weight, bias)
     yt = x.dtype if out_dtype is None else out_dtype
     if yt not in _NORM_TYPES:

@@ -3,8 +3,9 @@
 //
 //   S_t = f_t S_{t-1} + k_t v_tᵀ,   y_t = S_tᵀ q_t        (S_t is K x V)
 //
-// the M²RNN recurrence without the transition S·W and the tanh, and therefore
-// associative: a chunk of tokens can be evaluated with matrix products.
+// the M²RNN recurrence without the transition S·W, the tanh and the factor (1 - f_t)
+// in front of the input, and therefore associative: a chunk of tokens can be
+// evaluated with matrix products.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
