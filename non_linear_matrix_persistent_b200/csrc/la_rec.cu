@@ -146,9 +146,6 @@ __global__ void __launch_bounds__(kBwdThreads) m2rnn_la_bwd_simt_kernel(const La
     float* f = D + kSub * (kSub + 1);
     float* red = f + kSub;
     const int ld = kSub + 1;
-    const float *k_in = static_cast<const float*>(p.k), *v_in = static_cast<const float*>(p.v),
-                *q_in = static_cast<const float*>(p.q), *dy_in = static_cast<const float*>(p.dy);
-    float *dk_out = static_cast<float*>(p.dk), *dq_out = static_cast<float*>(p.dq), *dv_out = static_cast<float*>(p.dv);
     const size_t qk0 = (size_t)la_qk_pair(p, bh) * p.T * K, vy0 = (size_t)bh * p.T * V, kq_out = (size_t)bh * p.T * K;
     const int nck = (p.T + kLaChunk - 1) / kLaChunk;
     for (int i = tid; i < K * V; i += kBwdThreads) G[i] = p.dST ? p.dST[(size_t)bh * K * V + i] : 0.f;
@@ -162,16 +159,17 @@ __global__ void __launch_bounds__(kBwdThreads) m2rnn_la_bwd_simt_kernel(const La
             float s = p.ckpt[((size_t)bh * nck + c) * K * V + ((colv >> 2) * K + row) * 4 + (colv & 3)];
             for (int t = c * kLaChunk; t < t0; ++t)
                 s = fmaf(la_gate(p, la_f_input(p, bh, t)), s,
-                         k_in[qk0 + (size_t)t * K + row] * v_in[vy0 + (size_t)t * V + colv]);
+                         static_cast<const float*>(p.k)[qk0 + (size_t)t * K + row] *
+                             static_cast<const float*>(p.v)[vy0 + (size_t)t * V + colv]);
             S[i] = s;
         }
         for (int i = tid; i < n * K; i += kBwdThreads) {
-            k[i] = k_in[qk0 + (size_t)t0 * K + i];
-            q[i] = q_in[qk0 + (size_t)t0 * K + i];
+            k[i] = static_cast<const float*>(p.k)[qk0 + (size_t)t0 * K + i];
+            q[i] = static_cast<const float*>(p.q)[qk0 + (size_t)t0 * K + i];
         }
         for (int i = tid; i < n * V; i += kBwdThreads) {
-            v[i] = v_in[vy0 + (size_t)t0 * V + i];
-            dy[i] = dy_in[vy0 + (size_t)t0 * V + i];
+            v[i] = static_cast<const float*>(p.v)[vy0 + (size_t)t0 * V + i];
+            dy[i] = static_cast<const float*>(p.dy)[vy0 + (size_t)t0 * V + i];
         }
         if (tid < n) f[tid] = la_gate(p, la_f_input(p, bh, t0 + tid));
         __syncthreads();
@@ -207,8 +205,8 @@ __global__ void __launch_bounds__(kBwdThreads) m2rnn_la_bwd_simt_kernel(const La
             float dq = Sdy[e] * (D[t * ld] * f[0]), dk = Gv[e] * D[(n - 1) * ld + t];
             for (int s = 0; s <= t; ++s) dq = fmaf(D[t * ld + s] * YV[t * ld + s], k[s * K + i], dq);
             for (int s = t; s < n; ++s) dk = fmaf(D[s * ld + t] * YV[s * ld + t], q[s * K + i], dk);
-            dq_out[kq_out + (size_t)t0 * K + e] = dq;
-            dk_out[kq_out + (size_t)t0 * K + e] = dk;
+            static_cast<float*>(p.dq)[kq_out + (size_t)t0 * K + e] = dq;
+            static_cast<float*>(p.dk)[kq_out + (size_t)t0 * K + e] = dk;
         }
         for (int e = tid; e < n * V; e += kBwdThreads) {
             const int s = e / V, j = e % V;
@@ -216,7 +214,7 @@ __global__ void __launch_bounds__(kBwdThreads) m2rnn_la_bwd_simt_kernel(const La
             for (int i = 0; i < K; ++i) a = fmaf(G[i * V + j], k[s * K + i], a);
             a *= D[(n - 1) * ld + s];
             for (int t = s; t < n; ++t) a = fmaf(D[t * ld + s] * QK[t * ld + s], dy[t * V + j], a);
-            dv_out[vy0 + (size_t)t0 * V + e] = a;
+            static_cast<float*>(p.dv)[vy0 + (size_t)t0 * V + e] = a;
         }
         if (tid < n) {
             const int u = tid;
