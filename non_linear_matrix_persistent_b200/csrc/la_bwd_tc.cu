@@ -97,7 +97,7 @@ struct BCfg {
     // the low term of dP'ᵀ of the other shapes: over state terms that are no longer
     // read (those of S, or where G's are done too and those of a q come early, of G),
     // or the v tile.  Where it shares its place with a q, a q waits for the outputs'
-    // products (64 x 64 so: 152 us for the training shape below, not 139).
+    // products (64 x 64 so: 152 us where it takes 139, see above).
     static constexpr bool kEarlyAq = KP == 64;
     static constexpr int kOffLo = kRoomy ? kOffX + (kEarlyAq ? kG0 : 0) : 2 * kQ;
     static_assert(!kEarlyAq || kLateLo || (kG0 >= 3 * kQ && kX - kG0 >= 2 * kTileBytes), "a q beside the low term of dP'");
@@ -348,6 +348,8 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
             }
             auto sum_for_G = [&]() -> bool {
                 if (!la_wait(r_aq, ph, abort_flag, limit)) return false;
+                // 64 x 128: its columns hold dk's operand until the products with that are done
+                if (C::kDG == C::kDP && KP == 64 && !la_wait(b_out, ph, abort_flag, limit)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int x = 2; x >= 0; --x) {      // the terms of a q
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(BCfg<KP, VP>::kThreads, 1)
                     tma_tile(base + 2 * C::kQ + x * kTileBytes, &maps.v, x * 64, t, bh, full);
             };
             // the next chunk's checkpoint into L2 (its tiles too, or two chunks
-            // ahead, was slower: 7B-MoE shape 515 against 475 us)
+            // ahead, was 8% slower for 128 pairs of 128 x 128 over 4096 tokens)
             auto prefetch = [&](int i) {
                 if (i < n && !p.fault)
                     bulk_prefetch(p.ckpt + ((size_t)bh * nchunks + chunk_of(i)) * p.K * p.V, p.K * p.V * 4);
